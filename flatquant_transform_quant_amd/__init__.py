@@ -16,11 +16,15 @@ Output storage in torch:
   * ``int8`` / ``e4m3`` / ``e5m2`` modes (per-token 8-bit codes): out is ``torch.int8`` /
     ``torch.float8_e4m3fn`` / ``torch.float8_e5m2`` (or ``torch.uint8``) [K, M, N],
     quantScale ``torch.float32`` [K].
+
+A paged key-value cache in the same formats is a :class:`KVCache` (``empty_kv_cache`` allocates
+one); ``kv_write``, ``kv_read``, ``attn_decode`` and ``attn_prefill`` are the calls on it.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfq.so")
@@ -92,13 +96,23 @@ def _load():
     L.fq_int4_gemm.restype = ctypes.c_int32
     L.fq_dequant.argtypes = [P, P, P, vp]
     L.fq_dequant.restype = ctypes.c_int32
+    # (descriptors of the calls below are passed by address, see _Desc)
+    dbl, u64 = ctypes.c_double, ctypes.c_uint64
+    L.fq_kv_write.argtypes = [vp, vp, vp, dbl, dbl, vp, vp, vp, vp, vp]
+    L.fq_kv_read.argtypes = [vp] * 9
+    L.fq_attn_decode_get_workspace_size.argtypes = [vp, vp, vp, ctypes.POINTER(u64)]
+    L.fq_attn_decode.argtypes = [vp] * 7 + [dbl, vp, vp, vp, u64, vp]
+    L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp]
+    for f in (L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode, L.fq_attn_prefill):
+        f.restype = ctypes.c_int32
     return L
 
 
 lib = _load()
 EXPORTS = ("fq_get_workspace_size", "fq_run", "fq_executor_destroy", "fq_executor_set_repeatable",
            "fq_executor_set_kernel", "fq_executor_kernel", "fq_status_string", "fq_last_error", "fq_dequant",
-           "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc")
+           "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc", "fq_kv_write", "fq_kv_read",
+           "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill")
 NO_ALLOC_SCRATCH_BYTES = 64 << 20  # FQ_NO_ALLOC_SCRATCH_BYTES of include/fq.h
 
 
@@ -384,4 +398,230 @@ def int4_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=No
                       (stream if stream is not None else torch.cuda.current_stream(a_codes.device)).cuda_stream)
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_int4_gemm")
+    return out
+
+
+# ---- paged key-value cache and attention ---------------------------------------------------
+
+_DESC = struct.Struct("=Qii4q4q")  # the layout of fq_tensor
+_ZEROS = (0, 0, 0, 0)
+_codes = {}  # torch dtype -> fq_dtype, filled on first use
+
+
+def _dtype_code(dtype) -> int:
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float16: DT_FLOAT16, torch.bfloat16: DT_BFLOAT16, torch.float32: DT_FLOAT32,
+                       torch.int32: DT_INT32, torch.int8: DT_INT8, torch.float8_e4m3fn: DT_FLOAT8_E4M3FN})
+    return _codes.get(dtype, -1)  # -1 is rejected by the library's checks
+
+
+class _Desc:
+    """An fq_tensor descriptor as bytes; passed by address (cheaper to build than a Structure)."""
+    __slots__ = ("raw", "ptr")
+
+    def __init__(self, data_ptr, dtype, shape, strides):
+        n = len(shape)
+        self.raw = ctypes.create_string_buffer(
+            _DESC.pack(data_ptr, dtype, n, *shape, *_ZEROS[n:], *strides, *_ZEROS[n:]) if n <= 4
+            else _DESC.pack(data_ptr, dtype, n, *_ZEROS, *_ZEROS), _DESC.size)
+        self.ptr = ctypes.addressof(self.raw)
+
+
+def _desc(t, dtype=None) -> _Desc:
+    return _Desc(t.data_ptr(), _dtype_code(t.dtype) if dtype is None else dtype, t.shape, t.stride())
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+
+class _on_device:
+    """The launch goes to the tensors' device, whichever is current."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        torch = _torch()
+        self.guard = (torch.cuda.device(device) if device.type == "cuda" and device.index != torch.cuda.current_device()
+                      else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _stream(stream, device):
+    return stream if stream is not None else _torch().cuda.current_stream(device)
+
+
+def _record(stream, *tensors):
+    """Tensors allocated here on the current stream and used on the caller's `stream`."""
+    for t in tensors:
+        if stream is not None and t is not None and stream != _torch().cuda.current_stream(t.device):
+            t.record_stream(stream)
+
+
+KV_MODES = ("f16", "bf16", "int8", "e4m3", "int4", "fp4")
+
+
+class KVCache:
+    """The two sides of a paged key-value cache and their descriptors (include/fq.h).
+
+    Storage, P tokens a page: ``f16`` / ``bf16`` codes of that dtype [pages, Hkv, P, D], no
+    scales; ``int8`` torch.int8 and ``e4m3`` torch.float8_e4m3fn (or uint8) [pages, Hkv, P, D],
+    ``int4`` uint8 [pages, Hkv, P, D/2], each with float32 scales [pages, Hkv, P]; ``fp4`` uint8
+    [pages, Hkv, P, D/2] with uint8 e8m0 scales [pages, Hkv, P, 2 * ceilDiv(D, 64)].  The
+    first dimension may be strided (both sides in one allocation)."""
+
+    def __init__(self, mode: str, k, v, k_scale=None, v_scale=None):
+        if mode not in KV_MODES:
+            raise ValueError(f"unknown cache mode {mode!r}")
+        torch = _torch()
+        _same_device(k, v, k_scale, v_scale)
+        self.mode, self.k, self.v, self.k_scale, self.v_scale = mode, k, v, k_scale, v_scale
+        self.device = k.device
+        codes = {"f16": (torch.float16,), "bf16": (torch.bfloat16,), "int8": (torch.int8, torch.uint8),
+                 "e4m3": (torch.float8_e4m3fn, torch.uint8)}.get(mode, (torch.uint8,))
+        scales = None if mode in ("f16", "bf16") else torch.uint8 if mode == "fp4" else torch.float32
+        dt = {"f16": DT_FLOAT16, "bf16": DT_BFLOAT16, "int8": DT_INT8, "e4m3": DT_FLOAT8_E4M3FN, "int4": DT_INT4,
+              "fp4": DT_FLOAT4_E2M1}[mode]
+        sdt = DT_FLOAT8_E8M0 if mode == "fp4" else DT_FLOAT32
+
+        def side(c, s):
+            if c.dim() != 4 or c.dtype not in codes or (s is None) != (scales is None) or (s is not None and s.dtype != scales):
+                raise ValueError(f"storage of a {mode} cache: see KVCache")
+            shape, st = list(c.shape), list(c.stride())
+            if mode in ("int4", "fp4"):  # two codes a byte: sizes and strides in codes
+                shape[3] *= 2
+                st = [2 * n for n in st[:3]] + [1 if st[3] == 1 else 2 * st[3]]
+            return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _desc(s, sdt)
+
+        (self._kc, self._ks), (self._vc, self._vs) = side(k, k_scale), side(v, v_scale)
+        self.pages, self.heads, self.page_size = k.shape[:3]
+        self.head_dim = k.shape[3] * (2 if mode in ("int4", "fp4") else 1)
+
+    def _ptrs(self):
+        return (self._kc.ptr, self._ks.ptr if self._ks else None, self._vc.ptr, self._vs.ptr if self._vs else None)
+
+
+def empty_kv_cache(pages: int, heads: int, page_size: int, head_dim: int, mode: str, device="cuda") -> KVCache:
+    """A cache with uninitialised contents."""
+    torch = _torch()
+    if mode not in KV_MODES:
+        raise ValueError(f"unknown cache mode {mode!r}")
+    shape = (pages, heads, page_size)
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}.get(mode, torch.uint8)
+    codes = lambda: torch.empty(shape + (head_dim // 2 if mode in ("int4", "fp4") else head_dim,), dtype=dt, device=device)  # noqa: E731
+
+    def scales():
+        if mode in ("f16", "bf16"):
+            return None
+        if mode == "fp4":
+            return torch.empty(shape + (2 * (-(-head_dim // 64)),), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=torch.float32, device=device)
+
+    return KVCache(mode, codes(), codes(), scales(), scales())
+
+
+def kv_write(cache: KVCache, k, v, slots, clip_ratio: float = 1.0, dst_type_max: float = 0.0, stream=None) -> None:
+    """Quantize rows k, v [T, Hkv, D] (bfloat16 or float16) into the cache at slots [T] (int32:
+    page * page_size + offset; negative: not written)."""
+    _same_device(k, v, slots, cache.k)
+    kd, vd, sd = _desc(k), _desc(v), _desc(slots)
+    with _on_device(k.device):
+        st = lib.fq_kv_write(kd.ptr, vd.ptr, sd.ptr, clip_ratio, dst_type_max, *cache._ptrs(),
+                             _stream(stream, k.device).cuda_stream or None)
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_kv_write")
+
+
+def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=None, v_out=None, stream=None):
+    """The cached tokens of every sequence as values: (k, v) [total, Hkv, D] of ``dtype``,
+    sequence b in rows cu_seqlens[b] .. cu_seqlens[b+1]-1 (int32 [B+1]); block_table int32
+    [B, pages per sequence]."""
+    torch = _torch()
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        shape = (total, cache.heads, cache.head_dim)
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        _record(stream, k_out, v_out)
+    elif k_out.dtype != dtype or v_out.dtype != dtype or k_out.shape[0] != total or v_out.shape[0] != total:
+        raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
+    _same_device(cache.k, block_table, cu_seqlens, k_out, v_out)
+    bd, cd, kd, vd = _desc(block_table), _desc(cu_seqlens), _desc(k_out), _desc(v_out)
+    with _on_device(cache.device):
+        st = lib.fq_kv_read(*cache._ptrs(), bd.ptr, cd.ptr, kd.ptr, vd.ptr, _stream(stream, cache.device).cuda_stream or None)
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_kv_read")
+    return k_out, v_out
+
+
+def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out=None, lse=None, workspace=None,
+                stream=None):
+    """Attention of one new token per sequence: q [B, Hq, D] over the first lengths[b] (int32
+    [B]) cached tokens of sequence b; Hq a multiple of the cache's heads.  scale 0 means
+    1/sqrt(D).  ``lse`` (float32 [B, Hq]), when given, receives the log of the softmax's sum.
+    ``workspace`` (uint8, at least attn_decode_workspace_size) may be passed to reuse one."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _record(stream, out)
+    _same_device(q, cache.k, block_table, lengths, out, lse, workspace)
+    qd, bd, ld, od = _desc(q), _desc(block_table), _desc(lengths), _desc(out)
+    sd = _desc(lse) if lse is not None else None
+    size = ctypes.c_uint64(0)
+    st = lib.fq_attn_decode_get_workspace_size(qd.ptr, cache._kc.ptr, bd.ptr, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_decode_get_workspace_size")
+    s = _stream(stream, q.device)
+    need = size.value
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+        _record(stream, workspace)
+    with _on_device(q.device):
+        st = lib.fq_attn_decode(qd.ptr, *cache._ptrs(), bd.ptr, ld.ptr, scale, od.ptr, sd.ptr if sd else None,
+                                workspace.data_ptr() if workspace is not None else None,
+                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                s.cuda_stream or None)
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_decode")
+    return out
+
+
+def attn_decode_workspace_size(q, cache: KVCache, block_table) -> int:
+    size = ctypes.c_uint64(0)
+    qd, bd = _desc(q), _desc(block_table)
+    st = lib.fq_attn_decode_get_workspace_size(qd.ptr, cache._kc.ptr, bd.ptr, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_decode_get_workspace_size")
+    return size.value
+
+
+def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0.0, out=None, lse=None, stream=None):
+    """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hkv, D] (one 16-bit dtype),
+    sequence b in rows cu_q[b] .. cu_q[b+1]-1 of q and cu_k[b] .. cu_k[b+1]-1 of k and v (int32
+    [B+1]; cu_k defaults to cu_q).  Causal: row i sees keys up to (Lk - Lq) + i.  scale 0 means
+    1/sqrt(D).  ``lse``: float32 [Tq, Hq]."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _record(stream, out)
+    if cu_k is None:
+        cu_k = cu_q
+    _same_device(q, k, v, cu_q, cu_k, out, lse)
+    qd, kd, vd, ad, bd, od = _desc(q), _desc(k), _desc(v), _desc(cu_q), _desc(cu_k), _desc(out)
+    sd = _desc(lse) if lse is not None else None
+    with _on_device(q.device):
+        st = lib.fq_attn_prefill(qd.ptr, kd.ptr, vd.ptr, ad.ptr, bd.ptr, 1 if causal else 0, scale, od.ptr,
+                                 sd.ptr if sd else None, _stream(stream, q.device).cuda_stream or None)
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_prefill")
     return out

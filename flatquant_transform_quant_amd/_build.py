@@ -28,7 +28,8 @@ COMMON = [
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    return sorted(f for d in (CSRC, os.path.join(CSRC, "attn")) for ext in ("*.hip", "*.cpp")
+                  for f in glob.glob(os.path.join(d, ext)))
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -15,10 +15,17 @@
 #include <new>
 #include <unordered_set>
 
+#include "attn/fq_host_util.h"
 #include "fq.h"
 #include "fq_internal.h"
 
 using fq::ceil_div;
+using fq::clear_last_error;
+using fq::device_is_gfx950;
+using fq::fail_runtime;
+using fq::is_contiguous;
+using fq::shape_is;
+using fq::strides_ok;
 
 namespace {
 
@@ -40,7 +47,7 @@ struct fq_executor {
   uint64_t off_x, off_p1, off_p2, off_out, off_scale, off_ctr, ws_size;
 };
 
-namespace {
+namespace fq {
 
 bool is_contiguous(const fq_tensor& t) {
   int64_t expect = 1;
@@ -58,7 +65,7 @@ bool strides_ok(const fq_tensor& t) {
   return true;
 }
 
-bool shape_is(const fq_tensor& t, int nd, int64_t a, int64_t b = 0, int64_t c = 0) {
+bool shape_is(const fq_tensor& t, int nd, int64_t a, int64_t b, int64_t c) {
   if (t.ndim != nd) return false;
   const int64_t want[3] = {a, b, c};
   for (int d = 0; d < nd; ++d)
@@ -66,10 +73,16 @@ bool shape_is(const fq_tensor& t, int nd, int64_t a, int64_t b = 0, int64_t c = 
   return true;
 }
 
-uint64_t align256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
-
 // Detail of the last runtime failure on this thread (fq_last_error).
-thread_local char g_last_error[256];
+static thread_local char g_last_error[256];
+
+void clear_last_error() { g_last_error[0] = '\0'; }
+
+const char* last_error() { return g_last_error; }
+
+void set_last_error(const char* fmt, unsigned long long a, unsigned long long b) {
+  std::snprintf(g_last_error, sizeof(g_last_error), fmt, a, b);
+}
 
 fq_status fail_runtime(const char* what, hipError_t err) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (hipError %d)", what,
@@ -78,8 +91,8 @@ fq_status fail_runtime(const char* what, hipError_t err) {
 }
 
 // gfx950 check, cached per device id.
-std::mutex g_arch_mu;
-int g_arch_ok[64];  // 0 unknown, 1 yes, -1 no
+static std::mutex g_arch_mu;
+static int g_arch_ok[64];  // 0 unknown, 1 yes, -1 no
 
 bool device_is_gfx950() {
   int dev = 0;
@@ -98,6 +111,12 @@ bool device_is_gfx950() {
   }
   return ok;
 }
+
+}  // namespace fq
+
+namespace {
+
+uint64_t align256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
 
 // Executors handed out and not yet released.  fq_run and the other calls look a pointer
 // up here before touching it, so a released (single-use, already run) executor is
@@ -147,7 +166,7 @@ fq_status fq_get_workspace_size(const fq_tensor* x, const fq_tensor* kroneckerP1
                                 const fq_tensor* kroneckerP2, double clipRatio, double dstTypeMax,
                                 const fq_tensor* out, const fq_tensor* quantScale,
                                 uint64_t* workspaceSize, fq_executor** executor) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   // [FQV2] 容易踩的坑: a NULL among the three inputs and two outputs -> 161001.
   if (!x || !kroneckerP1 || !kroneckerP2 || !out || !quantScale || !workspaceSize || !executor)
     return FQ_ERR_PARAM_NULLPTR;
@@ -300,7 +319,7 @@ static void release(fq_executor* e) {
 }
 
 fq_status fq_run(void* workspace, uint64_t workspaceSize, fq_executor* executor, hipStream_t stream) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   if (!executor) return FQ_ERR_PARAM_NULLPTR;
   if (!live(executor)) return FQ_ERR_PARAM_INVALID;
   fq_executor* e = executor;
@@ -432,15 +451,14 @@ fq_status scratch_of_current_device(void** out) {
 extern "C" {
 
 fq_status fq_run_no_alloc(fq_executor* executor, hipStream_t stream) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   if (!executor) return FQ_ERR_PARAM_NULLPTR;
   if (!live(executor)) return FQ_ERR_PARAM_INVALID;
   fq_executor* e = executor;
   if (e->ws_size > FQ_NO_ALLOC_SCRATCH_BYTES) {
-    std::snprintf(g_last_error, sizeof(g_last_error),
-                  "the planned workspace of %llu bytes exceeds the %llu-byte scratch of fq_run_no_alloc",
-                  static_cast<unsigned long long>(e->ws_size),
-                  static_cast<unsigned long long>(FQ_NO_ALLOC_SCRATCH_BYTES));
+    fq::set_last_error("the planned workspace of %llu bytes exceeds the %llu-byte scratch of fq_run_no_alloc",
+                       static_cast<unsigned long long>(e->ws_size),
+                       static_cast<unsigned long long>(FQ_NO_ALLOC_SCRATCH_BYTES));
     if (!e->repeatable) release(e);
     return FQ_ERR_PARAM_INVALID;
   }
@@ -465,7 +483,7 @@ fq_status fq_v1_get_workspace_size(const fq_tensor* x, const fq_tensor* kronecke
 }
 
 fq_status fq_dequant(const fq_tensor* codes, const fq_tensor* scale, const fq_tensor* out, hipStream_t stream) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   if (!codes || !scale || !out || !codes->data || !scale->data || !out->data) return FQ_ERR_PARAM_NULLPTR;
   // out: the values, [K, M, N] in x's dtype (its sizes fix K, M and N)
   if (out->ndim != 3 || !strides_ok(*out)) return FQ_ERR_PARAM_INVALID;
@@ -524,7 +542,7 @@ fq_status fq_dequant(const fq_tensor* codes, const fq_tensor* scale, const fq_te
 
 fq_status fq_int4_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
                        const fq_tensor* c, hipStream_t stream) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   for (const fq_tensor* t : {a, a_scale, w, w_scale, c})
     if (!t || !t->data) return FQ_ERR_PARAM_NULLPTR;
   for (const fq_tensor* t : {a, a_scale, w, w_scale, c})
@@ -555,7 +573,7 @@ fq_status fq_int4_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_te
 
 fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
                      const fq_tensor* c, hipStream_t stream) {
-  g_last_error[0] = '\0';
+  clear_last_error();
   for (const fq_tensor* t : {a, a_scale, w, w_scale, c})
     if (!t || !t->data) return FQ_ERR_PARAM_NULLPTR;
   for (const fq_tensor* t : {a, a_scale, w, w_scale, c})
@@ -605,7 +623,7 @@ int32_t fq_executor_kernel(const fq_executor* executor) {
   return executor->kernel;
 }
 
-const char* fq_last_error(void) { return g_last_error; }
+const char* fq_last_error(void) { return fq::last_error(); }
 
 const char* fq_status_string(fq_status status) {
   switch (status) {

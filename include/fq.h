@@ -235,6 +235,92 @@ fq_status fq_int4_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_te
 fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
                      const fq_tensor* c, hipStream_t stream);
 
+/* ---- paged key-value cache -------------------------------------------------------------
+ * The keys and values of an attention layer, kept in the formats the quantizer writes.  A cache
+ * is two sides (keys, values) of the same shape; each is a codes tensor and, for the low-bit
+ * formats, a scale tensor, over pages of P tokens:
+ *   codes  FLOAT16 | BFLOAT16                    [pages, Hkv, P, D]
+ *          INT8 | FLOAT8_E4M3FN                  [pages, Hkv, P, D]   scale FLOAT32 [pages, Hkv, P]
+ *          INT4          (2 codes per byte)      [pages, Hkv, P, D]   scale FLOAT32 [pages, Hkv, P]
+ *          FLOAT4_E2M1   (2 codes per byte)      [pages, Hkv, P, D]   scale FLOAT8_E8M0
+ *                                                             [pages, Hkv, P, 2 * ceilDiv(D, 64)]
+ *   P a power of two, 16 <= P <= 1024; 8 <= D <= 256, D % 8 == 0 (% 32 for FLOAT4_E2M1);
+ *   1 <= Hkv <= 1024; pages * P < 2^31.  The scale pointers are NULL for the 16-bit formats.
+ * A row -- one token's D elements of one head -- is quantized as the quantizer's per-token and
+ * per-group rules quantize a slice: scale = fl32(max|x| / fl32(max_val / clipRatio)) (max_val
+ * 127, 448, 7) and code = clamp(round_half_even(fl32(x / scale))); or one e8m0 byte per 32
+ * elements by dstTypeMax's rule and E2M1 codes (bytes past D/32 in the scale row are 0).  An
+ * all-zero row (group) gets scale 0 and codes 0.  A row (group) that holds an infinity or NaN
+ * reads back as NaN throughout: its scale is stored non-finite (e8m0 0xFF).
+ * Every dimension but the first must be contiguous; the first may have any stride that is a
+ * multiple of 16 bytes (of 4 bytes for the scales), so one allocation can interleave the two
+ * sides.  Codes 16-byte aligned, scales 4-byte aligned.  Token t of a sequence lies in page
+ * block_table[sequence, t / P] at offset t % P.  All tensors are device memory owned by the
+ * caller, valid until the work completes on the stream; all calls enqueue on `stream` without
+ * synchronizing, allocate nothing, may be captured in a graph, and read slots, block tables and
+ * lengths on the device, where every index is checked: one outside the cache is never followed.
+ *
+ * 16-bit row tensors (k, v, q, outputs) are FLOAT16 | BFLOAT16 [rows, heads, D] with innermost
+ * stride 1, the other strides multiples of 8 elements and data 16-byte aligned; an empty one
+ * (a dimension of 0) may have NULL data, and a call with no rows does nothing.
+ * Errors of all these calls: a required tensor or data pointer NULL -> FQ_ERR_PARAM_NULLPTR;
+ * any dtype, shape, stride, alignment or scalar outside the above -> FQ_ERR_PARAM_INVALID (no
+ * HIP call is made before these checks); not a gfx950 device, or a launch failure ->
+ * FQ_ERR_RUNTIME.
+ *
+ * fq_kv_write: rows k[i], v[i] ([T, Hkv, D]) go to slot slots[i] = page * P + offset (INT32
+ * [T]).  A negative slot, or one beyond the cache, writes nothing (padding).  No slot may occur
+ * twice in a call.  clipRatio in (0, 1] acts on the per-token formats, dstTypeMax (0, or 6 to
+ * 12) on FLOAT4_E2M1; a 16-bit cache must have k's dtype and stores the rows unchanged. */
+fq_status fq_kv_write(const fq_tensor* k, const fq_tensor* v, const fq_tensor* slots, double clipRatio,
+                      double dstTypeMax, const fq_tensor* k_cache, const fq_tensor* k_scale,
+                      const fq_tensor* v_cache, const fq_tensor* v_scale, hipStream_t stream);
+
+/* fq_kv_read: the first cu[b+1] - cu[b] tokens of every sequence b, as values, packed: token t
+ * of sequence b goes to row cu[b] + t of k_out and v_out ([T, Hkv, D]).  block_table INT32
+ * [B, pages per sequence] (innermost stride 1), cu INT32 [B+1] ascending from 0.  The value is
+ * code * scale in fp32 rounded once to the output's dtype (a 16-bit cache must have the
+ * output's dtype).  Rows from cu[B] on are not written; a token whose table entry is missing or
+ * outside the cache gives zeros. */
+fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const fq_tensor* v_cache,
+                     const fq_tensor* v_scale, const fq_tensor* block_table, const fq_tensor* cu,
+                     const fq_tensor* k_out, const fq_tensor* v_out, hipStream_t stream);
+
+/* ---- attention of one new token over the cache --------------------------------------------
+ *     out[b, h] = sum_t p[t] v[t, h / g],  p = softmax over t < lengths[b] of scale * <q[b, h], k[t, h / g]>
+ * with g = Hq / Hkv (a whole number) query heads sharing a cache head.  q, out FLOAT16 |
+ * BFLOAT16 [B, Hq, D] of one dtype (a 16-bit cache must have it too), lengths INT32 [B] (the
+ * newest token included; capped at the table's reach), block_table as above, 1 <= Hq <= 65536.
+ * `lse`, when not NULL, is FLOAT32 [B, Hq] (contiguous) and receives log sum_t exp(scale *
+ * <q, k[t]>).  A length of 0 (an idle place of a fixed batch) gives zeros and lse = -infinity.
+ * A token whose table entry is outside the cache is left out of the sum; cache contents past a
+ * sequence's length are never used, whatever they hold.  scale is finite; 0 means 1/sqrt(D).
+ * Codes enter the products exactly; scores, softmax statistics and sums are fp32.  Results do
+ * not depend on the run: the same inputs give the same bits.
+ * The cache is read once, split over its length across the device and joined; the partial sums
+ * live in `workspace` (device memory, 16-byte aligned, of at least the size that
+ * fq_attn_decode_get_workspace_size gives for the same q, cache and table; contents need not be
+ * initialised; calls that overlap in time must not share it). */
+fq_status fq_attn_decode_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table,
+                                            uint64_t* workspaceSize);
+fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* k_scale,
+                         const fq_tensor* v_cache, const fq_tensor* v_scale, const fq_tensor* block_table,
+                         const fq_tensor* lengths, double scale, const fq_tensor* out, const fq_tensor* lse,
+                         void* workspace, uint64_t workspaceSize, hipStream_t stream);
+
+/* ---- attention over packed prompts -----------------------------------------------------------
+ * Sequences of different lengths packed row after row: sequence b has the query rows cu_q[b] ..
+ * cu_q[b+1]-1 of q, out [Tq, Hq, D] and the key rows cu_k[b] .. cu_k[b+1]-1 of k, v [Tk, Hkv, D]
+ * (all of one dtype; cu_q, cu_k INT32 [B+1], ascending from 0).  With causal != 0 query row i
+ * of a sequence sees its keys 0 .. (Lk - Lq) + i: the queries are the sequence's last rows, so
+ * a prompt's chunk attends to the part before it (read back with fq_kv_read) and to itself.
+ * With causal == 0 it sees all Lk.  A row that sees no key gives zeros and lse = -infinity.
+ * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536.  Rows of
+ * out past cu_q[B] are not written. */
+fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tensor* v, const fq_tensor* cu_q,
+                          const fq_tensor* cu_k, int32_t causal, double scale, const fq_tensor* out,
+                          const fq_tensor* lse, hipStream_t stream);
+
 /* Releases an executor that will not be run (or a repeatable one).  NULL is a no-op. */
 void fq_executor_destroy(fq_executor* executor);
 
