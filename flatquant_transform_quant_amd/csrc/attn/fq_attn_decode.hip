@@ -1,0 +1,782 @@
+// Attention of one new token per sequence over the paged cache.
+//
+// For a cache head and its g query heads: s[t, h] = <q_h, k_t>, p = softmax over t, o_h = sum_t
+// p[t, h] v_t.  Every cached byte is used for g <= 16 heads at once, so the products run on the
+// matrix cores with the heads as the 16 columns of a tile (heads beyond 16 take further tiles)
+// and the kernel is bound by reading the cache.
+//
+// One wave and 32 tokens (two subtiles of 16), v_mfma_f32_16x16x32:
+//   S^T = K Q^T: the A operand's row is a token, so a lane reads pieces of one key row straight
+//     from memory into operand position -- no LDS, no transpose.  Lane l ends with tokens
+//     16 a + 4 (l / 16) + 0..3 of both subtiles a, for head l % 16.
+//   O^T = V^T P^T: those 8 weights of a lane are, rounded to 16 bits, its B operand as they
+//     stand (contraction slot j of lane group l / 16 is token 16 (j / 4) + 4 (l / 16) + j % 4).
+//     V^T's row is an element d; a lane reads EC consecutive elements of its 8 tokens and pairs
+//     them across tokens with byte permutes: product jj takes element EC (l % 16) + jj.
+// Codes enter the products exactly, as f16 numbers (16-bit caches: as they are):
+//   int8, int4: the code plus 128 or 8 (u >= 0) in the low bits of a half is the f16 subnormal
+//     u 2^-24, so widening costs a byte permute or a mask; one packed fused multiply-add makes it
+//     the number (u - 128) 2^-9 or (u - 8) 2^-9, exactly.  (Subnormals themselves as operands lose
+//     accuracy in the products' internal alignment -- scores were off by 2^-17 -- and a bias left
+//     in and taken off the sums costs as much where a row's codes are small.)  Nibbles masked at
+//     bits 4..7 are 16 u: q carries 1/16 at those elements, the output is divided by 16.
+//   E4M3, E2M1: the converting instructions; E2M1 takes its group's power of two, relative to
+//     the largest of the tile (keys) or to a running reference (values), along with it.
+// A bf16 q is brought to f16 by a power of two per row (28 binades keep full precision).  The
+// value scale of a token multiplies its weight: w = p scale 2^-R rounded to f16, with R a
+// running reference exponent, so that w stays in range; a scale below 2^-24 of the largest
+// one in a sequence loses bits in proportion.
+// Softmax statistics are fp32: the running maximum m (base-2 scores) is only moved when a score
+// passes m + 8 (weights then reach 2^8, far inside f16's range), so the common tile has no
+// cross-lane step and no rescaling.
+//
+// Split: the units of work are 128 tokens (4 waves x 32) of a (sequence, cache head, head tile);
+// all units in order are dealt to the grid in equal runs, whatever the lengths.  A run that holds
+// only part of a segment leaves its unnormalised sums and (m, l) in the workspace, and a second
+// launch joins them in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include "fq_attn_dev.h"
+
+namespace fq {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kTile = 32;                    // tokens of a wave's step
+constexpr int kUnit = kWaves * kTile;        // tokens of a unit
+constexpr int kBatch = 31;                   // steps per fetch of the block table (64 subtiles cover one step more)
+constexpr int kMaxGrid = 1024;               // workgroups of a launch at most: four on each of 256 CUs
+constexpr float kLazy = 8.0f;                // base-2 slack of the running maximum
+constexpr float kInf = __builtin_inff();
+
+template <int MODE>
+constexpr int kBits = MODE == kKv16 ? 16 : (MODE == kKvInt8 || MODE == kKvE4M3) ? 8 : 4;
+
+// Sizes of a lane's pieces.  DP: D rounded up to 64, 128 or 256; PAD: D < DP, where pieces at
+// or past D are zeros (pieces are then 8 elements, which D's multiple of 8 never cuts).
+template <int MODE, int DP, bool PAD>
+struct Shape {
+  static constexpr int bits = kBits<MODE>;
+  static constexpr int CE = PAD ? 8 : (128 / bits < DP / 4 ? 128 / bits : DP / 4);  // elements of a key piece
+  static constexpr int KC = DP / (4 * CE);                                         // pieces of a lane in a key row
+  static constexpr int KW = CE * bits / 32;                                        // dwords of a piece
+  static constexpr int EC = DP / 16 < 8 ? DP / 16 : 8;                             // elements of a value piece
+  static constexpr int NH = DP / (16 * EC);
+  static constexpr int VB = EC * bits / 8;                                         // bytes of a value piece
+  static constexpr int VW = VB < 4 ? 1 : VB / 4;
+  static constexpr int KS = DP / 32;                                               // products of a score
+  // workgroups of a CU (waves of a SIMD): what registers and, at 256, LDS hold
+  static constexpr int per_cu = DP == 256 ? (bits == 16 ? 1 : 2) : bits == 16 ? (DP == 128 ? 2 : 4) : 3;
+};
+
+template <int MODE, int DP, bool PAD>
+struct Keys {
+  using S = Shape<MODE, DP, PAD>;
+  uint32_t w[2][S::KC][S::KW];
+  f32x4_t scale[MODE == kKv16 || MODE == kKvFp4 ? 1 : 2];
+  uint32_t e8[MODE == kKvFp4 ? 2 : 1][S::KC];
+};
+template <int MODE, int DP, bool PAD>
+struct Values {
+  using S = Shape<MODE, DP, PAD>;
+  uint32_t w[8][S::NH][S::VW];
+  f32x4_t scale[MODE == kKv16 || MODE == kKvFp4 ? 1 : 2];
+  uint32_t e8[MODE == kKvFp4 ? 8 : 1][S::NH];
+};
+
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
+
+template <int W>
+__device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t (&o)[W]) {
+  if constexpr (W == 4) {
+    const u32x4_t x = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = x[i];
+  } else if constexpr (W == 2) {
+    const u32x2_t x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    o[0] = x[0];
+    o[1] = x[1];
+  } else {
+    o[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t h2(float a, float b) { return round16x2<DT>(a, b); }
+
+// Two halves u 2^-24 (u the biased code, an f16 subnormal) -> (u - bias) 2^-9, exact.
+__device__ __forceinline__ uint32_t unbias_f16(uint32_t a, uint32_t minus) {
+  typedef __attribute__((ext_vector_type(2))) _Float16 h16x2;
+  const h16x2 up = __builtin_bit_cast(h16x2, 0x78007800u);  // 2^15
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h16x2, a), up, __builtin_bit_cast(h16x2, minus)));
+}
+constexpr uint32_t kMinus8 = 0xA400A400u, kMinus128 = 0xB400B400u;  // -8 2^-9, -128 2^-9
+template <int SEL>
+__device__ __forceinline__ uint32_t fp4_to_f16x2(uint32_t w, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, SEL));
+}
+template <bool HI>
+__device__ __forceinline__ uint32_t fp8_to_f16x2(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+}
+
+// 2^e as fp32 for e in [-126, 127]; 0 below (e never passes 127 here)
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
+
+// Operand of 8 key elements from a piece's dwords (e: which 8); s: the E2M1 group's factor.
+template <int MODE, int KW>
+__device__ __forceinline__ u32x4_t key_operand(const uint32_t (&w)[KW], int e, float s) {
+  if constexpr (MODE == kKv16) {
+    return u32x4_t{w[0], w[1], w[2], w[3]};
+  } else if constexpr (MODE == kKvInt8) {
+    const uint32_t a = w[2 * e] ^ 0x80808080u, b = w[2 * e + 1] ^ 0x80808080u;
+    return u32x4_t{unbias_f16(__builtin_amdgcn_perm(0u, a, 0x0C010C00u), kMinus128), unbias_f16(__builtin_amdgcn_perm(0u, a, 0x0C030C02u), kMinus128),
+                   unbias_f16(__builtin_amdgcn_perm(0u, b, 0x0C010C00u), kMinus128), unbias_f16(__builtin_amdgcn_perm(0u, b, 0x0C030C02u), kMinus128)};
+  } else if constexpr (MODE == kKvE4M3) {
+    return u32x4_t{fp8_to_f16x2<false>(w[2 * e]), fp8_to_f16x2<true>(w[2 * e]), fp8_to_f16x2<false>(w[2 * e + 1]),
+                   fp8_to_f16x2<true>(w[2 * e + 1])};
+  } else if constexpr (MODE == kKvInt4) {  // order n0 n4 n1 n5 n2 n6 n3 n7, the odd ones x 16
+    const uint32_t x = w[e] ^ 0x88888888u, y = x >> 8;
+    return u32x4_t{unbias_f16(x & 0x000F000Fu, kMinus8), unbias_f16(x & 0x00F000F0u, kMinus128), unbias_f16(y & 0x000F000Fu, kMinus8),
+                   unbias_f16(y & 0x00F000F0u, kMinus128)};
+  } else {
+    return u32x4_t{fp4_to_f16x2<0>(w[e], s), fp4_to_f16x2<1>(w[e], s), fp4_to_f16x2<2>(w[e], s), fp4_to_f16x2<3>(w[e], s)};
+  }
+}
+
+// Element of q at place j of such an operand, and the factor it carries.
+template <int MODE>
+__device__ __forceinline__ constexpr int q_place(int j) {
+  constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+  return MODE == kKvInt4 ? order[j] : j;
+}
+
+// max over the four lanes that share l % 16
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ int wave_imax(int v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = max(v, __shfl_xor(v, o));
+  return v;
+}
+
+// the same value, opaque to the compiler from here on
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+__device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int b) {
+  const int64_t reach = static_cast<int64_t>(a.bt.width) << a.c.page_log;
+  return static_cast<int32_t>(max(int64_t(0), min(static_cast<int64_t>(a.lengths[b]), reach)));
+}
+__device__ __forceinline__ int32_t units_of(int32_t n) { return n / kUnit + (n % kUnit != 0); }
+
+// A segment: the tokens of one (sequence, cache head, head tile).
+struct Segment {
+  int32_t b, hk, ht, n;  // n: the sequence's length
+};
+
+template <int MODE, int DT, int DP, bool PAD>
+__global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void decode_kernel(DecodeArgs a, float* __restrict__ part, int32_t nht, int32_t gh,
+                                                             bool single) {
+  using S = Shape<MODE, DP, PAD>;
+  constexpr bool kScaled = MODE == kKvInt8 || MODE == kKvE4M3 || MODE == kKvInt4;  // a scale per token
+  constexpr int PDT = MODE == kKv16 ? DT : kF16;                                   // operands' type
+  constexpr float kCode = MODE == kKvInt8 || MODE == kKvInt4 ? 512.0f : 1.0f;       // 1 / the operand's unit
+  constexpr int LDH = 17;  // row pitch of the output exchange (heads)
+  __shared__ float s_o[kWaves][DP * LDH];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  __shared__ int64_t s_sum[kWaves];
+  __shared__ int32_t s_b;
+  __shared__ int64_t s_at;
+
+  const KvCache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kb = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int D = PAD ? c.D : DP;
+  const int per_b = c.Hkv * nht;  // segments of a sequence
+  const int rowb = D * S::bits / 8;
+  const int sb = MODE == kKvFp4 ? 2 * ((D + 63) / 64) : 4;
+
+  // ---- this workgroup's run of units
+  int64_t u = 0, u_end = 0;  // units from the start of sequence b on
+  int b = 0;
+  if (single) {  // every segment is one unit: no plan, no join
+    b = blockIdx.x / per_b;
+    u = blockIdx.x - b * per_b;
+    u_end = u + 1;
+  } else {
+    // total, then the sequence that holds the first unit, by scans over the lengths 256 at a time
+    int64_t mine = 0;
+    for (int i = tid; i < a.B; i += kThreads) mine += units_of(length_of(a, i));
+    for (int o = 1; o < 64; o <<= 1) mine += __shfl_xor(mine, o);
+    if (lane == 0) s_sum[wv] = mine;
+    __syncthreads();
+    const int64_t total = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * per_b;
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x, first = per * blockIdx.x;
+    if (first >= total) return;
+    int64_t base = 0;
+    for (int i0 = 0; i0 < a.B; i0 += kThreads) {
+      __syncthreads();
+      const int i = i0 + tid;
+      const int64_t n = i < a.B ? static_cast<int64_t>(units_of(length_of(a, i))) * per_b : 0;
+      int64_t incl = n;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t t = __shfl_up(incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (lane == 63) s_sum[wv] = incl;
+      __syncthreads();
+      for (int w = 0; w < wv; ++w) incl += s_sum[w];
+      const int64_t end = base + incl;
+      if (first >= end - n && first < end) {
+        s_b = i;
+        s_at = end - n;
+      }
+      base += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+      if (first < base) break;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(s_b);
+    u = first - s_at;
+    u_end = min(first + per, total) - s_at;
+  }
+
+  bool first_seg = true;
+  while (u < u_end) {
+    // ---- the next segment of the run
+    const int32_t n = __builtin_amdgcn_readfirstlane(length_of(a, b));
+    const int32_t nu = single ? 1 : units_of(n);
+    if (u >= static_cast<int64_t>(nu) * per_b) {  // on to the next sequence
+      u -= static_cast<int64_t>(nu) * per_b;
+      u_end -= static_cast<int64_t>(nu) * per_b;
+      ++b;
+      continue;
+    }
+    const int seg = __builtin_amdgcn_readfirstlane(static_cast<int>(u / nu));
+    const int hk = seg / nht, ht = seg - hk * nht;
+    const int ua = __builtin_amdgcn_readfirstlane(static_cast<int>(u - static_cast<int64_t>(seg) * nu));
+    const int ue = static_cast<int>(min(static_cast<int64_t>(nu), ua + (u_end - u)));
+    u += ue - ua;
+    const int head = ht * 16 + r16;  // this lane's head within the group
+    const bool my_head = head < a.g;
+
+    // ---- q as the B operand, and the column's constants
+    u32x4_t qf[S::KS];
+    float cq = a.scale * 1.44269504f * kCode;
+    {
+      const uint16_t* qp = a.q.p + b * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
+      u32x4_t raw[S::KS];
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) {
+        const int d = S::CE * (4 * (ks / (S::CE / 8)) + kb) + 8 * (ks % (S::CE / 8));
+        raw[ks] = u32x4_t{0u, 0u, 0u, 0u};
+        if (my_head && d < D) raw[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
+      }
+      if constexpr (MODE == kKv16) {
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) qf[ks] = raw[ks];
+      } else {
+        float top = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+          float x[8];
+          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(x[j]));
+        }
+        // |q| < 2^(e + 1) at its largest; brought to [2^13, 2^14)
+        const int e = static_cast<int>((__float_as_uint(column_max(top)) >> 23) & 0xFFu) - 127;
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+          float x[8], y[8];
+          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            y[j] = __builtin_amdgcn_ldexpf(x[q_place<MODE>(j)], 13 - e);
+            if (MODE == kKvInt4 && (j & 2)) y[j] *= 0.0625f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[ks][i] = h2<kF16>(y[2 * i], y[2 * i + 1]);
+        }
+        cq = __builtin_amdgcn_ldexpf(cq, e - 13);
+      }
+    }
+
+    // ---- state of the segment
+    f32x4_t acc[S::NH][S::EC];
+#pragma unroll
+    for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+      for (int j = 0; j < S::EC; ++j) acc[h][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -kInf, l = 0.0f;
+    int ref = -100000;      // exponent R of the value scales (wave-uniform); far below any
+    float ref_inv = 0.0f;   // 2^-R
+    float ref_lim = 0.0f;   // a scale at or above 2^(R + 6) moves R
+
+    // this wave's steps: tokens kUnit (ua + i) + kTile wv ..
+    const int t_first = kUnit * ua + kTile * wv;
+    const int t_last = min(n, kUnit * ue);
+    const int steps = t_first < t_last ? (t_last - t_first + kUnit - 1) / kUnit : 0;
+
+    int32_t pages = -1;  // lane 2 i + s: the page of subtile s of step (batch) + i
+    auto fetch_pages = [&](int step) __attribute__((always_inline)) {
+      const int64_t t = static_cast<int64_t>(t_first) + static_cast<int64_t>(kUnit) * (step + (lane >> 1)) + 16 * (lane & 1);
+      pages = t < n ? kv_page(a.bt, b, static_cast<int32_t>(t), c.page_log, c.pages) : -1;
+    };
+    const int64_t khead = static_cast<int64_t>(hk) << c.page_log;
+    const uint32_t koff = r16 * rowb + kb * (S::CE * S::bits / 8), keoff = r16 * sb + (S::CE * kb) / 32;
+    const uint32_t voff = 4 * kb * rowb + r16 * S::VB, veoff = 4 * kb * sb + (S::EC * r16) / 32;
+    // Loads go through a buffer resource per subtile that starts at its first row and ends behind
+    // its last token (at nothing for a subtile without a page): rows past n, and the pieces of
+    // padded lanes, whose offset is kOut, are zeros without a branch.
+    auto rows_of = [&](int step, int s) __attribute__((always_inline)) {
+      return max(0, min(16, n - (t_first + kUnit * step + 16 * s)));
+    };
+    auto resource = [&](const uint8_t* base, int64_t page_b, int row_b, int step, int s, int idx) __attribute__((always_inline)) {
+      const int32_t pg = __builtin_amdgcn_readlane(pages, 2 * idx + s);
+      const int off = (t_first + kUnit * step + 16 * s) & ((1 << c.page_log) - 1);
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (max(pg, 0) * page_b + (khead + off) * row_b), static_cast<int16_t>(0),
+                                               pg < 0 ? 0 : rows_of(step, s) * row_b, kBufferWord3);
+    };
+    auto load_keys = [&](Keys<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const auto rc = resource(c.k.codes, c.k.page_b, rowb, step, s, idx);
+#pragma unroll
+        for (int p = 0; p < S::KC; ++p)
+          load_words<S::KW>(rc, (PAD && S::CE * (4 * p + kb) >= D ? kOut : koff) + p * (4 * S::CE * S::bits / 8), x.w[s][p]);
+        if constexpr (MODE != kKv16) {
+          const auto rs = resource(c.k.scale, c.k.scale_page_b, sb, step, s, idx);
+          if constexpr (MODE == kKvFp4) {
+#pragma unroll
+            for (int p = 0; p < S::KC; ++p)
+              x.e8[s][p] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && S::CE * (4 * p + kb) >= D ? kOut : keoff) + S::CE * 4 * p / 32, 0, 0);
+          } else {
+            x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
+          }
+        }
+      }
+    };
+    auto load_values = [&](Values<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const auto rc = resource(c.v.codes, c.v.page_b, rowb, step, s, idx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < S::NH; ++h) {
+            const uint32_t o = (PAD && 128 * h + S::EC * r16 >= D ? kOut : voff) + i * rowb + h * (16 * S::VB);
+            if constexpr (S::VB == 2)
+              x.w[4 * s + i][h][0] = __builtin_amdgcn_raw_buffer_load_b16(rc, o, 0, 0);
+            else
+              load_words<S::VW>(rc, o, x.w[4 * s + i][h]);
+          }
+        if constexpr (MODE != kKv16) {
+          const auto rs = resource(c.v.scale, c.v.scale_page_b, sb, step, s, idx);
+          if constexpr (MODE == kKvFp4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int h = 0; h < S::NH; ++h)
+                x.e8[4 * s + i][h] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && 128 * h + S::EC * r16 >= D ? kOut : veoff) + i * sb + 4 * h, 0, 0);
+          } else {
+            x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
+          }
+        }
+      }
+    };
+    // the rows a lane's four tokens of a subtile have left (0 .. 4): for steps that are not whole
+    auto mine = [&](int step, int s, int idx) __attribute__((always_inline)) {
+      return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows_of(step, s)) - 4 * kb;
+    };
+
+    // base-2 scores of a step
+    auto score = [&](const Keys<MODE, DP, PAD>& x, int step, int idx, bool whole, float (&s)[8]) __attribute__((always_inline)) {
+      int ek = 0;  // E2M1: the tile's largest exponent
+      if constexpr (MODE == kKvFp4) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int p = 0; p < S::KC; ++p) ek = max(ek, static_cast<int>(x.e8[s][p]));
+        ek = __builtin_amdgcn_readfirstlane(wave_imax(ek));
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+          constexpr int E = S::CE / 8;
+          const float f = MODE == kKvFp4 ? (x.e8[t][ks / E] == 255u ? __builtin_nanf("") : pow2(static_cast<int>(x.e8[t][ks / E]) - ek)) : 0.0f;
+          z = mfma16x16x32<PDT>(key_operand<MODE, S::KW>(x.w[t][ks / E], ks % E, f), qf[ks], z);
+        }
+        const float cf = MODE == kKvFp4 ? __builtin_amdgcn_ldexpf(cq, ek - 127) : cq;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 * t + i] = z[i] * (kScaled ? cf * x.scale[t][i] : cf);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int left = mine(step, t, idx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i >= left) s[4 * t + i] = -kInf;
+        }
+      }
+    };
+
+    // their weights p = exp2(s - m), the running maximum and sum moved along
+    auto weigh = [&](float (&s)[8]) __attribute__((always_inline)) {
+      float top = s[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
+      if (__any(top > m + kLazy)) {
+        const float mn = fmaxf(m, column_max(top));
+        const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+          for (int j = 0; j < S::EC; ++j) acc[h][j] *= f;
+      }
+      const float ms = m == -kInf ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(s[i] - ms);
+        l += s[i];
+      }
+    };
+
+    // the weighted values
+    auto add = [&](Values<MODE, DP, PAD>& x, int step, int idx, bool whole, float (&w)[8]) __attribute__((always_inline)) {
+      auto move_ref = [&](int r) __attribute__((always_inline)) {  // sums to the reference 2^r
+        const float f = ref < -1000 ? 0.0f : pow2(max(ref - r, -127));
+#pragma unroll
+        for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+          for (int j = 0; j < S::EC; ++j) acc[h][j] *= f;
+        ref = r;
+      };
+      if constexpr (MODE == kKvFp4) {
+        int ev = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int h = 0; h < S::NH; ++h) ev = max(ev, x.e8[i][h] == 255u ? 0 : static_cast<int>(x.e8[i][h]));  // (255: NaN)
+        if (__any(ev > ref + 6)) move_ref(__builtin_amdgcn_readfirstlane(wave_imax(ev)));
+      }
+      if constexpr (kScaled) {
+        if (!whole) {  // (the scales of tokens past n may be anything)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int left = mine(step, t, idx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i >= left) x.scale[t][i] = 0.0f;
+          }
+        }
+        float big = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, x.scale[i / 4][i % 4]);
+        if (__any(big >= ref_lim)) {
+          // (a tile of zero scales leaves the reference where it is)
+          const int r = __builtin_amdgcn_readfirstlane(wave_imax(static_cast<int>((__float_as_uint(big) >> 23) & 0xFFu) - 127));
+          if (r > ref && r > -127) {
+            move_ref(r);
+            ref_inv = pow2(min(-r, 127));
+            ref_lim = r + 6 > 127 ? kInf : pow2(max(r + 6, -126));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= x.scale[i / 4][i % 4] * ref_inv;
+      }
+      u32x4_t pf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pf[i] = h2<PDT>(w[2 * i], w[2 * i + 1]);
+#pragma unroll
+      for (int h = 0; h < S::NH; ++h) {
+#pragma unroll
+        for (int q = 0; q < S::EC / 4; ++q) {  // elements 4 q .. 4 q + 3
+          uint32_t o[4][4];  // operand dwords: tokens 2 p, 2 p + 1 of an element
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const auto& y0 = x.w[2 * p][h];
+            const auto& y1 = x.w[2 * p + 1][h];
+            if constexpr (MODE == kKvInt8) {
+              constexpr uint32_t sel[4] = {0x0C040C00u, 0x0C050C01u, 0x0C060C02u, 0x0C070C03u};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                o[j][p] = unbias_f16(__builtin_amdgcn_perm(y1[q] ^ 0x80808080u, y0[q] ^ 0x80808080u, sel[j]), kMinus128);
+            } else if constexpr (MODE == kKvInt4) {
+              const uint32_t z = __builtin_amdgcn_perm(y1[0], y0[0], q ? 0x07060302u : 0x05040100u) ^ 0x88888888u, zz = z >> 8;
+              o[0][p] = unbias_f16(z & 0x000F000Fu, kMinus8);
+              o[1][p] = unbias_f16(z & 0x00F000F0u, kMinus128);
+              o[2][p] = unbias_f16(zz & 0x000F000Fu, kMinus8);
+              o[3][p] = unbias_f16(zz & 0x00F000F0u, kMinus128);
+            } else {
+              uint32_t e0[2], e1[2];  // the elements of both tokens as halves
+              if constexpr (MODE == kKv16) {
+                e0[0] = y0[2 * q];
+                e0[1] = y0[2 * q + 1];
+                e1[0] = y1[2 * q];
+                e1[1] = y1[2 * q + 1];
+              } else if constexpr (MODE == kKvE4M3) {
+                e0[0] = fp8_to_f16x2<false>(y0[q]);
+                e0[1] = fp8_to_f16x2<true>(y0[q]);
+                e1[0] = fp8_to_f16x2<false>(y1[q]);
+                e1[1] = fp8_to_f16x2<true>(y1[q]);
+              } else {
+                const uint32_t b0 = x.e8[2 * p][h], b1 = x.e8[2 * p + 1][h];
+                const float f0 = b0 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b0) - ref);
+                const float f1 = b1 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b1) - ref);
+                e0[0] = q ? fp4_to_f16x2<2>(y0[0], f0) : fp4_to_f16x2<0>(y0[0], f0);
+                e0[1] = q ? fp4_to_f16x2<3>(y0[0], f0) : fp4_to_f16x2<1>(y0[0], f0);
+                e1[0] = q ? fp4_to_f16x2<2>(y1[0], f1) : fp4_to_f16x2<0>(y1[0], f1);
+                e1[1] = q ? fp4_to_f16x2<3>(y1[0], f1) : fp4_to_f16x2<1>(y1[0], f1);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                o[j][p] = __builtin_amdgcn_perm(e1[j / 2], e0[j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[h][4 * q + j] = mfma16x16x32<PDT>(u32x4_t{o[j][0], o[j][1], o[j][2], o[j][3]}, pf, acc[h][4 * q + j]);
+          __builtin_amdgcn_sched_barrier(0);  // (bounds the operands alive at once)
+        }
+      }
+    };
+
+    // ---- the steps, in a pipeline: the next step's keys are loaded as soon as this one's scores
+    // are formed, its values as soon as this one's are added, so a wave always has one of the
+    // two in flight.
+    if (steps > 0) {
+      Keys<MODE, DP, PAD> kx;
+      Values<MODE, DP, PAD> vx;
+      float s[8];
+      int base = 0;
+      fetch_pages(0);
+      load_keys(kx, 0, 0);
+      load_values(vx, 0, 0);
+      for (int i = 0; i < steps; ++i) {
+        const int idx = i - base;
+        const bool whole = t_first + kUnit * i + kTile <= n && __builtin_amdgcn_readlane(pages, 2 * idx) >= 0 &&
+                           __builtin_amdgcn_readlane(pages, 2 * idx + 1) >= 0;
+        score(kx, i, idx, whole, s);
+        if (i + 1 < steps) load_keys(kx, i + 1, idx + 1);
+        weigh(s);
+        add(vx, i, idx, whole, s);
+        if (i + 1 < steps) load_values(vx, i + 1, idx + 1);
+        if (idx + 1 == kBatch) {  // the last fetched step is under way: fetch from it on
+          base = i + 1;
+          fetch_pages(base);
+        }
+      }
+    }
+
+    // ---- the four waves' sums joined; the whole segment's rows out, or its part to the workspace
+    // (lane indices redefined: what derives from them is not kept in registers across the steps)
+    const int el = static_cast<int>(here(lane)), er = el & 15, eb = el >> 4;
+    l = column_sum(l);
+    if (eb == 0) {
+      s_m[wv][er] = m;
+      s_l[wv][er] = l;
+    }
+    __syncthreads();
+    {
+      float mx = -kInf;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][er]);
+      float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
+      if (m != m || mx == kInf) f = __builtin_nanf("");
+      if (MODE != kKv16) f *= kCode;
+      const int e = kScaled ? (ref < -1000 ? 0 : ref) : MODE == kKvFp4 ? (ref < -1000 ? 0 : ref - 127) : 0;
+#pragma unroll
+      for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+        for (int j = 0; j < S::EC; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float g = MODE == kKvInt4 && (j & 1) ? f * 0.0625f : f;
+            s_o[wv][(128 * h + S::EC * (4 * eb + i) + j) * LDH + er] = __builtin_amdgcn_ldexpf(acc[h][j][i] * g, e);
+          }
+    }
+    __syncthreads();
+    const bool all = ua == 0 && ue == nu;
+    const int heads = min(16, a.g - ht * 16);
+    float* slot = part + (static_cast<int64_t>(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * (static_cast<int64_t>(gh) * (DP + 2));
+    for (int i = static_cast<int>(here(tid)); i < heads * DP; i += kThreads) {
+      const int hd = i / DP, d = i - hd * DP;
+      float mx = -kInf, ls = 0.0f, o = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][hd]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float mw = s_m[w][hd];
+        ls += s_l[w][hd] == 0.0f ? 0.0f : s_l[w][hd] * __builtin_amdgcn_exp2f(mw - mx);  // (nothing seen, or NaN)
+        o += s_o[w][d * LDH + hd];
+      }
+      const int hq = hk * a.g + ht * 16 + hd;
+      if (all) {
+        if (!PAD || d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = round16<DT>(ls == 0.0f ? 0.0f : o / ls);
+        if (a.lse && d == 0)
+          a.lse[static_cast<int64_t>(b) * a.Hq + hq] = ls == 0.0f ? -kInf : (mx + __builtin_amdgcn_logf(ls)) * 0.693147181f;
+      } else {
+        slot[hd * DP + d] = o;
+        if (d == 0) {
+          slot[gh * DP + hd] = mx;
+          slot[gh * (DP + 1) + hd] = ls;
+        }
+      }
+    }
+    __syncthreads();
+    first_seg = false;
+  }
+}
+
+// Joins the parts of the segments that were split, and writes the rows of empty sequences.
+// One workgroup per (sequence, query head).
+template <int DT, int DP>
+__global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, const float* __restrict__ part, int32_t nht,
+                                                               int32_t gh, int32_t grid) {
+  __shared__ int64_t s_sum[2][kWaves];
+  __shared__ float s_f[kMaxGrid + 1], s_red[kThreads], s_w[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
+  const int hk = hq / a.g, hg = hq - hk * a.g, ht = hg / 16, hd = hg - ht * 16;
+  const int per_b = a.c.Hkv * nht, D = a.c.D;
+  uint16_t* out = a.out.p + b * a.out.row + hq * a.out.head;
+  const int32_t n = length_of(a, b);
+  if (n == 0) {
+    for (int d = tid; d < D; d += kThreads) out[d] = 0;
+    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
+    return;
+  }
+  int64_t sum = 0, before = 0;
+  for (int i = tid; i < a.B; i += kThreads) {
+    const int64_t k = units_of(length_of(a, i));
+    sum += k;
+    if (i < b) before += k;
+  }
+  for (int o = 1; o < 64; o <<= 1) {
+    sum += __shfl_xor(sum, o);
+    before += __shfl_xor(before, o);
+  }
+  if (lane == 0) {
+    s_sum[0][wv] = sum;
+    s_sum[1][wv] = before;
+  }
+  __syncthreads();
+  const int64_t total = (s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b;
+  before = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b;
+  const int64_t per = (total + grid - 1) / grid;
+  const int32_t nu = units_of(n);
+  const int64_t ua = before + static_cast<int64_t>(hk * nht + ht) * nu, ue = ua + nu;
+  const int i0 = static_cast<int>(ua / per), i1 = static_cast<int>((ue - 1) / per);
+  if (i0 == i1) return;  // one workgroup had it all and wrote the rows
+  // workgroup i's part is its first one unless its run began before this segment
+  auto slot = [&](int i) {
+    return part + (static_cast<int64_t>(i) * 2 + (per * i < ua ? 1 : 0)) * (static_cast<int64_t>(gh) * (DP + 2));
+  };
+  const int np = i1 - i0 + 1;
+  float mx = -kInf;
+  for (int i = tid; i < np; i += kThreads) mx = fmaxf(mx, slot(i0 + i)[gh * DP + hd]);
+  mx = wave_max(mx);
+  if (lane == 0) s_w[wv] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3]));
+  for (int i = tid; i < np; i += kThreads) {
+    const float mi = slot(i0 + i)[gh * DP + hd];
+    s_f[i] = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - mx);
+  }
+  __syncthreads();
+  constexpr int G = kThreads / DP;  // groups that share the parts
+  const int d = tid % DP, gr = tid / DP;
+  float o = 0.0f, ls = 0.0f;
+  for (int i = gr; i < np; i += G) {
+    const float* p = slot(i0 + i);
+    o += p[hd * DP + d] * s_f[i];
+    ls += p[gh * (DP + 1) + hd] * s_f[i];
+  }
+  if constexpr (G > 1) {
+    s_red[tid] = o;
+    __syncthreads();
+    for (int k = 1; k < G; ++k) o += gr == 0 ? s_red[k * DP + d] : 0.0f;
+    __syncthreads();
+    s_red[tid] = ls;
+    __syncthreads();
+    for (int k = 1; k < G; ++k) ls += gr == 0 ? s_red[k * DP + d] : 0.0f;
+  }
+  if (gr == 0 && d < D) out[d] = round16<DT>(ls == 0.0f ? 0.0f : o / ls);
+  if (a.lse && tid == 0)
+    a.lse[static_cast<int64_t>(b) * a.Hq + hq] = ls == 0.0f ? -kInf : (mx + __builtin_amdgcn_logf(ls)) * 0.693147181f;
+}
+
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+template <int MODE, int DT, int DP, bool PAD>
+hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
+  const int nht = (a.g + 15) / 16, gh = a.g < 16 ? a.g : 16;
+  const int64_t reach = static_cast<int64_t>(a.bt.width) << a.c.page_log;
+  const int64_t segments = static_cast<int64_t>(a.B) * a.c.Hkv * nht;
+  const bool single = reach <= kUnit;
+  if (single) {
+    decode_kernel<MODE, DT, DP, PAD><<<static_cast<uint32_t>(segments), kThreads, 0, s>>>(a, part, nht, gh, true);
+    return hipGetLastError();
+  }
+  constexpr int grid = 256 * Shape<MODE, DP, PAD>::per_cu;
+  decode_kernel<MODE, DT, DP, PAD><<<grid, kThreads, 0, s>>>(a, part, nht, gh, false);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  decode_join_kernel<DT, DP><<<static_cast<uint32_t>(a.B) * a.Hq, kThreads, 0, s>>>(a, part, nht, gh, grid);
+  return hipGetLastError();
+}
+
+template <int MODE, int DT>
+hipError_t by_size(const DecodeArgs& a, float* part, hipStream_t s) {
+  switch (a.c.D) {
+    case 64: return go<MODE, DT, 64, false>(a, part, s);
+    case 128: return go<MODE, DT, 128, false>(a, part, s);
+    case 256: return go<MODE, DT, 256, false>(a, part, s);
+    default: break;
+  }
+  switch (padded(a.c.D)) {
+    case 64: return go<MODE, DT, 64, true>(a, part, s);
+    case 128: return go<MODE, DT, 128, true>(a, part, s);
+    default: return go<MODE, DT, 256, true>(a, part, s);
+  }
+}
+
+template <int MODE>
+hipError_t by_dtype(const DecodeArgs& a, float* part, hipStream_t s) {
+  return a.c.dtype == kF16 ? by_size<MODE, kF16>(a, part, s) : by_size<MODE, kBF16>(a, part, s);
+}
+
+}  // namespace
+
+uint64_t attn_decode_workspace(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t max_tokens) {
+  if (B == 0 || max_tokens <= kUnit) return 0;
+  const int g = Hq / Hkv, gh = g < 16 ? g : 16;
+  return static_cast<uint64_t>(kMaxGrid) * 2 * gh * (padded(D) + 2) * sizeof(float);
+}
+
+hipError_t launch_attn_decode(const DecodeArgs& a, void* ws, hipStream_t s) {
+  float* part = static_cast<float*>(ws);
+  switch (a.c.mode) {
+    case kKv16: return by_dtype<kKv16>(a, part, s);
+    case kKvInt8: return by_dtype<kKvInt8>(a, part, s);
+    case kKvE4M3: return by_dtype<kKvE4M3>(a, part, s);
+    case kKvInt4: return by_dtype<kKvInt4>(a, part, s);
+    default: return by_dtype<kKvFp4>(a, part, s);
+  }
+}
+
+}  // namespace fq

@@ -88,7 +88,7 @@ fq_status side_of(const fq_tensor* codes, const fq_tensor* scale, bool first, Kv
   sd->scale = nullptr;
   sd->scale_page_b = 0;
   if (mode == kKv16) return FQ_SUCCESS;
-  if (!strides_ok(*scale) || !aligned(scale->data, 4)) return FQ_ERR_PARAM_INVALID;
+  if (!strides_ok(*scale) || !aligned(scale->data, 16)) return FQ_ERR_PARAM_INVALID;
   int64_t eb;
   if (mode == kKvFp4) {
     if (scale->dtype != FQ_DT_FLOAT8_E8M0 || scale->ndim != 4 || scale->shape[0] != pages || scale->shape[1] != H ||
@@ -100,7 +100,7 @@ fq_status side_of(const fq_tensor* codes, const fq_tensor* scale, bool first, Kv
     eb = 4;
   }
   const int64_t sstride0 = pages == 1 ? 0 : scale->strides[0];
-  if (!inner_contiguous(*scale) || sstride0 * eb % 4 != 0 || sstride0 >= lim) return FQ_ERR_PARAM_INVALID;
+  if (!inner_contiguous(*scale) || sstride0 * eb % 16 != 0 || sstride0 >= lim) return FQ_ERR_PARAM_INVALID;
   sd->scale = static_cast<uint8_t*>(scale->data);
   sd->scale_page_b = sstride0 * eb;
   return FQ_SUCCESS;

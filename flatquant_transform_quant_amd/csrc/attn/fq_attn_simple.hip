@@ -65,24 +65,6 @@ __device__ __forceinline__ void attend(const uint16_t* q, uint16_t* out, float* 
   if (lse && lane == 0) *lse = l == 0.0f ? -__builtin_inff() : m + __logf(l);
 }
 
-template <int MODE, int DT>
-__global__ __launch_bounds__(64) void decode_simple_kernel(DecodeArgs a) {
-  const int b = blockIdx.y, h = blockIdx.x, hk = h / a.g;
-  const KvCache& c = a.c;
-  const int64_t reach = min(static_cast<int64_t>(a.bt.width) << c.page_log, static_cast<int64_t>(INT32_MAX));
-  const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(a.lengths[b]), reach)));
-  attend<MODE, DT>(a.q.p + b * a.q.row + h * a.q.head, a.out.p + b * a.out.row + h * a.out.head,
-                   a.lse ? a.lse + static_cast<int64_t>(b) * a.Hq + h : nullptr, c.D, n, a.scale,
-                   [&](int side, int t, const uint8_t*& p, const uint8_t*& s) {
-                     const int32_t page = kv_page(a.bt, b, t, c.page_log, c.pages);
-                     if (page < 0) return;
-                     const KvSide& sd = side ? c.v : c.k;
-                     const int64_t r = (static_cast<int64_t>(hk) << c.page_log) + (t & ((1 << c.page_log) - 1));
-                     p = sd.codes + page * sd.page_b + r * kv_row_bytes(MODE, c.D);
-                     s = sd.scale + page * sd.scale_page_b + r * kv_scale_bytes(MODE, c.D);
-                   });
-}
-
 template <int DT>
 __global__ __launch_bounds__(64) void prefill_simple_kernel(PrefillArgs a) {
   const int t = blockIdx.y, h = blockIdx.x, hk = h / a.g;
@@ -104,27 +86,6 @@ __global__ __launch_bounds__(64) void prefill_simple_kernel(PrefillArgs a) {
 }
 
 }  // namespace
-
-uint64_t attn_decode_workspace(int32_t, int32_t, int32_t, int32_t, int64_t) { return 0; }
-
-hipError_t launch_attn_decode(const DecodeArgs& a, void*, hipStream_t s) {
-  const dim3 grid(a.Hq, a.B);
-  auto go = [&](auto m) {
-    if (a.c.dtype == kF16)
-      decode_simple_kernel<decltype(m)::value, kF16><<<grid, 64, 0, s>>>(a);
-    else
-      decode_simple_kernel<decltype(m)::value, kBF16><<<grid, 64, 0, s>>>(a);
-  };
-  using std::integral_constant;
-  switch (a.c.mode) {
-    case kKv16: go(integral_constant<int, kKv16>{}); break;
-    case kKvInt8: go(integral_constant<int, kKvInt8>{}); break;
-    case kKvE4M3: go(integral_constant<int, kKvE4M3>{}); break;
-    case kKvInt4: go(integral_constant<int, kKvInt4>{}); break;
-    default: go(integral_constant<int, kKvFp4>{}); break;
-  }
-  return hipGetLastError();
-}
 
 hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t s) {
   const dim3 grid(a.Hq, a.Tq);

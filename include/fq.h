@@ -253,9 +253,9 @@ fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tens
  * all-zero row (group) gets scale 0 and codes 0.  A row (group) that holds an infinity or NaN
  * reads back as NaN throughout: its scale is stored non-finite (e8m0 0xFF).
  * Every dimension but the first must be contiguous; the first may have any stride that is a
- * multiple of 16 bytes (of 4 bytes for the scales), so one allocation can interleave the two
- * sides.  Codes 16-byte aligned, scales 4-byte aligned.  Token t of a sequence lies in page
- * block_table[sequence, t / P] at offset t % P.  All tensors are device memory owned by the
+ * multiple of 16 bytes, so one allocation can interleave the two sides.  Codes and scales
+ * 16-byte aligned.  Token t of a sequence lies in page block_table[sequence, t / P] at offset
+ * t % P.  All tensors are device memory owned by the
  * caller, valid until the work completes on the stream; all calls enqueue on `stream` without
  * synchronizing, allocate nothing, may be captured in a graph, and read slots, block tables and
  * lengths on the device, where every index is checked: one outside the cache is never followed.
