@@ -275,6 +275,10 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
       !rows_ok(*k, Tk, Hkv, D, q->dtype, &a.k) || !rows_ok(*v, Tk, Hkv, D, q->dtype, &a.v) || !i32_vec(*cu_q, B + 1) ||
       !i32_vec(*cu_k, B + 1) || !lse_ok(lse, Tq, Hq))
     return FQ_ERR_PARAM_INVALID;
+  // a tile of 64 key rows within 31-bit offsets; the grid (a workgroup per 128 rows and head) within 31 bits
+  if ((Tk > 1 && (k->strides[0] > (int64_t(1) << 23) || v->strides[0] > (int64_t(1) << 23))) ||
+      (Tq / 128 + B) * Hq >= (int64_t(1) << 31))
+    return FQ_ERR_PARAM_INVALID;
   if (Tq == 0) return FQ_SUCCESS;
   if (!device_is_gfx950()) return fail_runtime("the current device is not gfx950", hipSuccess);
   a.lse = lse ? static_cast<float*>(lse->data) : nullptr;

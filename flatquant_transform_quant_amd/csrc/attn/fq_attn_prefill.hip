@@ -1,0 +1,337 @@
+// Attention over packed prompts: for every query row i of a sequence and query head h,
+//     o = sum_j p_j v_j,  p = softmax over the visible keys j of scale * <q, k_j>
+// in one pass over the keys, with the running maximum m and sum l of the softmax in fp32.
+//
+// A workgroup of four waves takes 128 query rows of one head (32 a wave) and walks the keys in
+// tiles of 64, copied by LDS-DMA into one of two buffers while the other is used; two workgroups
+// share a CU, so that one wave's softmax runs beside another's products.  Per wave and tile,
+// v_mfma_f32_32x32x16:
+//   S^T = K Q^T: A rows are keys (16-byte LDS reads), B columns the wave's query rows, kept in
+//     registers for the whole walk.  A lane ends with 32 scores of ONE query row (l % 32; the
+//     other half of the keys is with lane l ^ 32), so the softmax needs no step between lanes
+//     but a maximum between those two, and that only when m moves.
+//   O^T = V^T P^T: the weights, rounded to 16 bits, are the B operand exactly as they lie in
+//     the accumulators (contraction slot 4 x + i of half h is key 16 g + 8 x + 4 h + i); the A
+//     operand is read from the row-major V tile by the transposing LDS read, whose runs of
+//     four keys are just those slots.
+// LDS layouts: the 16-byte piece c of tile row r sits at c ^ (r & 15) (keys) or c ^ 4 (r & 3)
+// (values); with rows of 128 bytes, where two rows share the 64 banks, at c ^ ((r >> 1) & 7) and
+// c ^ 4 ((r >> 1) & 1): both kinds of read then touch every bank once.
+// The maximum is moved only when a score passes m + 8 in base-2 units (weights then reach 2^8):
+// the accumulators are rescaled a few times a walk instead of every tile.
+// A weight of 0 times an infinite or NaN value of a hidden key in a partly masked tile is NaN.
+// The walk ignores that; if a result is not finite, the workgroup walks again, this time taking
+// such values out of the masked tiles' products and adding them to the rows that do see them.
+#include <hip/hip_runtime.h>
+
+#include "fq_attn_dev.h"
+
+namespace fq {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
+constexpr int kKeys = 64;           // keys of a tile
+constexpr float kLazy = 8.0f;
+constexpr float kInf = __builtin_inff();
+constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
+
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x16_t mfma32x32x16(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// Buffer resource over `bytes` bytes from p as scalar registers; 0 bytes: every access is out of
+// range (a load returns zeros and touches no memory).
+__device__ __forceinline__ i32x4_t rsrc4(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return i32x4_t{static_cast<int>(static_cast<uint32_t>(a)), static_cast<int>(static_cast<uint32_t>(a >> 32) & 0xFFFF),
+                 static_cast<int>(bytes), kBufferWord3};
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// One LDS-DMA load: lane l's 16 bytes at rs + voff go to LDS lds + 16 l.  (As inline assembly: the
+// compiler would wait for every such load before any LDS read.)
+__device__ __forceinline__ void dma16(uint32_t lds, uint32_t voff, i32x4_t rs) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// This wave's loads landed and its LDS reads done, then the workgroup barrier.
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+__device__ __forceinline__ float half_max(float v) {  // with lane ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Bit 15 of each half that is infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite16(uint32_t x) {
+  constexpr uint32_t e = DT == kBF16 ? 0x7F807F80u : 0x7C007C00u, one = DT == kBF16 ? 0x00800080u : 0x04000400u;
+  return ((x & e) + one) & 0x80008000u;
+}
+
+template <int DT, int DP, bool PAD>
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(PrefillArgs a) {
+  constexpr int KS = DP / 16;            // products of a score block
+  constexpr int DB = DP / 32;            // 32-row blocks of O^T
+  constexpr int kRowB = DP * 2;          // bytes of a tile row
+  constexpr int kTileB = kKeys * kRowB;  // bytes of a tile (keys or values)
+  constexpr int kPieces = DP / 8;        // 16-byte pieces of a row
+  constexpr int NL = kTileB / 1024 / kWaves;
+  __shared__ __align__(16) uint8_t lds[4 * kTileB];  // buffer b: keys at 2 b, values at 2 b + 1
+  const lds_u8* const lds_l = (const lds_u8*)lds;
+  const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
+
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hf = lane >> 5;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int D = PAD ? a.D : DP;
+
+  // ---- which rows: tile of the packed sequences (every wave scans the lengths, 64 at a time) and head
+  int head = blockIdx.x % a.Hq;
+  int rank = blockIdx.x / a.Hq;
+  // (workgroups go to the 8 XCDs in turn: neighbouring heads, which share keys, on one XCD's L2)
+  if (a.Hq % 8 == 0) head = (head % 8) * (a.Hq / 8) + head / 8;
+  int seq = -1, q0 = 0, lq = 0, tile_q = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int b = b0 + lane;
+    int s = 0, n = 0;
+    if (b < a.B) {
+      s = max(0, min(a.cu_q[b], a.Tq));
+      n = max(0, min(a.cu_q[b + 1], a.Tq) - s);
+    }
+    const int nt = (n + kRows - 1) / kRows;
+    int incl = nt;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int sum = __builtin_amdgcn_readlane(incl, 63);
+    if (rank < sum) {
+      const int w = __builtin_ctzll(__ballot(incl > rank));
+      seq = b0 + w;
+      q0 = __builtin_amdgcn_readlane(s, w);
+      lq = __builtin_amdgcn_readlane(n, w);
+      // the last rows, which see the most keys, first
+      tile_q = __builtin_amdgcn_readlane(incl, w) - 1 - rank;
+      break;
+    }
+    rank -= sum;
+  }
+  if (seq < 0) return;
+  const int k0 = __builtin_amdgcn_readfirstlane(max(0, min(a.cu_k[seq], a.Tk)));
+  const int lk = __builtin_amdgcn_readfirstlane(max(0, min(a.cu_k[seq + 1], a.Tk) - k0));
+  const int row0 = tile_q * kRows;
+  const int row = row0 + 32 * wv + col;  // this lane's query row in the sequence
+  const int off = lk - lq;               // keys ahead of the first row
+  // the last key that a row sees; of this lane, of the wave's first and last rows, of the workgroup's
+  auto last_key = [&](int r) { return a.causal ? min(off + r, lk - 1) : lk - 1; };
+  const int lim = last_key(row);
+  const int lim_first = last_key(row0 + 32 * wv), lim_last = last_key(min(row0 + 32 * wv + 31, lq - 1));
+  const int tiles = (last_key(min(row0 + kRows, lq) - 1) + kKeys) / kKeys;
+  const int hk = head / a.g;
+
+  // ---- the query rows as B operands (a negative scale goes into their sign)
+  const float c = __builtin_fabsf(a.scale) * 1.44269504f;
+  u32x4_t qf[KS];
+  {
+    const uint16_t* qp = a.q.p + (q0 + min(row, lq - 1)) * a.q.row + head * a.q.head;
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int d = 16 * ks + 8 * hf;
+      qf[ks] = u32x4_t{0u, 0u, 0u, 0u};
+      if (!PAD || d < D) qf[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
+      qf[ks] ^= u32x4_t{sign, sign, sign, sign};
+    }
+  }
+
+  // ---- LDS-DMA: load i of wave w fills the 16-byte places 64 (NL w + i) + lane of a tile
+  uint32_t koff[NL], voff[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int at = 64 * (NL * wv + i) + lane, r = at / kPieces, p = at % kPieces;
+    const int kp = p ^ (DP == 64 ? (r >> 1) & 7 : r & 15), vp = p ^ (4 * (DP == 64 ? (r >> 1) & 1 : r & 3));
+    koff[i] = !PAD || 8 * kp < D ? static_cast<uint32_t>(r * a.k.row * 2 + 16 * kp) : kOut;
+    voff[i] = !PAD || 8 * vp < D ? static_cast<uint32_t>(r * a.v.row * 2 + 16 * vp) : kOut;
+  }
+  auto dma = [&](int t, int buf) __attribute__((always_inline)) {
+    const int left = min(kKeys, lk - t * kKeys);
+    const int64_t r = k0 + static_cast<int64_t>(t) * kKeys;
+    const i32x4_t rk = rsrc4(a.k.p + (r * a.k.row + hk * a.k.head), left > 0 ? static_cast<uint32_t>((left - 1) * a.k.row + D) * 2u : 0u);
+    const i32x4_t rv = rsrc4(a.v.p + (r * a.v.row + hk * a.v.head), left > 0 ? static_cast<uint32_t>((left - 1) * a.v.row + D) * 2u : 0u);
+    const uint32_t at = lds_addr + buf * (2 * kTileB) + 1024 * NL * wv;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) dma16(at + 1024 * i, koff[i], rk);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) dma16(at + kTileB + 1024 * i, voff[i], rv);
+  };
+
+  // ---- LDS reads: keys, piece 2 ks + hf of row col (+ 32); values, runs of the transposing read
+  const uint32_t krd = col * kRowB, kx = hf ^ (DP == 64 ? (col >> 1) & 7 : col & 15);
+  const int rj = (lane & 15) >> 2;
+  const uint32_t vrd = (4 * hf + rj) * kRowB + 32 * ((lane >> 4) & 1) + 8 * (lane & 3), vx = DP == 64 ? rj >> 1 : rj;
+
+  f32x16_t acc[DB];
+  float m, l;
+  for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    m = -kInf;
+    l = 0.0f;
+    if (tiles > 0) dma(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+      const int buf = t & 1;
+      tile_barrier();
+      if (t + 1 < tiles) dma(t + 1, buf ^ 1);
+      if (t * kKeys > lim_last) continue;  // no row of this wave sees the tile
+      const lds_u8* const kt = lds_l + buf * (2 * kTileB);
+      const lds_u8* const vt = kt + kTileB;
+      f32x16_t s[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const lds_u8* const p = kt + krd + 16 * (kx ^ (2 * ks));
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          s[b] = mfma32x32x16<DT>(*(const __attribute__((address_space(3))) u32x4_t*)(p + b * 32 * kRowB), qf[ks], s[b]);
+      }
+      const bool masked = t * kKeys + kKeys - 1 > lim_first;
+      if (masked) {
+        const int left = lim - t * kKeys - 4 * hf;  // visible: place <= left
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (32 * b + 8 * (i / 4) + i % 4 > left) s[b][i] = -kInf;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+      if (__any(top * c > m + kLazy)) {
+        const float mn = fmaxf(m, half_max(top) * c);
+        const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] *= f;
+      }
+      const float ms = m == -kInf ? 0.0f : m;
+      u32x4_t pf[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g % 2) + 2 * i], c, -ms));
+          const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g % 2) + 2 * i + 1], c, -ms));
+          pf[g][i] = round16x2<DT>(x, y);
+          l += x + y;
+        }
+      auto values = [&](int d, int g, int x) __attribute__((always_inline)) {
+        const lds_u8* const p = vt + vrd + 64 * (d ^ vx) + (16 * g + 8 * x) * kRowB;
+        return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p));
+      };
+      if (careful && masked) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            const u32x2_t lo = values(d, g, 0), hi = values(d, g, 1);
+            u32x4_t v = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] &= ~((not_finite16<DT>(v[i]) >> 15) * 0xFFFFu);
+            acc[d] = mfma32x32x16<DT>(v, pf[g], acc[d]);
+          }
+        for (int j = 0; j < kKeys; ++j) {
+          if (t * kKeys + j > lim) break;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int e = 32 * d + 8 * (i / 4) + 4 * hf + i % 4;
+              const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(
+                  vt + j * kRowB + 16 * ((e / 8) ^ (4 * (DP == 64 ? (j >> 1) & 1 : j & 3))) + 2 * (e % 8));
+              if (not_finite16<DT>(v)) acc[d][i] += load16<DT>(v);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            const u32x2_t lo = values(d, g, 0), hi = values(d, g, 1);
+            acc[d] = mfma32x32x16<DT>(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf[g], acc[d]);
+          }
+      }
+    }
+    if (careful) break;
+    float odd = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) odd = __builtin_fmaf(acc[d][i], 0.0f, odd);
+    if (!__syncthreads_or(odd != odd)) break;
+  }
+
+  // ---- rows out
+  l = half_sum(l);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (row < lq) {
+    uint16_t* const out = a.out.p + (q0 + row) * a.out.row + head * a.out.head;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 32 * d + 8 * i + 4 * hf;
+        if (!PAD || e < D)
+          *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
+                                                        round16x2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+      }
+    if (a.lse && hf == 0)
+      a.lse[static_cast<int64_t>(q0 + row) * a.Hq + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+  }
+}
+
+template <int DT>
+hipError_t by_size(const PrefillArgs& a, hipStream_t s) {
+  // tiles of all sequences: at most one partial one each
+  const dim3 g(static_cast<uint32_t>((a.Tq / kRows + a.B) * a.Hq));
+  if (a.D == 64) prefill_kernel<DT, 64, false><<<g, kThreads, 0, s>>>(a);
+  else if (a.D == 128) prefill_kernel<DT, 128, false><<<g, kThreads, 0, s>>>(a);
+  else if (a.D == 256) prefill_kernel<DT, 256, false><<<g, kThreads, 0, s>>>(a);
+  else if (a.D < 64) prefill_kernel<DT, 64, true><<<g, kThreads, 0, s>>>(a);
+  else if (a.D < 128) prefill_kernel<DT, 128, true><<<g, kThreads, 0, s>>>(a);
+  else prefill_kernel<DT, 256, true><<<g, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t s) {
+  return a.dtype == kF16 ? by_size<kF16>(a, s) : by_size<kBF16>(a, s);
+}
+
+}  // namespace fq

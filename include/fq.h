@@ -315,6 +315,8 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
  * of a sequence sees its keys 0 .. (Lk - Lq) + i: the queries are the sequence's last rows, so
  * a prompt's chunk attends to the part before it (read back with fq_kv_read) and to itself.
  * With causal == 0 it sees all Lk.  A row that sees no key gives zeros and lse = -infinity.
+ * Infinities and NaN in keys and values reach only the rows that see them.  The row strides of
+ * k and v are at most 2^23 elements.
  * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536.  Rows of
  * out past cu_q[B] are not written. */
 fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tensor* v, const fq_tensor* cu_q,
