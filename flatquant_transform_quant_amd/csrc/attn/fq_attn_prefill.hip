@@ -32,6 +32,7 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
+constexpr int kAhead = 6;           // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
@@ -190,7 +191,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
 
   f32x16_t acc[DB];
   float m, l;
-  for (int careful = 0; careful < 2; ++careful) {
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -205,18 +207,38 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
       if (t * kKeys > lim_last) continue;  // no row of this wave sees the tile
       const lds_u8* const kt = lds_l + buf * (2 * kTileB);
       const lds_u8* const vt = kt + kTileB;
+      // Fragments are read kAhead products before their use, the first of the values before the
+      // softmax; the scheduling barriers keep the compiler from moving each read to its use.
+      auto key = [&](int ks, int b) __attribute__((always_inline)) {
+        return *(const __attribute__((address_space(3))) u32x4_t*)(kt + krd + 16 * (kx ^ (2 * ks)) + b * 32 * kRowB);
+      };
+      auto value = [&](int d, int g) __attribute__((always_inline)) {
+        const lds_u8* const p = vt + vrd + 64 * (d ^ vx) + 16 * g * kRowB;
+        const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p));
+        const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 8 * kRowB)));
+        return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+      };
       f32x16_t s[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+      {
+        u32x4_t kf[2 * KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const lds_u8* const p = kt + krd + 16 * (kx ^ (2 * ks));
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          s[b] = mfma32x32x16<DT>(*(const __attribute__((address_space(3))) u32x4_t*)(p + b * 32 * kRowB), qf[ks], s[b]);
+        for (int i = 0; i < kAhead; ++i) kf[i] = key(i / 2, i % 2);
+        static_for<0, 2 * KS>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          if constexpr (i + kAhead < 2 * KS) kf[i + kAhead] = key((i + kAhead) / 2, (i + kAhead) % 2);
+          __builtin_amdgcn_sched_barrier(0);
+          s[i % 2] = mfma32x32x16<DT>(kf[i], qf[i / 2], s[i % 2]);
+          __builtin_amdgcn_sched_barrier(0);
+        });
       }
+      u32x4_t vf[4 * DB];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) vf[i] = value(i % DB, i / DB);
+      __builtin_amdgcn_sched_barrier(0);
       const bool masked = t * kKeys + kKeys - 1 > lim_first;
       if (masked) {
         const int left = lim - t * kKeys - 4 * hf;  // visible: place <= left
@@ -250,22 +272,21 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
           pf[g][i] = round16x2<DT>(x, y);
           l += x + y;
         }
-      auto values = [&](int d, int g, int x) __attribute__((always_inline)) {
-        const lds_u8* const p = vt + vrd + 64 * (d ^ vx) + (16 * g + 8 * x) * kRowB;
-        return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p));
-      };
-      if (careful && masked) {
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<0, 4 * DB>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i + kAhead < 4 * DB) vf[i + kAhead] = value((i + kAhead) % DB, (i + kAhead) / DB);
+        if constexpr (CAREFUL) {
+          if (masked)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int d = 0; d < DB; ++d) {
-            const u32x2_t lo = values(d, g, 0), hi = values(d, g, 1);
-            u32x4_t v = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] &= ~((not_finite16<DT>(v[i]) >> 15) * 0xFFFFu);
-            acc[d] = mfma32x32x16<DT>(v, pf[g], acc[d]);
-          }
-        for (int j = 0; j < kKeys; ++j) {
+            for (int j = 0; j < 4; ++j) vf[i][j] &= ~((not_finite16<DT>(vf[i][j]) >> 15) * 0xFFFFu);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        acc[i % DB] = mfma32x32x16<DT>(vf[i], pf[i / DB], acc[i % DB]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (CAREFUL) {
+        for (int j = 0; masked && j < kKeys; ++j) {
           if (t * kKeys + j > lim) break;
 #pragma unroll
           for (int d = 0; d < DB; ++d)
@@ -277,23 +298,17 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
               if (not_finite16<DT>(v)) acc[d][i] += load16<DT>(v);
             }
         }
-      } else {
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int d = 0; d < DB; ++d) {
-            const u32x2_t lo = values(d, g, 0), hi = values(d, g, 1);
-            acc[d] = mfma32x32x16<DT>(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf[g], acc[d]);
-          }
       }
     }
-    if (careful) break;
+  };
+  walk(std::false_type{});
+  {
     float odd = 0.0f;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) odd = __builtin_fmaf(acc[d][i], 0.0f, odd);
-    if (!__syncthreads_or(odd != odd)) break;
+    if (__syncthreads_or(odd != odd)) walk(std::true_type{});
   }
 
   // ---- rows out
