@@ -102,8 +102,10 @@ def _load():
     L.fq_kv_read.argtypes = [vp] * 9
     L.fq_attn_decode_get_workspace_size.argtypes = [vp, vp, vp, ctypes.POINTER(u64)]
     L.fq_attn_decode.argtypes = [vp] * 7 + [dbl, vp, vp, vp, u64, vp]
-    L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp]
-    for f in (L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode, L.fq_attn_prefill):
+    L.fq_attn_prefill_get_workspace_size.argtypes = [vp, vp, vp, ctypes.c_int32, ctypes.POINTER(u64)]
+    L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
+    for f in (L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
+              L.fq_attn_prefill_get_workspace_size, L.fq_attn_prefill):
         f.restype = ctypes.c_int32
     return L
 
@@ -112,7 +114,8 @@ lib = _load()
 EXPORTS = ("fq_get_workspace_size", "fq_run", "fq_executor_destroy", "fq_executor_set_repeatable",
            "fq_executor_set_kernel", "fq_executor_kernel", "fq_status_string", "fq_last_error", "fq_dequant",
            "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc", "fq_kv_write", "fq_kv_read",
-           "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill")
+           "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill_get_workspace_size",
+           "fq_attn_prefill")
 NO_ALLOC_SCRATCH_BYTES = 64 << 20  # FQ_NO_ALLOC_SCRATCH_BYTES of include/fq.h
 
 
@@ -605,23 +608,43 @@ def attn_decode_workspace_size(q, cache: KVCache, block_table) -> int:
     return size.value
 
 
-def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0.0, out=None, lse=None, stream=None):
+def attn_prefill_workspace_size(q, k, cu_q, causal: bool = True) -> int:
+    size = ctypes.c_uint64(0)
+    qd, kd, ad = _desc(q), _desc(k), _desc(cu_q)
+    st = lib.fq_attn_prefill_get_workspace_size(qd.ptr, kd.ptr, ad.ptr, 1 if causal else 0, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_prefill_get_workspace_size")
+    return size.value
+
+
+def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0.0, out=None, lse=None, workspace=None,
+                 stream=None):
     """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hkv, D] (one 16-bit dtype),
     sequence b in rows cu_q[b] .. cu_q[b+1]-1 of q and cu_k[b] .. cu_k[b+1]-1 of k and v (int32
     [B+1]; cu_k defaults to cu_q).  Causal: row i sees keys up to (Lk - Lq) + i.  scale 0 means
-    1/sqrt(D).  ``lse``: float32 [Tq, Hq]."""
+    1/sqrt(D).  ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least
+    attn_prefill_workspace_size) may be passed to reuse one."""
     torch = _torch()
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _record(stream, out)
     if cu_k is None:
         cu_k = cu_q
-    _same_device(q, k, v, cu_q, cu_k, out, lse)
+    _same_device(q, k, v, cu_q, cu_k, out, lse, workspace)
     qd, kd, vd, ad, bd, od = _desc(q), _desc(k), _desc(v), _desc(cu_q), _desc(cu_k), _desc(out)
     sd = _desc(lse) if lse is not None else None
+    size = ctypes.c_uint64(0)
+    st = lib.fq_attn_prefill_get_workspace_size(qd.ptr, kd.ptr, ad.ptr, 1 if causal else 0, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_prefill_get_workspace_size")
+    if size.value and workspace is None:
+        workspace = torch.empty((size.value,), dtype=torch.uint8, device=q.device)
+        _record(stream, workspace)
     with _on_device(q.device):
         st = lib.fq_attn_prefill(qd.ptr, kd.ptr, vd.ptr, ad.ptr, bd.ptr, 1 if causal else 0, scale, od.ptr,
-                                 sd.ptr if sd else None, _stream(stream, q.device).cuda_stream or None)
+                                 sd.ptr if sd else None, workspace.data_ptr() if workspace is not None else None,
+                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                 _stream(stream, q.device).cuda_stream or None)
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_attn_prefill")
     return out

@@ -255,30 +255,46 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
   return err == hipSuccess ? FQ_SUCCESS : fail_runtime("decode attention kernel launch", err);
 }
 
+// The parts of a prompt call that its workspace depends on.
+static bool prefill_sizes(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q) {
+  if (q->ndim != 3 || k->ndim != 3 || cu_q->ndim != 1) return false;
+  const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  const int64_t B = cu_q->shape[0] - 1, lim = (int64_t(1) << 31) - 65536;
+  return B >= 1 && B <= 65536 && Tq >= 0 && Tk >= 0 && Tq < lim && Tk < lim && Hq >= 1 && Hq <= 65536 && Hkv >= 1 &&
+         Hkv <= 1024 && Hq % Hkv == 0 && D >= 8 && D <= 256 && D % 8 == 0 &&
+         (Tq / 128 + B) * Hq < (int64_t(1) << 28);  // workgroups (a row tile and head each), cut into up to 8 parts
+}
+
+fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t causal,
+                                             uint64_t* workspaceSize) {
+  clear_last_error();
+  if (!q || !k || !cu_q || !workspaceSize) return FQ_ERR_PARAM_NULLPTR;
+  if (!prefill_sizes(q, k, cu_q)) return FQ_ERR_PARAM_INVALID;
+  *workspaceSize = attn_prefill_workspace(q->shape[0], k->shape[0], cu_q->shape[0] - 1, q->shape[1], q->shape[2], causal != 0);
+  return FQ_SUCCESS;
+}
+
 fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tensor* v, const fq_tensor* cu_q,
                           const fq_tensor* cu_k, int32_t causal, double scale, const fq_tensor* out,
-                          const fq_tensor* lse, hipStream_t stream) {
+                          const fq_tensor* lse, void* workspace, uint64_t workspaceSize, hipStream_t stream) {
   clear_last_error();
   for (const fq_tensor* t : {q, k, v, cu_q, cu_k, out})
     if (missing(t)) return FQ_ERR_PARAM_NULLPTR;
   if (lse && missing(lse)) return FQ_ERR_PARAM_NULLPTR;
-  if (q->ndim != 3 || k->ndim != 3 || cu_q->ndim != 1 || row_dtype(q->dtype) == 0 || !std::isfinite(scale) ||
-      !std::isfinite(static_cast<float>(scale)))
+  if (!prefill_sizes(q, k, cu_q) || row_dtype(q->dtype) == 0 || !std::isfinite(scale) || !std::isfinite(static_cast<float>(scale)))
     return FQ_ERR_PARAM_INVALID;
   const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
   const int64_t B = cu_q->shape[0] - 1;
-  if (B < 1 || B > 65536 || Tq < 0 || Tk < 0 || Tq >= (int64_t(1) << 31) - 65536 || Tk >= (int64_t(1) << 31) - 65536 ||
-      Hq < 1 || Hq > 65536 || Hkv < 1 || Hkv > 1024 || Hq % Hkv != 0 || D < 8 || D > 256 || D % 8 != 0)
-    return FQ_ERR_PARAM_INVALID;
   PrefillArgs a;
   if (!rows_ok(*q, Tq, Hq, D, q->dtype, &a.q) || !rows_ok(*out, Tq, Hq, D, q->dtype, &a.out) ||
       !rows_ok(*k, Tk, Hkv, D, q->dtype, &a.k) || !rows_ok(*v, Tk, Hkv, D, q->dtype, &a.v) || !i32_vec(*cu_q, B + 1) ||
       !i32_vec(*cu_k, B + 1) || !lse_ok(lse, Tq, Hq))
     return FQ_ERR_PARAM_INVALID;
-  // a tile of 64 key rows within 31-bit offsets; the grid (a workgroup per 128 rows and head) within 31 bits
-  if ((Tk > 1 && (k->strides[0] > (int64_t(1) << 23) || v->strides[0] > (int64_t(1) << 23))) ||
-      (Tq / 128 + B) * Hq >= (int64_t(1) << 31))
-    return FQ_ERR_PARAM_INVALID;
+  // a tile of 64 key rows within 31-bit offsets
+  if (Tk > 1 && (k->strides[0] > (int64_t(1) << 23) || v->strides[0] > (int64_t(1) << 23))) return FQ_ERR_PARAM_INVALID;
+  const uint64_t need = attn_prefill_workspace(Tq, Tk, B, Hq, D, causal != 0);
+  if (need > 0 && !workspace) return FQ_ERR_PARAM_NULLPTR;
+  if (workspaceSize < need || (need > 0 && !aligned(workspace, 16))) return FQ_ERR_PARAM_INVALID;
   if (Tq == 0) return FQ_SUCCESS;
   if (!device_is_gfx950()) return fail_runtime("the current device is not gfx950", hipSuccess);
   a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
@@ -293,7 +309,7 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
   a.dtype = row_dtype(q->dtype);
   a.causal = causal ? 1 : 0;
   a.scale = scale == 0.0 ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(scale);
-  const hipError_t err = launch_attn_prefill(a, stream);
+  const hipError_t err = launch_attn_prefill(a, workspace, stream);
   return err == hipSuccess ? FQ_SUCCESS : fail_runtime("prompt attention kernel launch", err);
 }
 

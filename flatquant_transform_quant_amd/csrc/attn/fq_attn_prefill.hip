@@ -19,10 +19,14 @@
 // c ^ 4 ((r >> 1) & 1): both kinds of read then touch every bank once.
 // The maximum is moved only when a score passes m + 8 in base-2 units (weights then reach 2^8):
 // the accumulators are rescaled a few times a walk instead of every tile.
+// Tiles of all sequences are handed out longest walk first; where they do not fill the device, the
+// long walks are cut into parts whose sums a second launch joins.
 // A weight of 0 times an infinite or NaN value of a hidden key in a partly masked tile is NaN.
 // The walk ignores that; if a result is not finite, the workgroup walks again, this time taking
 // such values out of the masked tiles' products and adding them to the rows that do see them.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "fq_attn_dev.h"
 
@@ -32,7 +36,8 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
-constexpr int kAhead = 6;           // fragments read ahead of their products
+constexpr int kAhead = 4;           // fragments read ahead of their products
+constexpr int kMaxParts = 8, kMinChunk = 16, kEnough = 512;  // see parts_of()
 constexpr float kLazy = 8.0f;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
@@ -87,8 +92,108 @@ __device__ __forceinline__ uint32_t not_finite16(uint32_t x) {
   return ((x & e) + one) & 0x80008000u;
 }
 
+// Inclusive sum over the lanes before and at each lane (DPP row shifts, then the rows' last lanes).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+// the largest over the wave
+__device__ __forceinline__ int wave_top(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x112, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x114, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x118, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
+
+// The 128 query rows and the head that workgroup number `id` works on.
+struct Place {
+  int seq;       // -1: none left for this workgroup
+  int tile;      // tile of the sequence
+  int q0, lq;    // its query rows
+  int k0, lk;    // its key rows
+  int head;
+  int chunk;     // key tiles of a part, where the walk is split (the longest walk over `parts`)
+};
+
+// the last key that query row r of a sequence sees
+__device__ __forceinline__ int last_key(const PrefillArgs& a, int off, int lk, int r) { return a.causal ? min(off + r, lk - 1) : lk - 1; }
+__device__ __forceinline__ int key_tiles(const PrefillArgs& a, int off, int lk, int lq, int tile) {
+  return max(0, (last_key(a, off, lk, min((tile + 1) * kRows, lq) - 1) + kKeys) / kKeys);
+}
+
+// Tiles are handed out longest walk first, over all sequences: a tile's level is the number of
+// whole 128-key blocks before its last row's key, every sequence has at most one tile of a level,
+// so the level of the rank-th tile is found by bisection on the number of tiles at or above a
+// level.  More than 64 sequences, or no causal mask: sequence by sequence, last tile first.
+__device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int parts) {
+  const int lane = threadIdx.x & 63;
+  Place p;
+  p.head = id % a.Hq;
+  int rank = id / a.Hq;
+  // (workgroups go to the 8 XCDs in turn: neighbouring heads, which share keys, on one XCD's L2)
+  if (a.Hq % 8 == 0) p.head = (p.head % 8) * (a.Hq / 8) + p.head / 8;
+  p.seq = -1;
+  p.tile = p.q0 = p.lq = 0;
+  p.chunk = 1 << 30;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int b = b0 + lane;
+    int s = 0, n = 0, ks = 0, kn = 0;
+    if (b < a.B) {
+      s = max(0, min(a.cu_q[b], a.Tq));
+      n = max(0, min(a.cu_q[b + 1], a.Tq) - s);
+      ks = max(0, min(a.cu_k[b], a.Tk));
+      kn = max(0, min(a.cu_k[b + 1], a.Tk) - ks);
+    }
+    const int nt = (n + kRows - 1) / kRows;
+    int w;
+    if (a.causal && a.B <= 64) {
+      const int total = wave_total(nt);
+      if (rank >= total) return p;
+      const int first = max(0, kn - n + kRows - 1) / kRows;  // level of the sequence's tile 0 (0 where no key is ahead)
+      auto above = [&](int level) { return max(0, min(nt, first + nt - level)); };  // this sequence's tiles at or above
+      int lo = 0, hi = 1 << 24;  // tiles at or above lo: more than rank; at or above hi: not
+      hi = wave_top(first + nt);
+      if (parts > 1) p.chunk = max(kMinChunk, (wave_top(nt > 0 ? key_tiles(a, kn - n, kn, n, nt - 1) : 0) + parts - 1) / parts);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (wave_total(above(mid)) > rank) lo = mid; else hi = mid;
+      }
+      const int in = rank - wave_total(above(lo + 1));  // the in-th sequence with a tile of level lo
+      // (level 0 can hold several tiles of a sequence: those that see no key before the prefix)
+      const int here = above(lo) - above(lo + 1), incl = wave_scan(here);
+      w = __builtin_ctzll(__ballot(incl > in));
+      const int t = max(0, lo - first) + (incl - 1 - in);
+      p.tile = __builtin_amdgcn_readlane(t, w);
+    } else {
+      const int incl = wave_scan(nt), sum = __builtin_amdgcn_readlane(incl, 63);
+      if (rank >= sum) {
+        rank -= sum;
+        continue;
+      }
+      w = __builtin_ctzll(__ballot(incl > rank));
+      p.tile = __builtin_amdgcn_readlane(incl, w) - 1 - rank;
+    }
+    p.seq = b0 + w;
+    p.q0 = __builtin_amdgcn_readlane(s, w);
+    p.lq = __builtin_amdgcn_readlane(n, w);
+    p.k0 = __builtin_amdgcn_readlane(ks, w);
+    p.lk = __builtin_amdgcn_readlane(kn, w);
+    return p;
+  }
+  return p;
+}
+
 template <int DT, int DP, bool PAD>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(PrefillArgs a) {
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(PrefillArgs a, int parts, float* __restrict__ ws) {
   constexpr int KS = DP / 16;            // products of a score block
   constexpr int DB = DP / 32;            // 32-row blocks of O^T
   constexpr int kRowB = DP * 2;          // bytes of a tile row
@@ -103,65 +208,22 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int D = PAD ? a.D : DP;
 
-  // ---- which rows: tile of the packed sequences (every wave scans the lengths, 64 at a time) and head
-  int head = blockIdx.x % a.Hq;
-  int rank = blockIdx.x / a.Hq;
-  // (workgroups go to the 8 XCDs in turn: neighbouring heads, which share keys, on one XCD's L2)
-  if (a.Hq % 8 == 0) head = (head % 8) * (a.Hq / 8) + head / 8;
-  int seq = -1, q0 = 0, lq = 0, tile_q = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int b = b0 + lane;
-    int s = 0, n = 0;
-    if (b < a.B) {
-      s = max(0, min(a.cu_q[b], a.Tq));
-      n = max(0, min(a.cu_q[b + 1], a.Tq) - s);
-    }
-    const int nt = (n + kRows - 1) / kRows;
-    int incl = nt;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(incl, o);
-      if (lane >= o) incl += t;
-    }
-    const int sum = __builtin_amdgcn_readlane(incl, 63);
-    if (rank < sum) {
-      const int w = __builtin_ctzll(__ballot(incl > rank));
-      seq = b0 + w;
-      q0 = __builtin_amdgcn_readlane(s, w);
-      lq = __builtin_amdgcn_readlane(n, w);
-      // the last rows, which see the most keys, first
-      tile_q = __builtin_amdgcn_readlane(incl, w) - 1 - rank;
-      break;
-    }
-    rank -= sum;
-  }
-  if (seq < 0) return;
-  const int k0 = __builtin_amdgcn_readfirstlane(max(0, min(a.cu_k[seq], a.Tk)));
-  const int lk = __builtin_amdgcn_readfirstlane(max(0, min(a.cu_k[seq + 1], a.Tk) - k0));
-  const int row0 = tile_q * kRows;
+  // ---- which rows, and which part of their walk
+  const int part = parts > 1 ? static_cast<int>(blockIdx.x / a.Hq) % parts : 0;
+  const Place pl = place_of(a, parts > 1 ? static_cast<int>(blockIdx.x % a.Hq + blockIdx.x / (a.Hq * parts) * a.Hq) : blockIdx.x, parts);
+  if (pl.seq < 0) return;
+  const int head = pl.head, q0 = pl.q0, lq = pl.lq, k0 = pl.k0, lk = pl.lk;
+  const int row0 = pl.tile * kRows;
   const int row = row0 + 32 * wv + col;  // this lane's query row in the sequence
   const int off = lk - lq;               // keys ahead of the first row
-  // the last key that a row sees; of this lane, of the wave's first and last rows, of the workgroup's
-  auto last_key = [&](int r) { return a.causal ? min(off + r, lk - 1) : lk - 1; };
-  const int lim = last_key(row);
-  const int lim_first = last_key(row0 + 32 * wv), lim_last = last_key(min(row0 + 32 * wv + 31, lq - 1));
-  const int tiles = (last_key(min(row0 + kRows, lq) - 1) + kKeys) / kKeys;
+  // the last key that this lane's row, the wave's first and last rows see; the walk's tiles
+  const int lim = last_key(a, off, lk, row);
+  const int lim_first = last_key(a, off, lk, row0 + 32 * wv), lim_last = last_key(a, off, lk, min(row0 + 32 * wv + 31, lq - 1));
+  const int all_tiles = key_tiles(a, off, lk, lq, pl.tile);
+  const bool split = all_tiles > pl.chunk;
+  const int t_first = split ? part * pl.chunk : 0, t_end = split ? min(all_tiles, t_first + pl.chunk) : all_tiles;
+  if (part > 0 && (!split || t_first >= t_end)) return;
   const int hk = head / a.g;
-
-  // ---- the query rows as B operands (a negative scale goes into their sign)
-  const float c = __builtin_fabsf(a.scale) * 1.44269504f;
-  u32x4_t qf[KS];
-  {
-    const uint16_t* qp = a.q.p + (q0 + min(row, lq - 1)) * a.q.row + head * a.q.head;
-    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int d = 16 * ks + 8 * hf;
-      qf[ks] = u32x4_t{0u, 0u, 0u, 0u};
-      if (!PAD || d < D) qf[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
-      qf[ks] ^= u32x4_t{sign, sign, sign, sign};
-    }
-  }
 
   // ---- LDS-DMA: load i of wave w fills the 16-byte places 64 (NL w + i) + lane of a tile
   uint32_t koff[NL], voff[NL];
@@ -184,6 +246,24 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
     for (int i = 0; i < NL; ++i) dma16(at + kTileB + 1024 * i, voff[i], rv);
   };
 
+  // (the first tile is on its way before the query rows are waited for)
+  if (t_first < t_end) dma(t_first, t_first & 1);
+
+  // ---- the query rows as B operands (a negative scale goes into their sign)
+  const float c = __builtin_fabsf(a.scale) * 1.44269504f;
+  u32x4_t qf[KS];
+  {
+    const uint16_t* qp = a.q.p + (q0 + min(row, lq - 1)) * a.q.row + head * a.q.head;
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int d = 16 * ks + 8 * hf;
+      qf[ks] = u32x4_t{0u, 0u, 0u, 0u};
+      if (!PAD || d < D) qf[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
+      qf[ks] ^= u32x4_t{sign, sign, sign, sign};
+    }
+  }
+
   // ---- LDS reads: keys, piece 2 ks + hf of row col (+ 32); values, runs of the transposing read
   const uint32_t krd = col * kRowB, kx = hf ^ (DP == 64 ? (col >> 1) & 7 : col & 15);
   const int rj = (lane & 15) >> 2;
@@ -199,11 +279,11 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
       for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     m = -kInf;
     l = 0.0f;
-    if (tiles > 0) dma(0, 0);
-    for (int t = 0; t < tiles; ++t) {
+    if (CAREFUL && t_first < t_end) dma(t_first, t_first & 1);
+    for (int t = t_first; t < t_end; ++t) {
       const int buf = t & 1;
       tile_barrier();
-      if (t + 1 < tiles) dma(t + 1, buf ^ 1);
+      if (t + 1 < t_end) dma(t + 1, buf ^ 1);
       if (t * kKeys > lim_last) continue;  // no row of this wave sees the tile
       const lds_u8* const kt = lds_l + buf * (2 * kTileB);
       const lds_u8* const vt = kt + kTileB;
@@ -311,42 +391,137 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
     if (__syncthreads_or(odd != odd)) walk(std::true_type{});
   }
 
-  // ---- rows out
   l = half_sum(l);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (row < lq) {
-    uint16_t* const out = a.out.p + (q0 + row) * a.out.row + head * a.out.head;
+  if (split) {  // the part's sums as they are, [element][row], with m and l
+    float* const o = ws + (static_cast<int64_t>(blockIdx.x)) * ((DP + 2) * kRows) + 32 * wv + col;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 32 * d + 8 * i + 4 * hf;
-        if (!PAD || e < D)
-          *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
-                                                        round16x2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
-      }
-    if (a.lse && hf == 0)
-      a.lse[static_cast<int64_t>(q0 + row) * a.Hq + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+      for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kRows] = acc[d][i];
+    if (hf == 0) {
+      o[DP * kRows] = m;
+      o[(DP + 1) * kRows] = l;
+    }
+    return;
+  }
+
+  // ---- rows out: through LDS (each wave its own 32 rows, pieces placed as in a key tile), so that a
+  // store instruction writes whole rows
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  __syncthreads();  // the last tile's reads are done
+  uint8_t* const mine = lds + 32 * wv * kRowB;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 32 * d + 8 * i + 4 * hf;
+      *reinterpret_cast<u32x2_t*>(mine + col * kRowB + 16 * ((e / 8) ^ (DP == 64 ? (col >> 1) & 7 : col & 15)) + 8 * hf) =
+          u32x2_t{round16x2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
+                  round16x2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+    }
+  if (a.lse && hf == 0 && row < lq)
+    a.lse[static_cast<int64_t>(q0 + row) * a.Hq + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 32 * kPieces / 64; ++i) {
+    const int at = 64 * i + lane, r = at / kPieces, p = at % kPieces;
+    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(mine + r * kRowB + 16 * (p ^ (DP == 64 ? (r >> 1) & 7 : r & 15)));
+    const int to = row0 + 32 * wv + r;
+    if (to < lq && (!PAD || 8 * p < D))
+      *reinterpret_cast<u32x4_t*>(a.out.p + (q0 + to) * a.out.row + head * a.out.head + 8 * p) = w;
   }
 }
 
-template <int DT>
-hipError_t by_size(const PrefillArgs& a, hipStream_t s) {
-  // tiles of all sequences: at most one partial one each
-  const dim3 g(static_cast<uint32_t>((a.Tq / kRows + a.B) * a.Hq));
-  if (a.D == 64) prefill_kernel<DT, 64, false><<<g, kThreads, 0, s>>>(a);
-  else if (a.D == 128) prefill_kernel<DT, 128, false><<<g, kThreads, 0, s>>>(a);
-  else if (a.D == 256) prefill_kernel<DT, 256, false><<<g, kThreads, 0, s>>>(a);
-  else if (a.D < 64) prefill_kernel<DT, 64, true><<<g, kThreads, 0, s>>>(a);
-  else if (a.D < 128) prefill_kernel<DT, 128, true><<<g, kThreads, 0, s>>>(a);
-  else prefill_kernel<DT, 256, true><<<g, kThreads, 0, s>>>(a);
+// Joins the parts of the walks that were split: a workgroup per 128 rows and head, a thread per
+// row and half of the elements.
+template <int DT, int DP>
+__global__ __launch_bounds__(kThreads) void prefill_join_kernel(PrefillArgs a, int parts, const float* __restrict__ ws) {
+  const Place pl = place_of(a, blockIdx.x, parts);
+  if (pl.seq < 0) return;
+  const int tiles = key_tiles(a, pl.lk - pl.lq, pl.lk, pl.lq, pl.tile);
+  if (tiles <= pl.chunk) return;
+  const int n = (tiles + pl.chunk - 1) / pl.chunk;
+  const int r = threadIdx.x % kRows, hf = threadIdx.x / kRows, row = pl.tile * kRows + r;
+  if (row >= pl.lq) return;
+  // part i of this workgroup's rows was number (rank parts + i) Hq + head's place of the first launch
+  const int64_t first = static_cast<int64_t>(blockIdx.x / a.Hq) * parts * a.Hq + blockIdx.x % a.Hq;
+  auto at = [&](int i) { return ws + (first + static_cast<int64_t>(i) * a.Hq) * ((DP + 2) * kRows) + r; };
+  float m = -kInf, l = 0.0f, f[kMaxParts];
+  for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[DP * kRows]);
+#pragma unroll
+  for (int i = 0; i < kMaxParts; ++i) {
+    if (i >= n) break;
+    const float mi = at(i)[DP * kRows], li = at(i)[(DP + 1) * kRows];
+    f[i] = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
+    if (li != 0.0f) l += li * f[i];  // (nothing seen, or NaN)
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* const out = a.out.p + (pl.q0 + row) * a.out.row + pl.head * a.out.head;
+  for (int e = 8 * hf; e < a.D; e += 16) {
+    float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+      if (i >= n) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf(at(i)[(e + j) * kRows], f[i], o[j]);
+    }
+    u32x4_t w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = round16x2<DT>(o[2 * j] * inv, o[2 * j + 1] * inv);
+    *reinterpret_cast<u32x4_t*>(out + e) = w;
+  }
+  if (a.lse && hf == 0)
+    a.lse[static_cast<int64_t>(pl.q0 + row) * a.Hq + pl.head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+}
+
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// workgroups of a launch that does not split: tiles of all sequences (at most one partial one each)
+int64_t workgroups(int64_t Tq, int64_t B, int64_t Hq) { return (Tq / kRows + B) * Hq; }
+
+// Parts that the longest walk may be cut into.  The device runs 512 workgroups at a time (two a CU);
+// with fewer, the longest walk alone is the whole time.  128 rows behind 32768 keys, 32 heads (64
+// workgroups): 546 us in one part, 125 in 8; 512 behind 16384, 64 heads (320): 315 against 281.  A
+// part's sums go through memory (66 KB at 128), so nothing is split once the device is full: chunks
+// of 313 to 1024 rows behind up to 8192 keys, 32 heads (736): 204 whole, 227 in two parts, 261 in
+// three.  Nor is a walk of 16 tiles, which takes as long as a join: 1024 rows, 8 heads 23 and 28 us.
+int parts_of(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, bool causal) {
+  const int64_t w = workgroups(Tq, B, Hq);
+  if (!causal || B > 64 || w >= kEnough) return 1;
+  return static_cast<int>(std::min({int64_t(kMaxParts), (kEnough + w - 1) / w, std::max(int64_t(1), ceil_div(Tk, kKeys * kMinChunk))}));
+}
+
+template <int DT, int DP, bool PAD>
+hipError_t go(const PrefillArgs& a, float* ws, hipStream_t s) {
+  const int64_t w = workgroups(a.Tq, a.B, a.Hq);
+  const int parts = parts_of(a.Tq, a.Tk, a.B, a.Hq, a.causal);
+  prefill_kernel<DT, DP, PAD><<<static_cast<uint32_t>(w * parts), kThreads, 0, s>>>(a, parts, ws);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || parts == 1) return err;
+  prefill_join_kernel<DT, DP><<<static_cast<uint32_t>(w), kThreads, 0, s>>>(a, parts, ws);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t by_size(const PrefillArgs& a, float* ws, hipStream_t s) {
+  if (a.D == 64) return go<DT, 64, false>(a, ws, s);
+  if (a.D == 128) return go<DT, 128, false>(a, ws, s);
+  if (a.D == 256) return go<DT, 256, false>(a, ws, s);
+  if (a.D < 64) return go<DT, 64, true>(a, ws, s);
+  return a.D < 128 ? go<DT, 128, true>(a, ws, s) : go<DT, 256, true>(a, ws, s);
 }
 
 }  // namespace
 
-hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t s) {
-  return a.dtype == kF16 ? by_size<kF16>(a, s) : by_size<kBF16>(a, s);
+uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D, bool causal) {
+  const int parts = Tq == 0 ? 1 : parts_of(Tq, Tk, B, Hq, causal);
+  if (parts == 1) return 0;
+  return static_cast<uint64_t>(workgroups(Tq, B, Hq)) * parts * (padded(static_cast<int>(D)) + 2) * kRows * sizeof(float);
+}
+
+hipError_t launch_attn_prefill(const PrefillArgs& a, void* ws, hipStream_t s) {
+  float* const w = static_cast<float*>(ws);
+  return a.dtype == kF16 ? by_size<kF16>(a, w, s) : by_size<kBF16>(a, w, s);
 }
 
 }  // namespace fq

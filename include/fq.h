@@ -318,10 +318,14 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
  * Infinities and NaN in keys and values reach only the rows that see them.  The row strides of
  * k and v are at most 2^23 elements.
  * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536.  Rows of
- * out past cu_q[B] are not written. */
+ * out past cu_q[B] are not written.  A call with few rows over many keys splits the keys and joins
+ * the parts in `workspace` (as for fq_attn_decode, of the size that
+ * fq_attn_prefill_get_workspace_size gives for the same tensors; 0 for most calls). */
+fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t causal,
+                                             uint64_t* workspaceSize);
 fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tensor* v, const fq_tensor* cu_q,
                           const fq_tensor* cu_k, int32_t causal, double scale, const fq_tensor* out,
-                          const fq_tensor* lse, hipStream_t stream);
+                          const fq_tensor* lse, void* workspace, uint64_t workspaceSize, hipStream_t stream);
 
 /* Releases an executor that will not be run (or a repeatable one).  NULL is a no-op. */
 void fq_executor_destroy(fq_executor* executor);

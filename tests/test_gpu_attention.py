@@ -228,6 +228,22 @@ def test_prefill_long():
     _prefill([1300], [1300], 2, 2, 64, "f16", seed=5, scale=1.0)
 
 
+@pytest.mark.parametrize("lq,lk", [([40], [5000]), ([130, 1, 300, 0], [2100, 3000, 1300, 20]), ([1500], [1500])])
+def test_prefill_split_over_the_keys(lq, lk):
+    """Few rows over many keys: the walks are cut into parts and joined."""
+    for dt, D in (("bf16", 128), ("f16", 64), ("bf16", 200)):
+        q, k = torch.empty(sum(lq), 4, D, device=DEV), torch.empty(sum(lk), 2, D, device=DEV)
+        assert fq.attn_prefill_workspace_size(q, k, torch.empty(len(lq) + 1, device=DEV)) > 0
+        _prefill(lq, lk, 4, 2, D, dt, seed=6)
+
+
+def test_prefill_many_sequences():
+    """More sequences than a wave has lanes."""
+    rng = np.random.default_rng(8)
+    lens = [int(n) for n in rng.integers(0, 9, 150)] + [200, 0, 130]
+    _prefill(lens, lens, 2, 1, 64, "bf16", seed=7)
+
+
 def test_prefill_large_scores():
     """Scores whose maximum moves by hundreds between key tiles, upwards and downwards."""
     g = torch.Generator().manual_seed(3)
