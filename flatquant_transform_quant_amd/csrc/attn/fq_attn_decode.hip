@@ -178,6 +178,12 @@ __device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int32_t units_of(int32_t n) { return n / kUnit + (n % kUnit != 0); }
 
+// the same for every lane, told to the compiler
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // A segment: the tokens of one (sequence, cache head, head tile).
 struct Segment {
   int32_t b, hk, ht, n;  // n: the sequence's length
@@ -245,8 +251,8 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     }
     __syncthreads();
     b = __builtin_amdgcn_readfirstlane(s_b);
-    u = first - s_at;
-    u_end = min(first + per, total) - s_at;
+    u = uniform64(first - s_at);
+    u_end = uniform64(min(first + per, total) - s_at);
   }
 
   bool first_seg = true;
@@ -338,13 +344,15 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     // its last token (at nothing for a subtile without a page): rows past n, and the pieces of
     // padded lanes, whose offset is kOut, are zeros without a branch.
     auto rows_of = [&](int step, int s) __attribute__((always_inline)) {
-      return max(0, min(16, n - (t_first + kUnit * step + 16 * s)));
+      // (as a scalar: a clamp runs in a vector register, and a resource there costs a loop a load)
+      return __builtin_amdgcn_readfirstlane(max(0, min(16, n - (t_first + kUnit * step + 16 * s))));
     };
     auto resource = [&](const uint8_t* base, int64_t page_b, int row_b, int step, int s, int idx) __attribute__((always_inline)) {
       const int32_t pg = __builtin_amdgcn_readlane(pages, 2 * idx + s);
       const int off = (t_first + kUnit * step + 16 * s) & ((1 << c.page_log) - 1);
+      const int bytes = rows_of(step, s) * row_b;
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (max(pg, 0) * page_b + (khead + off) * row_b), static_cast<int16_t>(0),
-                                               pg < 0 ? 0 : rows_of(step, s) * row_b, kBufferWord3);
+                                               pg < 0 ? 0 : bytes, kBufferWord3);
     };
     auto load_keys = [&](Keys<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
 #pragma unroll
@@ -395,7 +403,8 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     };
     // the rows a lane's four tokens of a subtile have left (0 .. 4): for steps that are not whole
     auto mine = [&](int step, int s, int idx) __attribute__((always_inline)) {
-      return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows_of(step, s)) - 4 * kb;
+      const int rows = rows_of(step, s);
+      return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows) - 4 * kb;
     };
 
     // base-2 scores of a step
