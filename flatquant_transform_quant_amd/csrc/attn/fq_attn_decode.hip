@@ -26,6 +26,9 @@
 // value scale of a token multiplies its weight: w = p scale 2^-R rounded to f16, with R a
 // running reference exponent, so that w stays in range; a scale below 2^-24 of the largest
 // one in a sequence loses bits in proportion.
+// The weights' rounding would be most of the result's error.  With at most 8 heads in a group the
+// tile has columns to spare: they take the same heads with the remainders w - f16(w) as weights, so
+// the weights count with twice the bits and the matrix cores have no more to do.
 // Softmax statistics are fp32: the running maximum m (base-2 scores) is only moved when a score
 // passes m + 8 (weights then reach 2^8, far inside f16's range), so the common tile has no
 // cross-lane step and no rescaling.
@@ -35,6 +38,8 @@
 // only part of a segment leaves its unnormalised sums and (m, l) in the workspace, and a second
 // launch joins them in a fixed order.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "fq_attn_dev.h"
 
@@ -46,6 +51,7 @@ constexpr int kTile = 32;                    // tokens of a wave's step
 constexpr int kUnit = kWaves * kTile;        // tokens of a unit
 constexpr int kBatch = 31;                   // steps per fetch of the block table (64 subtiles cover one step more)
 constexpr int kMaxGrid = 1024;               // workgroups of a launch at most: four on each of 256 CUs
+constexpr int kHeldLengths = 512;            // lengths kept in LDS (those of later sequences are read again)
 constexpr float kLazy = 8.0f;                // base-2 slack of the running maximum
 constexpr float kInf = __builtin_inff();
 
@@ -184,10 +190,10 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// A segment: the tokens of one (sequence, cache head, head tile).
-struct Segment {
-  int32_t b, hk, ht, n;  // n: the sequence's length
-};
+// Workgroup i of `runs` (at most `total`, so that none is empty) has the units from run_start(i) up
+// to run_start(i + 1); unit u is in run run_of(u).
+__device__ __forceinline__ int64_t run_start(int64_t i, int64_t total, int64_t runs) { return i * total / runs; }
+__device__ __forceinline__ int run_of(int64_t u, int64_t total, int64_t runs) { return static_cast<int>(((u + 1) * runs - 1) / total); }
 
 template <int MODE, int DT, int DP, bool PAD>
 __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void decode_kernel(DecodeArgs a, float* __restrict__ part, int32_t nht, int32_t gh,
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   __shared__ float s_o[kWaves][DP * LDH];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ int64_t s_sum[kWaves];
-  __shared__ int32_t s_b;
+  __shared__ int32_t s_b, s_len[kHeldLengths];
   __shared__ int64_t s_at;
 
   const KvCache& c = a.c;
@@ -221,18 +227,23 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   } else {
     // total, then the sequence that holds the first unit, by scans over the lengths 256 at a time
     int64_t mine = 0;
-    for (int i = tid; i < a.B; i += kThreads) mine += units_of(length_of(a, i));
+    for (int i = tid; i < a.B; i += kThreads) {
+      const int32_t n = length_of(a, i);
+      if (i < kHeldLengths) s_len[i] = n;
+      mine += units_of(n);
+    }
     for (int o = 1; o < 64; o <<= 1) mine += __shfl_xor(mine, o);
     if (lane == 0) s_sum[wv] = mine;
     __syncthreads();
     const int64_t total = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * per_b;
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, first = per * blockIdx.x;
-    if (first >= total) return;
+    const int64_t runs = min(static_cast<int64_t>(gridDim.x), total);
+    if (blockIdx.x >= runs) return;
+    const int64_t first = run_start(blockIdx.x, total, runs), last = run_start(blockIdx.x + 1, total, runs);
     int64_t base = 0;
     for (int i0 = 0; i0 < a.B; i0 += kThreads) {
       __syncthreads();
       const int i = i0 + tid;
-      const int64_t n = i < a.B ? static_cast<int64_t>(units_of(length_of(a, i))) * per_b : 0;
+      const int64_t n = i < a.B ? static_cast<int64_t>(units_of(i < kHeldLengths ? s_len[i] : length_of(a, i))) * per_b : 0;
       int64_t incl = n;
       for (int o = 1; o < 64; o <<= 1) {
         const int64_t t = __shfl_up(incl, o);
@@ -252,13 +263,16 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     __syncthreads();
     b = __builtin_amdgcn_readfirstlane(s_b);
     u = uniform64(first - s_at);
-    u_end = uniform64(min(first + per, total) - s_at);
+    u_end = uniform64(last - s_at);
   }
 
   bool first_seg = true;
+  int32_t pages = -1;                 // lane 2 i + s: the page of subtile s of step (batch) + i
+  int pages_b = -1, pages_t = -1;     // the sequence and first token they were fetched for
+  const bool two = a.g <= 8;          // weights in two halves, see below
   while (u < u_end) {
     // ---- the next segment of the run
-    const int32_t n = __builtin_amdgcn_readfirstlane(length_of(a, b));
+    const int32_t n = __builtin_amdgcn_readfirstlane(!single && b < kHeldLengths ? s_len[b] : length_of(a, b));
     const int32_t nu = single ? 1 : units_of(n);
     if (u >= static_cast<int64_t>(nu) * per_b) {  // on to the next sequence
       u -= static_cast<int64_t>(nu) * per_b;
@@ -271,50 +285,10 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     const int ua = __builtin_amdgcn_readfirstlane(static_cast<int>(u - static_cast<int64_t>(seg) * nu));
     const int ue = static_cast<int>(min(static_cast<int64_t>(nu), ua + (u_end - u)));
     u += ue - ua;
-    const int head = ht * 16 + r16;  // this lane's head within the group
+    // This lane's head within the group.  Of at most 8 heads the tile's columns 8 .. 15 take the same
+    // heads again, with what the rounding of the weights left over: their sums are added to the others'.
+    const int head = ht * 16 + (two ? r16 & 7 : r16);
     const bool my_head = head < a.g;
-
-    // ---- q as the B operand, and the column's constants
-    u32x4_t qf[S::KS];
-    float cq = a.scale * 1.44269504f * kCode;
-    {
-      const uint16_t* qp = a.q.p + b * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
-      u32x4_t raw[S::KS];
-#pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) {
-        const int d = S::CE * (4 * (ks / (S::CE / 8)) + kb) + 8 * (ks % (S::CE / 8));
-        raw[ks] = u32x4_t{0u, 0u, 0u, 0u};
-        if (my_head && d < D) raw[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
-      }
-      if constexpr (MODE == kKv16) {
-#pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks) qf[ks] = raw[ks];
-      } else {
-        float top = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks) {
-          float x[8];
-          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(x[j]));
-        }
-        // |q| < 2^(e + 1) at its largest; brought to [2^13, 2^14)
-        const int e = static_cast<int>((__float_as_uint(column_max(top)) >> 23) & 0xFFu) - 127;
-#pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks) {
-          float x[8], y[8];
-          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[j] = __builtin_amdgcn_ldexpf(x[q_place<MODE>(j)], 13 - e);
-            if (MODE == kKvInt4 && (j & 2)) y[j] *= 0.0625f;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qf[ks][i] = h2<kF16>(y[2 * i], y[2 * i + 1]);
-        }
-        cq = __builtin_amdgcn_ldexpf(cq, e - 13);
-      }
-    }
 
     // ---- state of the segment
     f32x4_t acc[S::NH][S::EC];
@@ -332,10 +306,11 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     const int t_last = min(n, kUnit * ue);
     const int steps = t_first < t_last ? (t_last - t_first + kUnit - 1) / kUnit : 0;
 
-    int32_t pages = -1;  // lane 2 i + s: the page of subtile s of step (batch) + i
     auto fetch_pages = [&](int step) __attribute__((always_inline)) {
       const int64_t t = static_cast<int64_t>(t_first) + static_cast<int64_t>(kUnit) * (step + (lane >> 1)) + 16 * (lane & 1);
       pages = t < n ? kv_page(a.bt, b, static_cast<int32_t>(t), c.page_log, c.pages) : -1;
+      pages_b = b;
+      pages_t = t_first + kUnit * step;
     };
     const int64_t khead = static_cast<int64_t>(hk) << c.page_log;
     const uint32_t koff = r16 * rowb + kb * (S::CE * S::bits / 8), keoff = r16 * sb + (S::CE * kb) / 32;
@@ -406,6 +381,57 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       const int rows = rows_of(step, s);
       return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows) - 4 * kb;
     };
+
+    // the first step's loads are under way before q is waited for
+    Keys<MODE, DP, PAD> kx;
+    Values<MODE, DP, PAD> vx;
+    if (steps > 0) {
+      if (pages_b != b || pages_t != t_first) fetch_pages(0);
+      load_keys(kx, 0, 0);
+      load_values(vx, 0, 0);
+    }
+
+    // ---- q as the B operand, and the column's constants
+    u32x4_t qf[S::KS];
+    float cq = a.scale * 1.44269504f * kCode;
+    {
+      const uint16_t* qp = a.q.p + b * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
+      u32x4_t raw[S::KS];
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) {
+        const int d = S::CE * (4 * (ks / (S::CE / 8)) + kb) + 8 * (ks % (S::CE / 8));
+        raw[ks] = u32x4_t{0u, 0u, 0u, 0u};
+        if (my_head && d < D) raw[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
+      }
+      if constexpr (MODE == kKv16) {
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) qf[ks] = raw[ks];
+      } else {
+        float top = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+          float x[8];
+          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(x[j]));
+        }
+        // |q| < 2^(e + 1) at its largest; brought to [2^13, 2^14)
+        const int e = static_cast<int>((__float_as_uint(column_max(top)) >> 23) & 0xFFu) - 127;
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+          float x[8], y[8];
+          kv_decode8<kKv16, DT>(raw[ks], 1.0f, 0, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            y[j] = __builtin_amdgcn_ldexpf(x[q_place<MODE>(j)], 13 - e);
+            if (MODE == kKvInt4 && (j & 2)) y[j] *= 0.0625f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[ks][i] = h2<kF16>(y[2 * i], y[2 * i + 1]);
+        }
+        cq = __builtin_amdgcn_ldexpf(cq, e - 13);
+      }
+    }
 
     // base-2 scores of a step
     auto score = [&](const Keys<MODE, DP, PAD>& x, int step, int idx, bool whole, float (&s)[8]) __attribute__((always_inline)) {
@@ -510,6 +536,13 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       u32x4_t pf;
 #pragma unroll
       for (int i = 0; i < 4; ++i) pf[i] = h2<PDT>(w[2 * i], w[2 * i + 1]);
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t rest = h2<PDT>(w[2 * i] - load16<PDT>(static_cast<uint16_t>(pf[i])), w[2 * i + 1] - load16<PDT>(static_cast<uint16_t>(pf[i] >> 16)));
+          pf[i] = r16 < 8 ? pf[i] : rest;
+        }
+      }
 #pragma unroll
       for (int h = 0; h < S::NH; ++h) {
 #pragma unroll
@@ -568,13 +601,8 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     // are formed, its values as soon as this one's are added, so a wave always has one of the
     // two in flight.
     if (steps > 0) {
-      Keys<MODE, DP, PAD> kx;
-      Values<MODE, DP, PAD> vx;
       float s[8];
       int base = 0;
-      fetch_pages(0);
-      load_keys(kx, 0, 0);
-      load_values(vx, 0, 0);
       for (int i = 0; i < steps; ++i) {
         const int idx = i - base;
         const bool whole = t_first + kUnit * i + kTile <= n && __builtin_amdgcn_readlane(pages, 2 * idx) >= 0 &&
@@ -632,6 +660,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
         const float mw = s_m[w][hd];
         ls += s_l[w][hd] == 0.0f ? 0.0f : s_l[w][hd] * __builtin_amdgcn_exp2f(mw - mx);  // (nothing seen, or NaN)
         o += s_o[w][d * LDH + hd];
+        if (two) o += s_o[w][d * LDH + hd + 8];
       }
       const int hq = hk * a.g + ht * 16 + hd;
       if (all) {
@@ -651,30 +680,33 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   }
 }
 
-// Joins the parts of the segments that were split, and writes the rows of empty sequences.
-// One workgroup per (sequence, query head).
+// Joins the parts of the segments that were split, and writes the rows of empty sequences.  One
+// workgroup per segment and, with gridDim.y > 1, every gridDim.y-th of its heads.
 template <int DT, int DP>
 __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, const float* __restrict__ part, int32_t nht,
                                                                int32_t gh, int32_t grid) {
+  constexpr int G = kThreads / DP;  // threads that share an element's parts
+  constexpr int kBatch = 8;         // parts of a thread in flight
   __shared__ int64_t s_sum[2][kWaves];
-  __shared__ float s_f[kMaxGrid + 1], s_red[kThreads], s_w[kWaves];
+  __shared__ float s_m[G][DP], s_l[G][DP], s_o[G][DP];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
-  const int hk = hq / a.g, hg = hq - hk * a.g, ht = hg / 16, hd = hg - ht * 16;
   const int per_b = a.c.Hkv * nht, D = a.c.D;
-  uint16_t* out = a.out.p + b * a.out.row + hq * a.out.head;
+  const int b = blockIdx.x / per_b, seg = blockIdx.x - b * per_b, hk = seg / nht, ht = seg - hk * nht;
+  const int heads = min(16, a.g - ht * 16);
+  const int d = tid % DP, gr = tid / DP;
   const int32_t n = length_of(a, b);
-  if (n == 0) {
-    for (int d = tid; d < D; d += kThreads) out[d] = 0;
-    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
-    return;
-  }
   int64_t sum = 0, before = 0;
   for (int i = tid; i < a.B; i += kThreads) {
     const int64_t k = units_of(length_of(a, i));
     sum += k;
     if (i < b) before += k;
   }
+  for (int hd = blockIdx.y; n == 0 && hd < heads; hd += gridDim.y) {
+    const int hq = hk * a.g + ht * 16 + hd;
+    if (gr == 0 && d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = 0;
+    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
+  }
+  if (n == 0) return;
   for (int o = 1; o < 64; o <<= 1) {
     sum += __shfl_xor(sum, o);
     before += __shfl_xor(before, o);
@@ -686,47 +718,65 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   __syncthreads();
   const int64_t total = (s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b;
   before = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b;
-  const int64_t per = (total + grid - 1) / grid;
   const int32_t nu = units_of(n);
-  const int64_t ua = before + static_cast<int64_t>(hk * nht + ht) * nu, ue = ua + nu;
-  const int i0 = static_cast<int>(ua / per), i1 = static_cast<int>((ue - 1) / per);
+  const int64_t ua = before + static_cast<int64_t>(seg) * nu, ue = ua + nu;
+  const int64_t runs = min(static_cast<int64_t>(grid), total);
+  const int i0 = run_of(ua, total, runs), i1 = run_of(ue - 1, total, runs);
   if (i0 == i1) return;  // one workgroup had it all and wrote the rows
-  // workgroup i's part is its first one unless its run began before this segment
-  auto slot = [&](int i) {
-    return part + (static_cast<int64_t>(i) * 2 + (per * i < ua ? 1 : 0)) * (static_cast<int64_t>(gh) * (DP + 2));
-  };
   const int np = i1 - i0 + 1;
-  float mx = -kInf;
-  for (int i = tid; i < np; i += kThreads) mx = fmaxf(mx, slot(i0 + i)[gh * DP + hd]);
-  mx = wave_max(mx);
-  if (lane == 0) s_w[wv] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3]));
-  for (int i = tid; i < np; i += kThreads) {
-    const float mi = slot(i0 + i)[gh * DP + hd];
-    s_f[i] = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - mx);
+  const int64_t pitch = static_cast<int64_t>(gh) * (DP + 2);
+  // run i's part is its first one unless the run began before this segment (only i0 can have)
+  const float* const p0 = part + (static_cast<int64_t>(i0) * 2 + (run_start(i0, total, runs) < ua ? 1 : 0)) * pitch;
+  const float* const p1 = part + static_cast<int64_t>(i0) * 2 * pitch;  // + 2 i pitch for run i0 + i
+  for (int hd = blockIdx.y; hd < heads; hd += gridDim.y) {
+    float m = -kInf, l = 0.0f, o = 0.0f;
+    for (int k = gr; k < np; k += G * kBatch) {
+      float pm[kBatch], pl[kBatch], po[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = k + j * G;
+        const float* const p = i == 0 ? p0 : p1 + 2 * pitch * i;
+        pm[j] = i < np ? p[gh * DP + hd] : -kInf;
+        pl[j] = i < np ? p[gh * (DP + 1) + hd] : 0.0f;
+        po[j] = i < np ? p[hd * DP + d] : 0.0f;
+      }
+      float mn = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, pm[j]);
+      const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float w = pm[j] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(pm[j] - mn);
+        l += pl[j] * w;
+        o += po[j] * w;
+      }
+      m = mn;
+    }
+    if constexpr (G > 1) {
+      s_m[gr][d] = m;
+      s_l[gr][d] = l;
+      s_o[gr][d] = o;
+      __syncthreads();
+      float mn = m;
+#pragma unroll
+      for (int g = 0; g < G; ++g) mn = fmaxf(mn, s_m[g][d]);
+      l = o = 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float w = s_m[g][d] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(s_m[g][d] - mn);
+        l += s_l[g][d] * w;
+        o += s_o[g][d] * w;
+      }
+      m = mn;
+      __syncthreads();
+    }
+    const int hq = hk * a.g + ht * 16 + hd;
+    if (gr == 0 && d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = round16<DT>(l == 0.0f ? 0.0f : o / l);
+    if (a.lse && tid == 0)
+      a.lse[static_cast<int64_t>(b) * a.Hq + hq] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
   }
-  __syncthreads();
-  constexpr int G = kThreads / DP;  // groups that share the parts
-  const int d = tid % DP, gr = tid / DP;
-  float o = 0.0f, ls = 0.0f;
-  for (int i = gr; i < np; i += G) {
-    const float* p = slot(i0 + i);
-    o += p[hd * DP + d] * s_f[i];
-    ls += p[gh * (DP + 1) + hd] * s_f[i];
-  }
-  if constexpr (G > 1) {
-    s_red[tid] = o;
-    __syncthreads();
-    for (int k = 1; k < G; ++k) o += gr == 0 ? s_red[k * DP + d] : 0.0f;
-    __syncthreads();
-    s_red[tid] = ls;
-    __syncthreads();
-    for (int k = 1; k < G; ++k) ls += gr == 0 ? s_red[k * DP + d] : 0.0f;
-  }
-  if (gr == 0 && d < D) out[d] = round16<DT>(ls == 0.0f ? 0.0f : o / ls);
-  if (a.lse && tid == 0)
-    a.lse[static_cast<int64_t>(b) * a.Hq + hq] = ls == 0.0f ? -kInf : (mx + __builtin_amdgcn_logf(ls)) * 0.693147181f;
 }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -745,7 +795,9 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   decode_kernel<MODE, DT, DP, PAD><<<grid, kThreads, 0, s>>>(a, part, nht, gh, false);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  decode_join_kernel<DT, DP><<<static_cast<uint32_t>(a.B) * a.Hq, kThreads, 0, s>>>(a, part, nht, gh, grid);
+  // (enough workgroups of the join to fill the device, at most one a head)
+  const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(1024, segments)));
+  decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid);
   return hipGetLastError();
 }
 
