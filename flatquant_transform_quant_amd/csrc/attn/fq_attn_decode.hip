@@ -72,7 +72,7 @@ struct Shape {
   static constexpr int VW = VB < 4 ? 1 : VB / 4;
   static constexpr int KS = DP / 32;                                               // products of a score
   // workgroups of a CU (waves of a SIMD): what registers and, at 256, LDS hold
-  static constexpr int per_cu = DP == 256 ? (bits == 16 ? 1 : 2) : bits == 16 ? (DP == 128 ? 2 : 4) : 3;
+  static constexpr int per_cu = DP == 256 ? (bits == 16 ? 1 : 2) : DP == 64 ? 4 : bits == 4 ? 3 : 2;
 };
 
 template <int MODE, int DP, bool PAD>
@@ -184,16 +184,28 @@ __device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int32_t units_of(int32_t n) { return n / kUnit + (n % kUnit != 0); }
 
-// the same for every lane, told to the compiler
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+// Inclusive sum over the lanes up to each lane (DPP row shifts, then the rows' last lanes).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 
-// Workgroup i of `runs` (at most `total`, so that none is empty) has the units from run_start(i) up
-// to run_start(i + 1); unit u is in run run_of(u).
-__device__ __forceinline__ int64_t run_start(int64_t i, int64_t total, int64_t runs) { return i * total / runs; }
-__device__ __forceinline__ int run_of(int64_t u, int64_t total, int64_t runs) { return static_cast<int>(((u + 1) * runs - 1) / total); }
+// Workgroup i of `runs` (at most `total`, so that none is empty; all below 2^31, which the host
+// checks) has the units from start(i) = i total / runs up to start(i + 1); unit u is in run of(u).
+struct Runs {
+  uint32_t total, runs, q, r;
+  __device__ Runs(uint32_t units, uint32_t grid) : total(units), runs(min(units, grid)) {
+    q = runs ? total / runs : 0u;
+    r = total - q * runs;
+  }
+  __device__ uint32_t start(uint32_t i) const { return i * q + i * r / runs; }
+  __device__ uint32_t of(uint32_t u) const { return static_cast<uint32_t>(((u + uint64_t(1)) * runs - 1) / total); }
+};
 
 template <int MODE, int DT, int DP, bool PAD>
 __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void decode_kernel(DecodeArgs a, float* __restrict__ part, int32_t nht, int32_t gh,
@@ -205,9 +217,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   constexpr int LDH = 17;  // row pitch of the output exchange (heads)
   __shared__ float s_o[kWaves][DP * LDH];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
-  __shared__ int64_t s_sum[kWaves];
-  __shared__ int32_t s_b, s_len[kHeldLengths];
-  __shared__ int64_t s_at;
+  __shared__ int32_t s_sum[kWaves], s_len[kHeldLengths], s_b, s_at;
 
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kb = lane >> 4;
@@ -218,52 +228,53 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   const int sb = MODE == kKvFp4 ? 2 * ((D + 63) / 64) : 4;
 
   // ---- this workgroup's run of units
-  int64_t u = 0, u_end = 0;  // units from the start of sequence b on
+  int u = 0, u_end = 0;  // units from the start of sequence b on
   int b = 0;
   if (single) {  // every segment is one unit: no plan, no join
     b = blockIdx.x / per_b;
     u = blockIdx.x - b * per_b;
     u_end = u + 1;
   } else {
-    // total, then the sequence that holds the first unit, by scans over the lengths 256 at a time
-    int64_t mine = 0;
+    // the units of all sequences, then the sequence that holds the first unit: scans over the
+    // lengths, 256 at a time; the first pass over them keeps the first scan
+    int mine = 0, incl = 0, n0 = 0;
     for (int i = tid; i < a.B; i += kThreads) {
       const int32_t n = length_of(a, i);
       if (i < kHeldLengths) s_len[i] = n;
       mine += units_of(n);
+      if (i == tid) n0 = mine;
     }
-    for (int o = 1; o < 64; o <<= 1) mine += __shfl_xor(mine, o);
-    if (lane == 0) s_sum[wv] = mine;
+    incl = wave_scan(n0);
+    const int all = a.B <= kThreads ? incl : wave_scan(mine);
+    if (lane == 63) s_sum[wv] = all;
     __syncthreads();
-    const int64_t total = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * per_b;
-    const int64_t runs = min(static_cast<int64_t>(gridDim.x), total);
-    if (blockIdx.x >= runs) return;
-    const int64_t first = run_start(blockIdx.x, total, runs), last = run_start(blockIdx.x + 1, total, runs);
-    int64_t base = 0;
+    const Runs run((s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * per_b, gridDim.x);
+    if (blockIdx.x >= run.runs) return;
+    const int first = run.start(blockIdx.x), last = run.start(blockIdx.x + 1);
+    int base = 0;
     for (int i0 = 0; i0 < a.B; i0 += kThreads) {
-      __syncthreads();
       const int i = i0 + tid;
-      const int64_t n = i < a.B ? static_cast<int64_t>(units_of(i < kHeldLengths ? s_len[i] : length_of(a, i))) * per_b : 0;
-      int64_t incl = n;
-      for (int o = 1; o < 64; o <<= 1) {
-        const int64_t t = __shfl_up(incl, o);
-        if (lane >= o) incl += t;
+      if (a.B > kThreads) {
+        n0 = i < a.B ? units_of(i < kHeldLengths ? s_len[i] : length_of(a, i)) : 0;
+        incl = wave_scan(n0);
+        __syncthreads();
+        if (lane == 63) s_sum[wv] = incl;
+        __syncthreads();
       }
-      if (lane == 63) s_sum[wv] = incl;
-      __syncthreads();
-      for (int w = 0; w < wv; ++w) incl += s_sum[w];
-      const int64_t end = base + incl;
-      if (first >= end - n && first < end) {
+      int end = base + incl;
+      for (int w = 0; w < wv; ++w) end += s_sum[w];
+      if (first >= (end - n0) * per_b && first < end * per_b) {
         s_b = i;
-        s_at = end - n;
+        s_at = (end - n0) * per_b;
       }
       base += s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-      if (first < base) break;
+      if (first < base * per_b) break;
     }
     __syncthreads();
     b = __builtin_amdgcn_readfirstlane(s_b);
-    u = uniform64(first - s_at);
-    u_end = uniform64(last - s_at);
+    const int at = __builtin_amdgcn_readfirstlane(s_at);
+    u = first - at;
+    u_end = last - at;
   }
 
   bool first_seg = true;
@@ -274,21 +285,21 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     // ---- the next segment of the run
     const int32_t n = __builtin_amdgcn_readfirstlane(!single && b < kHeldLengths ? s_len[b] : length_of(a, b));
     const int32_t nu = single ? 1 : units_of(n);
-    if (u >= static_cast<int64_t>(nu) * per_b) {  // on to the next sequence
-      u -= static_cast<int64_t>(nu) * per_b;
-      u_end -= static_cast<int64_t>(nu) * per_b;
+    if (u >= nu * per_b) {  // on to the next sequence
+      u -= nu * per_b;
+      u_end -= nu * per_b;
       ++b;
       continue;
     }
-    const int seg = __builtin_amdgcn_readfirstlane(static_cast<int>(u / nu));
+    const int seg = __builtin_amdgcn_readfirstlane(u / nu);
     const int hk = seg / nht, ht = seg - hk * nht;
-    const int ua = __builtin_amdgcn_readfirstlane(static_cast<int>(u - static_cast<int64_t>(seg) * nu));
-    const int ue = static_cast<int>(min(static_cast<int64_t>(nu), ua + (u_end - u)));
+    const int ua = u - seg * nu, ue = min(nu, ua + (u_end - u));
     u += ue - ua;
     // This lane's head within the group.  Of at most 8 heads the tile's columns 8 .. 15 take the same
     // heads again, with what the rounding of the weights left over: their sums are added to the others'.
     const int head = ht * 16 + (two ? r16 & 7 : r16);
     const bool my_head = head < a.g;
+    const float minus = r16 < 8 ? -0.0f : -1.0f;
 
     // ---- state of the segment
     f32x4_t acc[S::NH][S::EC];
@@ -536,11 +547,12 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       u32x4_t pf;
 #pragma unroll
       for (int i = 0; i < 4; ++i) pf[i] = h2<PDT>(w[2 * i], w[2 * i + 1]);
-      if (two) {
+      if (two) {  // minus: 1 in the columns of the remainders, else 0
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t rest = h2<PDT>(w[2 * i] - load16<PDT>(static_cast<uint16_t>(pf[i])), w[2 * i + 1] - load16<PDT>(static_cast<uint16_t>(pf[i] >> 16)));
-          pf[i] = r16 < 8 ? pf[i] : rest;
+          const uint32_t hi = pf[i];
+          pf[i] = h2<PDT>(__builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi)), minus, w[2 * i]),
+                          __builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi >> 16)), minus, w[2 * i + 1]));
         }
       }
 #pragma unroll
@@ -687,7 +699,8 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
                                                                int32_t gh, int32_t grid) {
   constexpr int G = kThreads / DP;  // threads that share an element's parts
   constexpr int kBatch = 8;         // parts of a thread in flight
-  __shared__ int64_t s_sum[2][kWaves];
+  constexpr int kFew = 4;
+  __shared__ int32_t s_sum[2][kWaves];
   __shared__ float s_m[G][DP], s_l[G][DP], s_o[G][DP];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int per_b = a.c.Hkv * nht, D = a.c.D;
@@ -695,9 +708,9 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   const int heads = min(16, a.g - ht * 16);
   const int d = tid % DP, gr = tid / DP;
   const int32_t n = length_of(a, b);
-  int64_t sum = 0, before = 0;
+  int sum = 0, before = 0;
   for (int i = tid; i < a.B; i += kThreads) {
-    const int64_t k = units_of(length_of(a, i));
+    const int k = units_of(length_of(a, i));
     sum += k;
     if (i < b) before += k;
   }
@@ -707,27 +720,57 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
     if (a.lse && tid == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
   }
   if (n == 0) return;
-  for (int o = 1; o < 64; o <<= 1) {
-    sum += __shfl_xor(sum, o);
-    before += __shfl_xor(before, o);
-  }
-  if (lane == 0) {
+  sum = wave_scan(sum);
+  before = wave_scan(before);
+  if (lane == 63) {
     s_sum[0][wv] = sum;
     s_sum[1][wv] = before;
   }
   __syncthreads();
-  const int64_t total = (s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b;
-  before = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b;
-  const int32_t nu = units_of(n);
-  const int64_t ua = before + static_cast<int64_t>(seg) * nu, ue = ua + nu;
-  const int64_t runs = min(static_cast<int64_t>(grid), total);
-  const int i0 = run_of(ua, total, runs), i1 = run_of(ue - 1, total, runs);
+  const Runs run((s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b, grid);
+  const int nu = units_of(n);
+  const uint32_t ua = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b + seg * nu;
+  const int i0 = run.of(ua), i1 = run.of(ua + nu - 1);
   if (i0 == i1) return;  // one workgroup had it all and wrote the rows
   const int np = i1 - i0 + 1;
   const int64_t pitch = static_cast<int64_t>(gh) * (DP + 2);
   // run i's part is its first one unless the run began before this segment (only i0 can have)
-  const float* const p0 = part + (static_cast<int64_t>(i0) * 2 + (run_start(i0, total, runs) < ua ? 1 : 0)) * pitch;
+  const float* const p0 = part + (static_cast<int64_t>(i0) * 2 + (run.start(i0) < ua ? 1 : 0)) * pitch;
   const float* const p1 = part + static_cast<int64_t>(i0) * 2 * pitch;  // + 2 i pitch for run i0 + i
+  if (np <= kFew) {  // (short segments: all parts of four elements of a thread in flight)
+    for (int e0 = blockIdx.y * 4 * kThreads + tid; e0 < heads * DP; e0 += gridDim.y * 4 * kThreads) {
+      float pm[4][kFew], pl[4][kFew], po[4][kFew];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = e0 + x * kThreads, hd = e / DP;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          const float* const p = i == 0 ? p0 : p1 + 2 * pitch * i;
+          const bool in = i < np && e < heads * DP;
+          pm[x][i] = in ? p[gh * DP + hd] : -kInf;
+          pl[x][i] = in ? p[gh * (DP + 1) + hd] : 0.0f;
+          po[x][i] = in ? p[e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = e0 + x * kThreads, hd = e / DP, de = e - hd * DP, hq = hk * a.g + ht * 16 + hd;
+        float m = -kInf, l = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) m = fmaxf(m, pm[x][i]);
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          const float w = pm[x][i] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(pm[x][i] - m);
+          l += pl[x][i] * w;
+          o += po[x][i] * w;
+        }
+        if (e < heads * DP && de < D) a.out.p[b * a.out.row + hq * a.out.head + de] = round16<DT>(l == 0.0f ? 0.0f : o / l);
+        if (a.lse && e < heads * DP && de == 0)
+          a.lse[static_cast<int64_t>(b) * a.Hq + hq] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+      }
+    }
+    return;
+  }
   for (int hd = blockIdx.y; hd < heads; hd += gridDim.y) {
     float m = -kInf, l = 0.0f, o = 0.0f;
     for (int k = gr; k < np; k += G * kBatch) {
@@ -796,7 +839,7 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // (enough workgroups of the join to fill the device, at most one a head)
-  const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(1024, segments)));
+  const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
   decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid);
   return hipGetLastError();
 }

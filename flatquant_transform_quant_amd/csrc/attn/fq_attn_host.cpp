@@ -204,7 +204,8 @@ static bool decode_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_
     return false;
   const int64_t n = block_table->shape[1] * P, most = (int64_t(1) << 31) - 1;
   *reach = n < most ? n : most;
-  return true;
+  // units of work (128 tokens of a sequence, cache head and 16 query heads) counted in 31 bits
+  return B * Hkv * ceil_div(Hq / Hkv, 16) * ceil_div(*reach, 128) < (int64_t(1) << 31);
 }
 
 fq_status fq_attn_decode_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table,
