@@ -406,61 +406,75 @@ def int4_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=No
 
 # ---- paged key-value cache and attention ---------------------------------------------------
 
-_DESC = struct.Struct("=Qii4q4q")  # the layout of fq_tensor
-_ZEROS = (0, 0, 0, 0)
+_DESC_BYTES = 80  # sizeof(fq_tensor): data, dtype, ndim, shape[4], strides[4]
+# by number of dimensions (the unused sizes and strides are padding, left at 0)
+_DESC = tuple(struct.Struct(f"=Qii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x") for n in range(5))
 _codes = {}  # torch dtype -> fq_dtype, filled on first use
 
 
-def _dtype_code(dtype) -> int:
+def _dtype_codes():
     if not _codes:
         torch = _torch()
         _codes.update({torch.float16: DT_FLOAT16, torch.bfloat16: DT_BFLOAT16, torch.float32: DT_FLOAT32,
                        torch.int32: DT_INT32, torch.int8: DT_INT8, torch.float8_e4m3fn: DT_FLOAT8_E4M3FN})
-    return _codes.get(dtype, -1)  # -1 is rejected by the library's checks
+    return _codes
+
+
+class _Descs:
+    """fq_tensor descriptors of a call's tensors side by side in one buffer, passed by address (a
+    call builds them anew, so building is kept cheap); None gives a null pointer."""
+    __slots__ = ("raw", "ptrs")
+
+    def __init__(self, *tensors):
+        n = len(tensors)
+        self.raw = raw = ctypes.create_string_buffer(n * _DESC_BYTES)
+        at = ctypes.addressof(raw)
+        codes = _codes or _dtype_codes()
+        self.ptrs = ptrs = []
+        for i, t in enumerate(tensors):
+            if t is None:
+                ptrs.append(None)
+                continue
+            shape = t.shape
+            # (an unknown dtype, or more than four dimensions, is for the library's checks to refuse)
+            nd = len(shape)
+            if nd <= 4:
+                _DESC[nd].pack_into(raw, i * _DESC_BYTES, t.data_ptr(), codes.get(t.dtype, -1), nd, *shape, *t.stride())
+            else:
+                _DESC[0].pack_into(raw, i * _DESC_BYTES, t.data_ptr(), -1, nd)
+            ptrs.append(at + i * _DESC_BYTES)
 
 
 class _Desc:
-    """An fq_tensor descriptor as bytes; passed by address (cheaper to build than a Structure)."""
+    """One descriptor with a given dtype, sizes and strides."""
     __slots__ = ("raw", "ptr")
 
     def __init__(self, data_ptr, dtype, shape, strides):
-        n = len(shape)
-        self.raw = ctypes.create_string_buffer(
-            _DESC.pack(data_ptr, dtype, n, *shape, *_ZEROS[n:], *strides, *_ZEROS[n:]) if n <= 4
-            else _DESC.pack(data_ptr, dtype, n, *_ZEROS, *_ZEROS), _DESC.size)
+        self.raw = ctypes.create_string_buffer(_DESC[len(shape)].pack(data_ptr, dtype, len(shape), *shape, *strides), _DESC_BYTES)
         self.ptr = ctypes.addressof(self.raw)
 
 
-def _desc(t, dtype=None) -> _Desc:
-    return _Desc(t.data_ptr(), _dtype_code(t.dtype) if dtype is None else dtype, t.shape, t.stride())
-
-
 def _same_device(first, *others):
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
 
 
-class _on_device:
-    """The launch goes to the tensors' device, whichever is current."""
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        torch = _torch()
-        self.guard = (torch.cuda.device(device) if device.type == "cuda" and device.index != torch.cuda.current_device()
-                      else None)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, name, device, *args):
+    """A launching call, on the tensors' device whichever is current."""
+    torch = _torch()
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args)
+    else:
+        st = fn(*args)
+    if st != FQ_SUCCESS:
+        raise FqError(st, name)
 
 
 def _stream(stream, device):
-    return stream if stream is not None else _torch().cuda.current_stream(device)
+    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream or None
 
 
 def _record(stream, *tensors):
@@ -503,14 +517,12 @@ class KVCache:
             if mode in ("int4", "fp4"):  # two codes a byte: sizes and strides in codes
                 shape[3] *= 2
                 st = [2 * n for n in st[:3]] + [1 if st[3] == 1 else 2 * st[3]]
-            return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _desc(s, sdt)
+            return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _Desc(s.data_ptr(), sdt, s.shape, s.stride())
 
         (self._kc, self._ks), (self._vc, self._vs) = side(k, k_scale), side(v, v_scale)
         self.pages, self.heads, self.page_size = k.shape[:3]
         self.head_dim = k.shape[3] * (2 if mode in ("int4", "fp4") else 1)
-
-    def _ptrs(self):
-        return (self._kc.ptr, self._ks.ptr if self._ks else None, self._vc.ptr, self._vs.ptr if self._vs else None)
+        self._ptrs = (self._kc.ptr, self._ks.ptr if self._ks else None, self._vc.ptr, self._vs.ptr if self._vs else None)
 
 
 def empty_kv_cache(pages: int, heads: int, page_size: int, head_dim: int, mode: str, device="cuda") -> KVCache:
@@ -535,13 +547,9 @@ def empty_kv_cache(pages: int, heads: int, page_size: int, head_dim: int, mode: 
 def kv_write(cache: KVCache, k, v, slots, clip_ratio: float = 1.0, dst_type_max: float = 0.0, stream=None) -> None:
     """Quantize rows k, v [T, Hkv, D] (bfloat16 or float16) into the cache at slots [T] (int32:
     page * page_size + offset; negative: not written)."""
-    _same_device(k, v, slots, cache.k)
-    kd, vd, sd = _desc(k), _desc(v), _desc(slots)
-    with _on_device(k.device):
-        st = lib.fq_kv_write(kd.ptr, vd.ptr, sd.ptr, clip_ratio, dst_type_max, *cache._ptrs(),
-                             _stream(stream, k.device).cuda_stream or None)
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_kv_write")
+    _same_device(cache.k, k, v, slots)
+    d = _Descs(k, v, slots)
+    _call(lib.fq_kv_write, "fq_kv_write", cache.device, *d.ptrs, clip_ratio, dst_type_max, *cache._ptrs, _stream(stream, cache.device))
 
 
 def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=None, v_out=None, stream=None):
@@ -559,12 +567,25 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
     elif k_out.dtype != dtype or v_out.dtype != dtype or k_out.shape[0] != total or v_out.shape[0] != total:
         raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
     _same_device(cache.k, block_table, cu_seqlens, k_out, v_out)
-    bd, cd, kd, vd = _desc(block_table), _desc(cu_seqlens), _desc(k_out), _desc(v_out)
-    with _on_device(cache.device):
-        st = lib.fq_kv_read(*cache._ptrs(), bd.ptr, cd.ptr, kd.ptr, vd.ptr, _stream(stream, cache.device).cuda_stream or None)
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_kv_read")
+    d = _Descs(block_table, cu_seqlens, k_out, v_out)
+    _call(lib.fq_kv_read, "fq_kv_read", cache.device, *cache._ptrs, *d.ptrs, _stream(stream, cache.device))
     return k_out, v_out
+
+
+def _workspace(fn, name, device, stream, given, *args):
+    """(tensor, pointer, bytes) of the workspace that `fn` asks for; `given` if the caller has one."""
+    size = ctypes.c_uint64(0)
+    st = fn(*args, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, name)
+    if given is not None:
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if size.value == 0:
+        return None, None, 0
+    torch = _torch()
+    ws = torch.empty((size.value,), dtype=torch.uint8, device=device)
+    _record(stream, ws)
+    return ws, ws.data_ptr(), size.value
 
 
 def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out=None, lse=None, workspace=None,
@@ -577,32 +598,20 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _record(stream, out)
-    _same_device(q, cache.k, block_table, lengths, out, lse, workspace)
-    qd, bd, ld, od = _desc(q), _desc(block_table), _desc(lengths), _desc(out)
-    sd = _desc(lse) if lse is not None else None
-    size = ctypes.c_uint64(0)
-    st = lib.fq_attn_decode_get_workspace_size(qd.ptr, cache._kc.ptr, bd.ptr, ctypes.byref(size))
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_attn_decode_get_workspace_size")
-    s = _stream(stream, q.device)
-    need = size.value
-    if need and workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-        _record(stream, workspace)
-    with _on_device(q.device):
-        st = lib.fq_attn_decode(qd.ptr, *cache._ptrs(), bd.ptr, ld.ptr, scale, od.ptr, sd.ptr if sd else None,
-                                workspace.data_ptr() if workspace is not None else None,
-                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                s.cuda_stream or None)
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_attn_decode")
+    _same_device(cache.k, q, block_table, lengths, out, lse, workspace)
+    d = _Descs(q, block_table, lengths, out, lse)
+    qp, bp, lp, op, sp = d.ptrs
+    ws, ptr, size = _workspace(lib.fq_attn_decode_get_workspace_size, "fq_attn_decode_get_workspace_size", cache.device, stream,
+                               workspace, qp, cache._kc.ptr, bp)
+    _call(lib.fq_attn_decode, "fq_attn_decode", cache.device, qp, *cache._ptrs, bp, lp, scale, op, sp, ptr, size,
+          _stream(stream, cache.device))
     return out
 
 
 def attn_decode_workspace_size(q, cache: KVCache, block_table) -> int:
     size = ctypes.c_uint64(0)
-    qd, bd = _desc(q), _desc(block_table)
-    st = lib.fq_attn_decode_get_workspace_size(qd.ptr, cache._kc.ptr, bd.ptr, ctypes.byref(size))
+    d = _Descs(q, block_table)
+    st = lib.fq_attn_decode_get_workspace_size(d.ptrs[0], cache._kc.ptr, d.ptrs[1], ctypes.byref(size))
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_attn_decode_get_workspace_size")
     return size.value
@@ -610,8 +619,8 @@ def attn_decode_workspace_size(q, cache: KVCache, block_table) -> int:
 
 def attn_prefill_workspace_size(q, k, cu_q, causal: bool = True) -> int:
     size = ctypes.c_uint64(0)
-    qd, kd, ad = _desc(q), _desc(k), _desc(cu_q)
-    st = lib.fq_attn_prefill_get_workspace_size(qd.ptr, kd.ptr, ad.ptr, 1 if causal else 0, ctypes.byref(size))
+    d = _Descs(q, k, cu_q)
+    st = lib.fq_attn_prefill_get_workspace_size(*d.ptrs, 1 if causal else 0, ctypes.byref(size))
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_attn_prefill_get_workspace_size")
     return size.value
@@ -631,20 +640,11 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
     if cu_k is None:
         cu_k = cu_q
     _same_device(q, k, v, cu_q, cu_k, out, lse, workspace)
-    qd, kd, vd, ad, bd, od = _desc(q), _desc(k), _desc(v), _desc(cu_q), _desc(cu_k), _desc(out)
-    sd = _desc(lse) if lse is not None else None
-    size = ctypes.c_uint64(0)
-    st = lib.fq_attn_prefill_get_workspace_size(qd.ptr, kd.ptr, ad.ptr, 1 if causal else 0, ctypes.byref(size))
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_attn_prefill_get_workspace_size")
-    if size.value and workspace is None:
-        workspace = torch.empty((size.value,), dtype=torch.uint8, device=q.device)
-        _record(stream, workspace)
-    with _on_device(q.device):
-        st = lib.fq_attn_prefill(qd.ptr, kd.ptr, vd.ptr, ad.ptr, bd.ptr, 1 if causal else 0, scale, od.ptr,
-                                 sd.ptr if sd else None, workspace.data_ptr() if workspace is not None else None,
-                                 workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                 _stream(stream, q.device).cuda_stream or None)
-    if st != FQ_SUCCESS:
-        raise FqError(st, "fq_attn_prefill")
+    d = _Descs(q, k, v, cu_q, cu_k, out, lse)
+    qp, kp, vp, ap, bp, op, sp = d.ptrs
+    causal = 1 if causal else 0
+    ws, ptr, size = _workspace(lib.fq_attn_prefill_get_workspace_size, "fq_attn_prefill_get_workspace_size", q.device, stream,
+                               workspace, qp, kp, ap, causal)
+    _call(lib.fq_attn_prefill, "fq_attn_prefill", q.device, qp, kp, vp, ap, bp, causal, scale, op, sp, ptr, size,
+          _stream(stream, q.device))
     return out

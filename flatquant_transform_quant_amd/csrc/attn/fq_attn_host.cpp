@@ -155,7 +155,7 @@ fq_status fq_kv_write(const fq_tensor* k, const fq_tensor* v, const fq_tensor* s
   if (k->ndim != 3) return FQ_ERR_PARAM_INVALID;
   const int64_t T = k->shape[0];
   Rows16 kr, vr;
-  if (row_dtype(k->dtype) == 0 || T < 0 || 2 * T * c.Hkv >= (int64_t(1) << 32) - 256 ||
+  if (row_dtype(k->dtype) == 0 || T < 0 || T >= (int64_t(1) << 31) - 65536 ||
       !rows_ok(*k, T, c.Hkv, c.D, k->dtype, &kr) || !rows_ok(*v, T, c.Hkv, c.D, k->dtype, &vr) || !i32_vec(*slots, T))
     return FQ_ERR_PARAM_INVALID;
   if (c.mode == kKv16 && c.dtype != row_dtype(k->dtype)) return FQ_ERR_PARAM_INVALID;

@@ -14,7 +14,7 @@ namespace fq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kReadTokens = 16;  // tokens of a workgroup of the read kernel
+constexpr int kEnough = 512;   // workgroups of a launch that need no more spreading
 
 // Max over aligned groups of SPAN lanes, as integers: |x| as fp32 bits orders finite values,
 // then infinity, then NaN, so a row that holds either shows it in its maximum.
@@ -31,30 +31,26 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
   return v;
 }
 
-// MODE, the rows' dtype, lanes per row, e8m0 rule (kE8V1 or kE8V2Div)
+// Both kernels: a lane group of LPR lanes owns one token of the workgroup's `tokens` and walks the
+// heads, kInFlight heads' keys and values at a time (all loaded before the first is used); with
+// fewer tokens than lane groups, the groups of a token share its heads.  So the page lookup
+// and the 64-bit addresses are formed once a token, and each head adds a constant.  The lane groups
+// of neighbouring tokens read (or write) neighbouring rows of a page.
+constexpr int kInFlight = 2;
+
+// How `tokens` is chosen: one a lane group where that gives enough workgroups; fewer spread a small
+// call over more of them, down to a lane group per head.
+int tokens_of(int64_t T, int Hkv, int lpr) {
+  int tokens = kThreads / lpr;
+  while (tokens > 1 && tokens / 2 * Hkv >= kThreads / lpr && ceil_div(T, tokens) < kEnough) tokens >>= 1;
+  return tokens;
+}
+
+// One 8-element piece of a row quantized and stored: codes and scale rows at `codes`, `scale`.
 template <int MODE, int DT, int LPR, int SV>
-__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCache c, uint32_t items, Rows16 kin, Rows16 vin,
-                                                             const int32_t* __restrict__ slots, float d, float dmax) {
-  // item = (token, head, side), the side fastest: a wave's 64 / LPR rows
-  const uint32_t item = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-  const int ch = threadIdx.x % LPR;  // elements 8 ch .. 8 ch + 7
-  const bool in_row = 8 * ch < c.D;
-  const uint32_t side = item & 1u, th = item >> 1;
-  const uint32_t t = th / static_cast<uint32_t>(c.Hkv), h = th - t * static_cast<uint32_t>(c.Hkv);
-  const bool live = item < items && in_row;
-  const int32_t slot = item < items ? slots[t] : -1;
-  u32x4_t raw = {0u, 0u, 0u, 0u};
-  if (live) {
-    const Rows16& in = side ? vin : kin;
-    raw = *reinterpret_cast<const u32x4_t*>(in.p + t * in.row + h * in.head + 8 * ch);
-  }
-  const int32_t page = slot >> c.page_log;  // a negative slot stays negative
-  const bool store = live && page >= 0 && page < c.pages;
-  const KvSide& sd = side ? c.v : c.k;
-  const int64_t row = (static_cast<int64_t>(h) << c.page_log) + (slot & ((1 << c.page_log) - 1));
+__device__ __forceinline__ void kv_store8(const u32x4_t raw, uint8_t* codes, uint8_t* scale, int ch, int D, float d, float dmax, bool store) {
   if constexpr (MODE == kKv16) {
-    if (store)
-      *reinterpret_cast<u32x4_t*>(sd.codes + page * sd.page_b + row * 2 * c.D + 16 * ch) = raw;
+    if (store) *reinterpret_cast<u32x4_t*>(codes + 16 * ch) = raw;
   } else {
     float x[8];
     kv_decode8<kKv16, DT>(raw, 1.0f, 0, x);
@@ -75,59 +71,96 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCache c, uint32_t 
         e8 = 255u;
       }
       if (store) {
-        *reinterpret_cast<uint32_t*>(sd.codes + page * sd.page_b + row * (c.D / 2) + 4 * ch) = w;
-        const int n = c.D / 32, sb = 2 * ((c.D + 63) / 64);
-        uint8_t* sc = sd.scale + page * sd.scale_page_b + row * sb;
+        *reinterpret_cast<uint32_t*>(codes + 4 * ch) = w;
         if (ch % 4 == 0) {
-          sc[ch / 4] = static_cast<uint8_t>(e8);
-          if (n < sb && ch / 4 == n - 1) sc[n] = 0;  // the pad byte of an odd group count
+          const int n = D / 32;
+          scale[ch / 4] = static_cast<uint8_t>(e8);
+          if ((n & 1) && ch / 4 == n - 1) scale[n] = 0;  // the pad byte of an odd group count
         }
       }
     } else {
-      const float scale = __uint_as_float(top) / d;
-      // q = x / scale, correctly rounded, from one reciprocal a row: with inv the rounded 1 / scale,
-      // q0 = x inv is within an ulp or so, the fused remainder x - q0 scale is exact, and q0 +
-      // remainder * inv rounds to the quotient (Markstein's correction).  Scales near the ends of
-      // the exponent range, where the remainder could underflow, divide.
-      const bool mid = scale > 0x1p-90f && scale < 0x1p100f;
-      const float inv = mid ? 1.0f / scale : 0.0f;
+      const float sc = __uint_as_float(top) / d;
+      // q = x / sc, correctly rounded, from one reciprocal a row: with inv the rounded 1 / sc, q0 = x inv
+      // is within an ulp or so, the fused remainder x - q0 sc is exact, and q0 + remainder * inv
+      // rounds to the quotient (Markstein's correction).  Scales near the ends of the exponent range,
+      // where the remainder could underflow, divide.
+      const bool mid = sc > 0x1p-90f && sc < 0x1p100f;
+      const float inv = mid ? 1.0f / sc : 0.0f;
       float q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float q0 = x[i] * inv;
-        q[i] = __builtin_fmaf(__builtin_fmaf(-q0, scale, x[i]), inv, q0);
+        q[i] = __builtin_fmaf(__builtin_fmaf(-q0, sc, x[i]), inv, q0);
         if constexpr (MODE == kKvE4M3) q[i] = __builtin_copysignf(q[i], x[i]);  // (the sum of a +0 and a -0 is +0)
       }
       if (!mid) {
-        const bool some = finite && scale > 0.0f;
+        const bool some = finite && sc > 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = some ? x[i] / scale : 0.0f;
+        for (int i = 0; i < 8; ++i) q[i] = some ? x[i] / sc : 0.0f;
       }
       if (store) {
-        uint8_t* const codes = sd.codes + page * sd.page_b;
         if constexpr (MODE == kKvInt4) {
           uint32_t w = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) w |= int4_nibble(q[i]) << (4 * i);
-          *reinterpret_cast<uint32_t*>(codes + row * (c.D / 2) + 4 * ch) = w;
+          *reinterpret_cast<uint32_t*>(codes + 4 * ch) = w;
         } else {
           constexpr int CM = MODE == kKvInt8 ? kPerTokenInt8 : kPerTokenE4M3;
-          *reinterpret_cast<u32x2_t*>(codes + row * c.D + 8 * ch) =
+          *reinterpret_cast<u32x2_t*>(codes + 8 * ch) =
               u32x2_t{code8x4<CM>(q[0], q[1], q[2], q[3]), code8x4<CM>(q[4], q[5], q[6], q[7])};
         }
-        if (ch == 0) *reinterpret_cast<float*>(sd.scale + page * sd.scale_page_b + row * 4) = scale;
+        if (ch == 0) *reinterpret_cast<float*>(scale) = sc;
       }
     }
   }
 }
 
+// MODE, the rows' dtype, lanes per row, e8m0 rule (kE8V1 or kE8V2Div)
+template <int MODE, int DT, int LPR, int SV>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvCache c, int32_t T, int32_t tokens, Rows16 kin, Rows16 vin,
+                                                             const int32_t* __restrict__ slots, float d, float dmax) {
+  const int ch = threadIdx.x % LPR, r = threadIdx.x / LPR;  // elements 8 ch .. 8 ch + 7
+  const int tk = r % tokens, h0 = r / tokens, dh = (kThreads / LPR) / tokens;
+  const int32_t t = blockIdx.x * tokens + tk;
+  const int32_t slot = t < T ? slots[t] : -1;
+  const int32_t page = slot >> c.page_log;  // a negative slot stays negative
+  const bool there = page >= 0 && page < c.pages && 8 * ch < c.D;  // (all lanes stay for the maxima)
+  const int64_t rowb = kv_row_bytes(MODE, c.D), sb = kv_scale_bytes(MODE, c.D);
+  const int64_t off = slot & ((1 << c.page_log) - 1);
+  const int64_t first = (static_cast<int64_t>(h0) << c.page_log) + off;
+  const uint16_t* src[2] = {kin.p + t * kin.row + h0 * kin.head + 8 * ch, vin.p + t * vin.row + h0 * vin.head + 8 * ch};
+  uint8_t* codes[2] = {c.k.codes + (page * c.k.page_b + first * rowb), c.v.codes + (page * c.v.page_b + first * rowb)};
+  uint8_t* scale[2] = {c.k.scale + (page * c.k.scale_page_b + first * sb), c.v.scale + (page * c.v.scale_page_b + first * sb)};
+  const int64_t src_d[2] = {dh * kin.head, dh * vin.head}, codes_d = (dh * rowb) << c.page_log, scale_d = (dh * sb) << c.page_log;
+  for (int h = h0; h < c.Hkv; h += dh * kInFlight) {
+    u32x4_t raw[2][kInFlight];
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i)
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        raw[side][i] = u32x4_t{0u, 0u, 0u, 0u};
+        if (there && h + i * dh < c.Hkv) raw[side][i] = *reinterpret_cast<const u32x4_t*>(src[side] + i * src_d[side]);
+      }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i)
+        kv_store8<MODE, DT, LPR, SV>(raw[side][i], codes[side] + i * codes_d, scale[side] + i * scale_d, ch, c.D, d, dmax,
+                                     there && h + i * dh < c.Hkv);
+      src[side] += kInFlight * src_d[side];
+      codes[side] += kInFlight * codes_d;
+      scale[side] += kInFlight * scale_d;
+    }
+  }
+}
+
 template <int MODE, int DT, int LPR>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCache c, int32_t T, int32_t B, BlockTable bt,
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCache c, int32_t T, int32_t B, int32_t tokens, BlockTable bt,
                                                             const int32_t* __restrict__ cu, Rows16 kout, Rows16 vout) {
   // this workgroup's tokens: their sequences by bisection of cu, their pages from the table
-  __shared__ int32_t s_page[kReadTokens], s_off[kReadTokens];
-  const int32_t t0 = blockIdx.x * kReadTokens;
-  if (threadIdx.x < kReadTokens) {
+  __shared__ int32_t s_page[kThreads / LPR], s_off[kThreads / LPR];
+  const int32_t t0 = blockIdx.x * tokens;
+  if (threadIdx.x < static_cast<uint32_t>(tokens)) {
     const int32_t t = t0 + static_cast<int32_t>(threadIdx.x);
     int32_t page = -2, off = 0;  // -2: not a row of any sequence, not written
     if (t < T && t < cu[B]) {
@@ -144,72 +177,92 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCache c, int32_t T,
     s_off[threadIdx.x] = off;
   }
   __syncthreads();
-  // items (side, head, token), the token fastest, LPR lanes each
-  const int ch = threadIdx.x % LPR;
-  const int n = 2 * c.Hkv * kReadTokens;
-  if (8 * ch >= c.D) return;
-#pragma unroll 4
-  for (int it = threadIdx.x / LPR; it < n; it += kThreads / LPR) {
-    const int tk = it % kReadTokens, sh = it / kReadTokens;
-    const int side = sh >= c.Hkv, h = sh - (side ? c.Hkv : 0);
-    const int32_t page = s_page[tk];
-    if (page == -2) continue;
-    const KvSide& sd = side ? c.v : c.k;
-    u32x4_t o = {0u, 0u, 0u, 0u};
-    if (page >= 0) {
-      const int64_t row = (static_cast<int64_t>(h) << c.page_log) + s_off[tk];
-      const u32x4_t w = kv_load8<MODE>(sd.codes + page * sd.page_b + row * kv_row_bytes(MODE, c.D), ch);
-      if constexpr (MODE == kKv16) {
-        o = w;
-      } else {
-        const uint8_t* sc = sd.scale + page * sd.scale_page_b;
-        float scale = 0.0f, v[8];
-        uint32_t e8 = 0;
-        if constexpr (MODE == kKvFp4)
-          e8 = sc[row * (2 * ((c.D + 63) / 64)) + ch / 4];
-        else
-          scale = *reinterpret_cast<const float*>(sc + row * 4);
-        kv_decode8<MODE, DT>(w, scale, e8, v);
+  const int ch = threadIdx.x % LPR, r = threadIdx.x / LPR;
+  const int tk = r % tokens, h0 = r / tokens, dh = (kThreads / LPR) / tokens;
+  const int32_t page = s_page[tk];
+  if (8 * ch >= c.D || page == -2) return;
+  const bool there = page >= 0;  // a token without a page gives zeros
+  const int64_t rowb = kv_row_bytes(MODE, c.D), sb = kv_scale_bytes(MODE, c.D), off = s_off[tk];
+  const int64_t first = (static_cast<int64_t>(h0) << c.page_log) + off, t = t0 + tk;
+  uint16_t* dst[2] = {kout.p + t * kout.row + h0 * kout.head + 8 * ch, vout.p + t * vout.row + h0 * vout.head + 8 * ch};
+  const uint8_t* codes[2] = {c.k.codes + (page * c.k.page_b + first * rowb), c.v.codes + (page * c.v.page_b + first * rowb)};
+  const uint8_t* scale[2] = {c.k.scale + (page * c.k.scale_page_b + first * sb), c.v.scale + (page * c.v.scale_page_b + first * sb)};
+  const int64_t dst_d[2] = {dh * kout.head, dh * vout.head}, codes_d = (dh * rowb) << c.page_log, scale_d = (dh * sb) << c.page_log;
+  for (int h = h0; h < c.Hkv; h += dh * kInFlight) {
+    u32x4_t w[2][kInFlight];
+    float sc[2][kInFlight];
+    uint32_t e8[2][kInFlight];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = round16x2<DT>(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < kInFlight; ++i)
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        w[side][i] = u32x4_t{0u, 0u, 0u, 0u};
+        sc[side][i] = 0.0f;
+        e8[side][i] = 0u;
+        if (there && h + i * dh < c.Hkv) {
+          w[side][i] = kv_load8<MODE>(codes[side] + i * codes_d, ch);
+          if constexpr (MODE == kKvFp4)
+            e8[side][i] = scale[side][i * scale_d + ch / 4];
+          else if constexpr (MODE != kKv16)
+            sc[side][i] = *reinterpret_cast<const float*>(scale[side] + i * scale_d);
+        }
       }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        if (h + i * dh >= c.Hkv) break;
+        u32x4_t o = w[side][i];
+        if constexpr (MODE != kKv16) {
+          float v[8];
+          kv_decode8<MODE, DT>(w[side][i], sc[side][i], e8[side][i], v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = round16x2<DT>(v[2 * j], v[2 * j + 1]);
+        }
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(dst[side] + i * dst_d[side]));
+      }
+      dst[side] += kInFlight * dst_d[side];
+      codes[side] += kInFlight * codes_d;
+      scale[side] += kInFlight * scale_d;
     }
-    const Rows16& out = side ? vout : kout;
-    __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(out.p + (t0 + tk) * out.row + h * out.head + 8 * ch));
   }
+}
+
+// f(lanes of a row)
+template <typename F>
+void by_lanes(int D, F&& f) {
+  if (D <= 64) f(std::integral_constant<int, 8>{});
+  else if (D <= 128) f(std::integral_constant<int, 16>{});
+  else f(std::integral_constant<int, 32>{});
 }
 
 template <int MODE, int DT>
 hipError_t write_mode(const KvCache& c, int64_t T, const Rows16& k, const Rows16& v, const int32_t* slots, float d,
                       float dmax, hipStream_t s) {
-  const uint32_t items = static_cast<uint32_t>(2 * T * c.Hkv);
   auto go = [&](auto lpr, auto sv) {
     constexpr int L = decltype(lpr)::value, SV = decltype(sv)::value;
-    kv_write_kernel<MODE, DT, L, SV><<<static_cast<uint32_t>(ceil_div(items, kThreads / L)), kThreads, 0, s>>>(
-        c, items, k, v, slots, d, dmax);
+    const int tokens = tokens_of(T, c.Hkv, L);
+    kv_write_kernel<MODE, DT, L, SV><<<static_cast<uint32_t>(ceil_div(T, tokens)), kThreads, 0, s>>>(
+        c, static_cast<int32_t>(T), tokens, k, v, slots, d, dmax);
   };
-  auto by_rule = [&](auto lpr) {
+  by_lanes(c.D, [&](auto lpr) {
     if constexpr (MODE == kKvFp4) {
       if (dmax != 0.0f) return go(lpr, std::integral_constant<int, kE8V2Div>{});
     }
     go(lpr, std::integral_constant<int, kE8V1>{});
-  };
-  if (c.D <= 64) by_rule(std::integral_constant<int, 8>{});
-  else if (c.D <= 128) by_rule(std::integral_constant<int, 16>{});
-  else by_rule(std::integral_constant<int, 32>{});
+  });
   return hipGetLastError();
 }
 
 template <int MODE, int DT>
 hipError_t read_mode(const KvCache& c, int64_t T, int32_t B, const BlockTable& bt, const int32_t* cu, const Rows16& k,
                      const Rows16& v, hipStream_t s) {
-  const uint32_t grid = static_cast<uint32_t>(ceil_div(T, kReadTokens));
-  auto go = [&](auto lpr) {
-    kv_read_kernel<MODE, DT, decltype(lpr)::value><<<grid, kThreads, 0, s>>>(c, static_cast<int32_t>(T), B, bt, cu, k, v);
-  };
-  if (c.D <= 64) go(std::integral_constant<int, 8>{});
-  else if (c.D <= 128) go(std::integral_constant<int, 16>{});
-  else go(std::integral_constant<int, 32>{});
+  by_lanes(c.D, [&](auto lpr) {
+    constexpr int L = decltype(lpr)::value;
+    const int tokens = tokens_of(T, c.Hkv, L);
+    kv_read_kernel<MODE, DT, L><<<static_cast<uint32_t>(ceil_div(T, tokens)), kThreads, 0, s>>>(c, static_cast<int32_t>(T), B, tokens,
+                                                                                              bt, cu, k, v);
+  });
   return hipGetLastError();
 }
 
