@@ -163,6 +163,31 @@ def test_decode_nan_reaches_only_who_sees_it():
     assert out[0, 2:].isnan().all() and not out[0, :2].isnan().any() and not out[1].isnan().any()
 
 
+@pytest.mark.parametrize("mode", MODES[1:])
+def test_decode_of_rows_that_hold_nan(mode):
+    """A value row with a NaN (an infinity) written to a low-bit cache reads as NaN: per token all of its elements, per group
+    its 32; a key row makes every element of its heads' outputs NaN."""
+    g = torch.Generator().manual_seed(2)
+    n, H, D, P = 50, 2, 128, 16
+    x, y = (torch.randn(n, H, D, generator=g).bfloat16() for _ in range(2))
+    y[20, 1, 70] = math.nan
+    y[33, 1, 70] = math.inf
+    cache = fq.empty_kv_cache(4, H, P, D, mode, DEV)
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+    table = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = torch.randn(1, 4, D, generator=g).bfloat16().to(DEV)
+    fq.kv_write(cache, x.to(DEV), y.to(DEV), slots)
+    out = fq.attn_decode(q, cache, table, lens)[0].isnan()
+    assert not out[:2].any()
+    hit = torch.zeros(D, dtype=torch.bool, device=DEV)
+    hit[64:96] = True
+    assert (out[2:] == (hit if mode == "fp4" else True)).all()
+    x[5, 0, 3] = math.nan
+    fq.kv_write(cache, x.to(DEV), y.to(DEV), slots)
+    assert fq.attn_decode(q, cache, table, lens)[0, :2].isnan().all()
+
+
 def test_decode_repeats_bit_for_bit_and_takes_a_workspace():
     cache, table, *_ = _fill([3000, 17, 900], 2, 128, 32, "int4", "bf16", 4)
     q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
