@@ -671,8 +671,10 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       for (int w = 0; w < kWaves; ++w) {
         const float mw = s_m[w][hd];
         ls += s_l[w][hd] == 0.0f ? 0.0f : s_l[w][hd] * __builtin_amdgcn_exp2f(mw - mx);  // (nothing seen, or NaN)
-        o += s_o[w][d * LDH + hd];
-        if (two) o += s_o[w][d * LDH + hd + 8];
+        const float x = s_o[w][d * LDH + hd];
+        o += x;
+        // (a seen infinity: its weight's remainder may be 0 or of the other sign, the sum is that of x)
+        if (two && __builtin_fabsf(x) < kInf) o += s_o[w][d * LDH + hd + 8];
       }
       const int hq = hk * a.g + ht * 16 + hd;
       if (all) {

@@ -202,8 +202,8 @@ static bool decode_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_
   if (B < 0 || B > 65536 || Hq < 1 || Hq > 65536 || Hkv < 1 || Hkv > 1024 || Hq % Hkv != 0 || D < 8 || D > 256 ||
       D != k_cache->shape[3] || P < 16 || P > 1024 || block_table->shape[1] < 0 || block_table->shape[1] >= (int64_t(1) << 31))
     return false;
-  const int64_t n = block_table->shape[1] * P, most = (int64_t(1) << 31) - 1;
-  *reach = n < most ? n : most;
+  *reach = block_table->shape[1] * P;
+  if (*reach >= (int64_t(1) << 31) - 65536) return false;  // (a step past the last token stays within 31 bits)
   // units of work (128 tokens of a sequence, cache head and 16 query heads) counted in 31 bits
   return B * Hkv * ceil_div(Hq / Hkv, 16) * ceil_div(*reach, 128) < (int64_t(1) << 31);
 }

@@ -221,6 +221,17 @@ def test_workspaces():
     assert p(prefill_args(tq=65536, tk=65536)) == OK and size.value == 0  # rows enough to fill the device
 
 
+def test_decode_reach_is_bounded():
+    """A table whose reach a step past the last token could carry beyond 31 bits is refused."""
+    size = ctypes.c_uint64()
+    for width, want in ((2 ** 27 - 4096, INVAL), (2 ** 27, INVAL), (2 ** 26, OK)):
+        a = decode_args(width=width)
+        assert a["kc"].shape[2] == 16
+        assert fq.lib.fq_attn_decode_get_workspace_size(ref(a["q"]), ref(a["kc"]), ref(a["bt"]), ctypes.byref(size)) == want
+        if want == INVAL:
+            assert decode(with_(a, ws=DUMMY, size=2 ** 40)) == INVAL
+
+
 def test_python_arguments_refused():
     c = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt)  # noqa: E731
     with pytest.raises(ValueError):

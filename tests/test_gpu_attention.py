@@ -163,6 +163,28 @@ def test_decode_nan_reaches_only_who_sees_it():
     assert out[0, 2:].isnan().all() and not out[0, :2].isnan().any() and not out[1].isnan().any()
 
 
+@pytest.mark.parametrize("Hq", [2, 4, 32])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_seen_infinities_stay_infinities(dtype, Hq):
+    """An infinite value that a row sees with a weight above zero makes that element infinite, not NaN, and no other element:
+    with one and two heads a group, where the weights count in two parts, and with 16; in a prompt the same."""
+    g = torch.Generator().manual_seed(8)
+    n, H, D = 300, 2, 64
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    k, v = (torch.randn(n, H, D, generator=g).to(dt).to(DEV) for _ in range(2))
+    q = torch.randn(n, Hq, D, generator=g).to(dt).to(DEV)
+    v[7, 0, 3], v[290, 0, 5], v[130, 1, 60] = math.inf, -math.inf, -math.inf
+    cache = fq.empty_kv_cache(20, H, 16, D, dtype, DEV)
+    fq.kv_write(cache, k, v, torch.arange(n, dtype=torch.int32, device=DEV))
+    table = torch.arange(20, dtype=torch.int32, device=DEV)[None]
+    want = torch.zeros(Hq, D, device=DEV)
+    want[: Hq // 2, 3], want[: Hq // 2, 5], want[Hq // 2 :, 60] = math.inf, -math.inf, -math.inf
+    last = [fq.attn_decode(q[-1:], cache, table, torch.tensor([n], dtype=torch.int32, device=DEV))[0],
+            fq.attn_prefill(q, k, v, torch.tensor([0, n], dtype=torch.int32, device=DEV))[-1]]
+    for got in last:
+        assert torch.equal(torch.where(got.isinf(), got.float(), 0.0), want) and not got.isnan().any()
+
+
 @pytest.mark.parametrize("mode", MODES[1:])
 def test_decode_of_rows_that_hold_nan(mode):
     """A value row with a NaN (an infinity) written to a low-bit cache reads as NaN: per token all of its elements, per group
