@@ -34,9 +34,13 @@
 // cross-lane step and no rescaling.
 //
 // Split: the units of work are 128 tokens (4 waves x 32) of a (sequence, cache head, head tile);
-// all units in order are dealt to the grid in equal runs, whatever the lengths.  A run that holds
-// only part of a segment leaves its unnormalised sums and (m, l) in the workspace, and a second
-// launch joins them in a fixed order.
+// all units in order are dealt to the grid in equal runs, whatever the lengths; a segment counts two
+// or three units more than it has, for its page lookup, first loads and rows out (else the runs over
+// many short segments end last: 64 sequences of 1024 to 16384 tokens, int8, 157 us without, 152, 151,
+// 152 with one to three; the same of 128 in int4 218, 219, 215 and 210, 208 with four).  A run that
+// holds only part of a segment leaves its unnormalised sums and (m, l) in the workspace, and a second
+// launch joins them in a fixed order.  A segment's first loads are under way while the rows of the one
+// before are written.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -71,7 +75,13 @@ struct Shape {
   static constexpr int VB = EC * bits / 8;                                         // bytes of a value piece
   static constexpr int VW = VB < 4 ? 1 : VB / 4;
   static constexpr int KS = DP / 32;                                               // products of a score
-  // workgroups of a CU (waves of a SIMD): what registers and, at 256, LDS hold
+  // units that a segment's beginning and end (page lookup, first loads, rows out) count as, see above
+  static constexpr int start = bits == 4 ? 3 : 2;
+  // Workgroups of a CU (waves of a SIMD): as many as registers and, at 256, LDS hold without spills in
+  // the loop.  us with 1, 2, 3, 4: 64 sequences of up to 16384 tokens, int8 at 128: 212, 158, 170, 455;
+  // 128 of them, int4: 349, 242, 220, 248; 32 of up to 4096, 16 bits at 128: 39, 37, 39, 62, at 256:
+  // 119, 170, 128, 131 and int8 at 256: 75, 68, 97, 109; 64 of up to 8192 at 64, int8: 115, 77, 68, 69,
+  // int4 199, 125, 107, 103, 16 bits 116, 113, 117, 121 -- but 37 short ones at 64: 48, 31, 25, 24.
   static constexpr int per_cu = DP == 256 ? (bits == 16 ? 1 : 2) : DP == 64 ? 4 : bits == 4 ? 3 : 2;
 };
 
@@ -183,6 +193,8 @@ __device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int b) {
   return static_cast<int32_t>(max(int64_t(0), min(static_cast<int64_t>(a.lengths[b]), reach)));
 }
 __device__ __forceinline__ int32_t units_of(int32_t n) { return n / kUnit + (n % kUnit != 0); }
+// what a segment counts as when the work is dealt (see the top)
+__device__ __forceinline__ int32_t weight_of(int32_t n, int start) { return n > 0 ? units_of(n) + start : 0; }
 
 // Inclusive sum over the lanes up to each lane (DPP row shifts, then the rows' last lanes).
 __device__ __forceinline__ int wave_scan(int v) {
@@ -195,8 +207,8 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Workgroup i of `runs` (at most `total`, so that none is empty; all below 2^31, which the host
-// checks) has the units from start(i) = i total / runs up to start(i + 1); unit u is in run of(u).
+// Workgroup i of `runs` (at most `total`; all below 2^31, which the host checks) has the units from
+// start(i) = i total / runs up to start(i + 1); unit u is in run of(u).
 struct Runs {
   uint32_t total, runs, q, r;
   __device__ Runs(uint32_t units, uint32_t grid) : total(units), runs(min(units, grid)) {
@@ -241,7 +253,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     for (int i = tid; i < a.B; i += kThreads) {
       const int32_t n = length_of(a, i);
       if (i < kHeldLengths) s_len[i] = n;
-      mine += units_of(n);
+      mine += weight_of(n, S::start);
       if (i == tid) n0 = mine;
     }
     incl = wave_scan(n0);
@@ -255,7 +267,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     for (int i0 = 0; i0 < a.B; i0 += kThreads) {
       const int i = i0 + tid;
       if (a.B > kThreads) {
-        n0 = i < a.B ? units_of(i < kHeldLengths ? s_len[i] : length_of(a, i)) : 0;
+        n0 = i < a.B ? weight_of(i < kHeldLengths ? s_len[i] : length_of(a, i), S::start) : 0;
         incl = wave_scan(n0);
         __syncthreads();
         if (lane == 63) s_sum[wv] = incl;
@@ -281,20 +293,123 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   int32_t pages = -1;                 // lane 2 i + s: the page of subtile s of step (batch) + i
   int pages_b = -1, pages_t = -1;     // the sequence and first token they were fetched for
   const bool two = a.g <= 8;          // weights in two halves, see below
-  while (u < u_end) {
-    // ---- the next segment of the run
-    const int32_t n = __builtin_amdgcn_readfirstlane(!single && b < kHeldLengths ? s_len[b] : length_of(a, b));
-    const int32_t nu = single ? 1 : units_of(n);
-    if (u >= nu * per_b) {  // on to the next sequence
-      u -= nu * per_b;
-      u_end -= nu * per_b;
-      ++b;
-      continue;
+  // ---- the segment at hand: its sequence, length, heads and units, this wave's first token and steps
+  int32_t n = 0;
+  int nu = 0, seg = 0, ua = 0, ue = 0, t_first = 0, steps = 0;
+  auto next_segment = [&]() __attribute__((always_inline)) {  // false: nothing of it is this run's
+    int nw;
+    for (;; ++b) {
+      n = __builtin_amdgcn_readfirstlane(!single && b < kHeldLengths ? s_len[b] : length_of(a, b));
+      nw = single ? 1 : weight_of(n, S::start);
+      if (u < nw * per_b) break;
+      u -= nw * per_b;
+      u_end -= nw * per_b;
     }
-    const int seg = __builtin_amdgcn_readfirstlane(u / nu);
-    const int hk = seg / nht, ht = seg - hk * nht;
-    const int ua = u - seg * nu, ue = min(nu, ua + (u_end - u));
-    u += ue - ua;
+    nu = single ? 1 : units_of(n);
+    seg = __builtin_amdgcn_readfirstlane(u / nw);
+    const int start = single ? 0 : S::start, at = u - seg * nw, take = min(nw - at, u_end - u);
+    u += take;
+    ua = max(0, at - start);
+    ue = at + take - start;
+    // this wave's steps: tokens kUnit (ua + i) + kTile wv ..
+    t_first = kUnit * ua + kTile * wv;
+    const int t_last = min(n, kUnit * ue);
+    steps = t_first < t_last ? (t_last - t_first + kUnit - 1) / kUnit : 0;
+    return ua < ue;
+  };
+
+  auto fetch_pages = [&](int step) __attribute__((always_inline)) {
+    const int64_t t = static_cast<int64_t>(t_first) + static_cast<int64_t>(kUnit) * (step + (lane >> 1)) + 16 * (lane & 1);
+    pages = t < n ? kv_page(a.bt, b, static_cast<int32_t>(t), c.page_log, c.pages) : -1;
+    pages_b = b;
+    pages_t = t_first + kUnit * step;
+  };
+  const uint32_t koff = r16 * rowb + kb * (S::CE * S::bits / 8), keoff = r16 * sb + (S::CE * kb) / 32;
+  const uint32_t voff = 4 * kb * rowb + r16 * S::VB, veoff = 4 * kb * sb + (S::EC * r16) / 32;
+  // Loads go through a buffer resource per subtile that starts at its first row and ends behind
+  // its last token (at nothing for a subtile without a page): rows past n, and the pieces of
+  // padded lanes, whose offset is kOut, are zeros without a branch.
+  auto rows_of = [&](int step, int s) __attribute__((always_inline)) {
+    // (as a scalar: a clamp runs in a vector register, and a resource there costs a loop a load)
+    return __builtin_amdgcn_readfirstlane(max(0, min(16, n - (t_first + kUnit * step + 16 * s))));
+  };
+  auto resource = [&](const uint8_t* base, int64_t page_b, int row_b, int step, int s, int idx) __attribute__((always_inline)) {
+    const int32_t pg = __builtin_amdgcn_readlane(pages, 2 * idx + s);
+    const int off = (t_first + kUnit * step + 16 * s) & ((1 << c.page_log) - 1);
+    const int bytes = rows_of(step, s) * row_b;
+    const int64_t row = (static_cast<int64_t>(seg / nht) << c.page_log) + off;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (max(pg, 0) * page_b + row * row_b), static_cast<int16_t>(0),
+                                             pg < 0 ? 0 : bytes, kBufferWord3);
+  };
+  auto load_keys = [&](Keys<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const auto rc = resource(c.k.codes, c.k.page_b, rowb, step, s, idx);
+#pragma unroll
+      for (int p = 0; p < S::KC; ++p)
+        load_words<S::KW>(rc, (PAD && S::CE * (4 * p + kb) >= D ? kOut : koff) + p * (4 * S::CE * S::bits / 8), x.w[s][p]);
+      if constexpr (MODE != kKv16) {
+        const auto rs = resource(c.k.scale, c.k.scale_page_b, sb, step, s, idx);
+        if constexpr (MODE == kKvFp4) {
+#pragma unroll
+          for (int p = 0; p < S::KC; ++p)
+            x.e8[s][p] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && S::CE * (4 * p + kb) >= D ? kOut : keoff) + S::CE * 4 * p / 32, 0, 0);
+        } else {
+          x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
+        }
+      }
+    }
+  };
+  auto load_values = [&](Values<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const auto rc = resource(c.v.codes, c.v.page_b, rowb, step, s, idx);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < S::NH; ++h) {
+          const uint32_t o = (PAD && 128 * h + S::EC * r16 >= D ? kOut : voff) + i * rowb + h * (16 * S::VB);
+          if constexpr (S::VB == 2)
+            x.w[4 * s + i][h][0] = __builtin_amdgcn_raw_buffer_load_b16(rc, o, 0, 0);
+          else
+            load_words<S::VW>(rc, o, x.w[4 * s + i][h]);
+        }
+      if constexpr (MODE != kKv16) {
+        const auto rs = resource(c.v.scale, c.v.scale_page_b, sb, step, s, idx);
+        if constexpr (MODE == kKvFp4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < S::NH; ++h)
+              x.e8[4 * s + i][h] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && 128 * h + S::EC * r16 >= D ? kOut : veoff) + i * sb + 4 * h, 0, 0);
+        } else {
+          x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
+        }
+      }
+    }
+  };
+  // the rows a lane's four tokens of a subtile have left (0 .. 4): for steps that are not whole
+  auto mine = [&](int step, int s, int idx) __attribute__((always_inline)) {
+    const int rows = rows_of(step, s);
+    return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows) - 4 * kb;
+  };
+
+  // the first step's loads of a segment
+  Keys<MODE, DP, PAD> kx;
+  Values<MODE, DP, PAD> vx;
+  auto begin = [&]() __attribute__((always_inline)) {
+    if (steps > 0) {
+      if (pages_b != b || pages_t != t_first) fetch_pages(0);
+      load_keys(kx, 0, 0);
+      load_values(vx, 0, 0);
+    }
+  };
+
+  if (!next_segment()) return;
+  begin();
+  for (bool more = true; more;) {
+    const int b0 = b, hk = seg / nht, ht = seg - hk * nht;
+    const bool all = ua == 0 && ue == nu;
     // This lane's head within the group.  Of at most 8 heads the tile's columns 8 .. 15 take the same
     // heads again, with what the rounding of the weights left over: their sums are added to the others'.
     const int head = ht * 16 + (two ? r16 & 7 : r16);
@@ -312,101 +427,11 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     float ref_inv = 0.0f;   // 2^-R
     float ref_lim = 0.0f;   // a scale at or above 2^(R + 6) moves R
 
-    // this wave's steps: tokens kUnit (ua + i) + kTile wv ..
-    const int t_first = kUnit * ua + kTile * wv;
-    const int t_last = min(n, kUnit * ue);
-    const int steps = t_first < t_last ? (t_last - t_first + kUnit - 1) / kUnit : 0;
-
-    auto fetch_pages = [&](int step) __attribute__((always_inline)) {
-      const int64_t t = static_cast<int64_t>(t_first) + static_cast<int64_t>(kUnit) * (step + (lane >> 1)) + 16 * (lane & 1);
-      pages = t < n ? kv_page(a.bt, b, static_cast<int32_t>(t), c.page_log, c.pages) : -1;
-      pages_b = b;
-      pages_t = t_first + kUnit * step;
-    };
-    const int64_t khead = static_cast<int64_t>(hk) << c.page_log;
-    const uint32_t koff = r16 * rowb + kb * (S::CE * S::bits / 8), keoff = r16 * sb + (S::CE * kb) / 32;
-    const uint32_t voff = 4 * kb * rowb + r16 * S::VB, veoff = 4 * kb * sb + (S::EC * r16) / 32;
-    // Loads go through a buffer resource per subtile that starts at its first row and ends behind
-    // its last token (at nothing for a subtile without a page): rows past n, and the pieces of
-    // padded lanes, whose offset is kOut, are zeros without a branch.
-    auto rows_of = [&](int step, int s) __attribute__((always_inline)) {
-      // (as a scalar: a clamp runs in a vector register, and a resource there costs a loop a load)
-      return __builtin_amdgcn_readfirstlane(max(0, min(16, n - (t_first + kUnit * step + 16 * s))));
-    };
-    auto resource = [&](const uint8_t* base, int64_t page_b, int row_b, int step, int s, int idx) __attribute__((always_inline)) {
-      const int32_t pg = __builtin_amdgcn_readlane(pages, 2 * idx + s);
-      const int off = (t_first + kUnit * step + 16 * s) & ((1 << c.page_log) - 1);
-      const int bytes = rows_of(step, s) * row_b;
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base) + (max(pg, 0) * page_b + (khead + off) * row_b), static_cast<int16_t>(0),
-                                               pg < 0 ? 0 : bytes, kBufferWord3);
-    };
-    auto load_keys = [&](Keys<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const auto rc = resource(c.k.codes, c.k.page_b, rowb, step, s, idx);
-#pragma unroll
-        for (int p = 0; p < S::KC; ++p)
-          load_words<S::KW>(rc, (PAD && S::CE * (4 * p + kb) >= D ? kOut : koff) + p * (4 * S::CE * S::bits / 8), x.w[s][p]);
-        if constexpr (MODE != kKv16) {
-          const auto rs = resource(c.k.scale, c.k.scale_page_b, sb, step, s, idx);
-          if constexpr (MODE == kKvFp4) {
-#pragma unroll
-            for (int p = 0; p < S::KC; ++p)
-              x.e8[s][p] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && S::CE * (4 * p + kb) >= D ? kOut : keoff) + S::CE * 4 * p / 32, 0, 0);
-          } else {
-            x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
-          }
-        }
-      }
-    };
-    auto load_values = [&](Values<MODE, DP, PAD>& x, int step, int idx) __attribute__((always_inline)) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const auto rc = resource(c.v.codes, c.v.page_b, rowb, step, s, idx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < S::NH; ++h) {
-            const uint32_t o = (PAD && 128 * h + S::EC * r16 >= D ? kOut : voff) + i * rowb + h * (16 * S::VB);
-            if constexpr (S::VB == 2)
-              x.w[4 * s + i][h][0] = __builtin_amdgcn_raw_buffer_load_b16(rc, o, 0, 0);
-            else
-              load_words<S::VW>(rc, o, x.w[4 * s + i][h]);
-          }
-        if constexpr (MODE != kKv16) {
-          const auto rs = resource(c.v.scale, c.v.scale_page_b, sb, step, s, idx);
-          if constexpr (MODE == kKvFp4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int h = 0; h < S::NH; ++h)
-                x.e8[4 * s + i][h] = __builtin_amdgcn_raw_buffer_load_b8(rs, (PAD && 128 * h + S::EC * r16 >= D ? kOut : veoff) + i * sb + 4 * h, 0, 0);
-          } else {
-            x.scale[s] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * kb, 0, 0));
-          }
-        }
-      }
-    };
-    // the rows a lane's four tokens of a subtile have left (0 .. 4): for steps that are not whole
-    auto mine = [&](int step, int s, int idx) __attribute__((always_inline)) {
-      const int rows = rows_of(step, s);
-      return (__builtin_amdgcn_readlane(pages, 2 * idx + s) < 0 ? 0 : rows) - 4 * kb;
-    };
-
-    // the first step's loads are under way before q is waited for
-    Keys<MODE, DP, PAD> kx;
-    Values<MODE, DP, PAD> vx;
-    if (steps > 0) {
-      if (pages_b != b || pages_t != t_first) fetch_pages(0);
-      load_keys(kx, 0, 0);
-      load_values(vx, 0, 0);
-    }
-
     // ---- q as the B operand, and the column's constants
     u32x4_t qf[S::KS];
     float cq = a.scale * 1.44269504f * kCode;
     {
-      const uint16_t* qp = a.q.p + b * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
+      const uint16_t* qp = a.q.p + b0 * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
       u32x4_t raw[S::KS];
 #pragma unroll
       for (int ks = 0; ks < S::KS; ++ks) {
@@ -631,6 +656,10 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       }
     }
 
+    // ---- the next segment's first loads, under way while this one's rows are written
+    more = u < u_end && next_segment();
+    if (more) begin();
+
     // ---- the four waves' sums joined; the whole segment's rows out, or its part to the workspace
     // (lane indices redefined: what derives from them is not kept in registers across the steps)
     const int el = static_cast<int>(here(lane)), er = el & 15, eb = el >> 4;
@@ -659,7 +688,6 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
           }
     }
     __syncthreads();
-    const bool all = ua == 0 && ue == nu;
     const int heads = min(16, a.g - ht * 16);
     float* slot = part + (static_cast<int64_t>(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * (static_cast<int64_t>(gh) * (DP + 2));
     for (int i = static_cast<int>(here(tid)); i < heads * DP; i += kThreads) {
@@ -678,9 +706,9 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       }
       const int hq = hk * a.g + ht * 16 + hd;
       if (all) {
-        if (!PAD || d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = round16<DT>(ls == 0.0f ? 0.0f : o / ls);
+        if (!PAD || d < D) a.out.p[b0 * a.out.row + hq * a.out.head + d] = round16<DT>(ls == 0.0f ? 0.0f : o / ls);
         if (a.lse && d == 0)
-          a.lse[static_cast<int64_t>(b) * a.Hq + hq] = ls == 0.0f ? -kInf : (mx + __builtin_amdgcn_logf(ls)) * 0.693147181f;
+          a.lse[static_cast<int64_t>(b0) * a.Hq + hq] = ls == 0.0f ? -kInf : (mx + __builtin_amdgcn_logf(ls)) * 0.693147181f;
       } else {
         slot[hd * DP + d] = o;
         if (d == 0) {
@@ -698,7 +726,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 // workgroup per segment and, with gridDim.y > 1, every gridDim.y-th of its heads.
 template <int DT, int DP>
 __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, const float* __restrict__ part, int32_t nht,
-                                                               int32_t gh, int32_t grid) {
+                                                               int32_t gh, int32_t grid, int32_t start) {
   constexpr int G = kThreads / DP;  // threads that share an element's parts
   constexpr int kBatch = 8;         // parts of a thread in flight
   constexpr int kFew = 4;
@@ -712,7 +740,7 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   const int32_t n = length_of(a, b);
   int sum = 0, before = 0;
   for (int i = tid; i < a.B; i += kThreads) {
-    const int k = units_of(length_of(a, i));
+    const int k = weight_of(length_of(a, i), start);
     sum += k;
     if (i < b) before += k;
   }
@@ -730,9 +758,9 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   }
   __syncthreads();
   const Runs run((s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b, grid);
-  const int nu = units_of(n);
-  const uint32_t ua = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b + seg * nu;
-  const int i0 = run.of(ua), i1 = run.of(ua + nu - 1);
+  const int nw = weight_of(n, start);
+  const uint32_t ua = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b + seg * nw;
+  const int i0 = run.of(ua + start), i1 = run.of(ua + nw - 1);
   if (i0 == i1) return;  // one workgroup had it all and wrote the rows
   const int np = i1 - i0 + 1;
   const int64_t pitch = static_cast<int64_t>(gh) * (DP + 2);
@@ -842,7 +870,7 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   if (err != hipSuccess) return err;
   // (enough workgroups of the join to fill the device, at most one a head)
   const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
-  decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid);
+  decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid, Shape<MODE, DP, PAD>::start);
   return hipGetLastError();
 }
 

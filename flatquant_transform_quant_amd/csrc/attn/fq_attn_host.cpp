@@ -204,8 +204,9 @@ static bool decode_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_
     return false;
   *reach = block_table->shape[1] * P;
   if (*reach >= (int64_t(1) << 31) - 65536) return false;  // (a step past the last token stays within 31 bits)
-  // units of work (128 tokens of a sequence, cache head and 16 query heads) counted in 31 bits
-  return B * Hkv * ceil_div(Hq / Hkv, 16) * ceil_div(*reach, 128) < (int64_t(1) << 31);
+  // units of work (128 tokens of a sequence, cache head and 16 query heads, and up to 3 a sequence
+  // more for its start) counted in 31 bits
+  return B * Hkv * ceil_div(Hq / Hkv, 16) * (ceil_div(*reach, 128) + 3) < (int64_t(1) << 31);
 }
 
 fq_status fq_attn_decode_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table,

@@ -291,8 +291,8 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
  * with g = Hq / Hkv (a whole number) query heads sharing a cache head.  q, out FLOAT16 |
  * BFLOAT16 [B, Hq, D] of one dtype (a 16-bit cache must have it too), lengths INT32 [B] (the
  * newest token included; capped at the table's reach), block_table as above, 1 <= Hq <= 65536;
- * reach = the table's width * P < 2^31 - 65536 and B * Hkv * ceilDiv(g, 16) * ceilDiv(reach, 128)
- * < 2^31.
+ * reach = the table's width * P < 2^31 - 65536 and B * Hkv * ceilDiv(g, 16) * (ceilDiv(reach, 128)
+ * + 3) < 2^31.
  * `lse`, when not NULL, is FLOAT32 [B, Hq] (contiguous) and receives log sum_t exp(scale *
  * <q, k[t]>).  A length of 0 (an idle place of a fixed batch) gives zeros and lse = -infinity.
  * A token whose table entry is outside the cache is left out of the sum; cache contents past a
