@@ -3,7 +3,12 @@
 // For a cache head and its g query heads: s[t, h] = <q_h, k_t>, p = softmax over t, o_h = sum_t
 // p[t, h] v_t.  Every cached byte is used for g <= 16 heads at once, so the products run on the
 // matrix cores with the heads as the 16 columns of a tile (heads beyond 16 take further tiles)
-// and the kernel is bound by reading the cache.
+// and the kernel is bound by reading the cache: int8, 8 cache heads of 128, 64 query heads, 64
+// sequences of 1024 to 16384 tokens (756 MB) 151 us, 5.0 TB/s, two of up to 131072 (492 MB) 100 us, 4.9;
+// a large copy moves 5.2.  4 bits are bound by the vector instructions that widen them: 128 sequences
+// (783 MB) 209 us in int4, 187 in E2M1, 3.7 and 4.2 TB/s.  Small calls are a chain of latencies: workgroups
+// start over 2 to 4 us, a run's plan takes 1.5 to 3, its pages and first keys 3, a step of 128 tokens 2 (3 at
+// full bandwidth), the join 5 (37 sequences of up to 2000 tokens, E4M3, 45 MB: 21 us).
 //
 // One wave and 32 tokens (two subtiles of 16), v_mfma_f32_16x16x32:
 //   S^T = K Q^T: the A operand's row is a token, so a lane reads pieces of one key row straight
@@ -28,7 +33,8 @@
 // one in a sequence loses bits in proportion.
 // The weights' rounding would be most of the result's error.  With at most 8 heads in a group the
 // tile has columns to spare: they take the same heads with the remainders w - f16(w) as weights, so
-// the weights count with twice the bits and the matrix cores have no more to do.
+// the weights count with twice the bits and the matrix cores have no more to do.  The remainders go in
+// times 2^11: those of weights below 2^-14, where f16 has fewer bits, keep theirs.
 // Softmax statistics are fp32: the running maximum m (base-2 scores) is only moved when a score
 // passes m + 8 (weights then reach 2^8, far inside f16's range), so the common tile has no
 // cross-lane step and no rescaling.
@@ -226,6 +232,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   constexpr bool kScaled = MODE == kKvInt8 || MODE == kKvE4M3 || MODE == kKvInt4;  // a scale per token
   constexpr int PDT = MODE == kKv16 ? DT : kF16;                                   // operands' type
   constexpr float kCode = MODE == kKvInt8 || MODE == kKvInt4 ? 512.0f : 1.0f;       // 1 / the operand's unit
+  constexpr float kUp = PDT == kF16 ? 2048.0f : 1.0f;                               // of the weights' remainders
   constexpr int LDH = 17;  // row pitch of the output exchange (heads)
   __shared__ float s_o[kWaves][DP * LDH];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
   // ---- this workgroup's run of units
   int u = 0, u_end = 0;  // units from the start of sequence b on
   int b = 0;
-  if (single) {  // every segment is one unit: no plan, no join
+  if (single) {  // a workgroup a segment: no plan, no join
     b = blockIdx.x / per_b;
     u = blockIdx.x - b * per_b;
     u_end = u + 1;
@@ -305,12 +312,12 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       u -= nw * per_b;
       u_end -= nw * per_b;
     }
-    nu = single ? 1 : units_of(n);
+    nu = single ? max(1, units_of(n)) : units_of(n);
     seg = __builtin_amdgcn_readfirstlane(u / nw);
     const int start = single ? 0 : S::start, at = u - seg * nw, take = min(nw - at, u_end - u);
     u += take;
     ua = max(0, at - start);
-    ue = at + take - start;
+    ue = single ? nu : at + take - start;
     // this wave's steps: tokens kUnit (ua + i) + kTile wv ..
     t_first = kUnit * ua + kTile * wv;
     const int t_last = min(n, kUnit * ue);
@@ -414,7 +421,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     // heads again, with what the rounding of the weights left over: their sums are added to the others'.
     const int head = ht * 16 + (two ? r16 & 7 : r16);
     const bool my_head = head < a.g;
-    const float minus = r16 < 8 ? -0.0f : -1.0f;
+    const float up = r16 < 8 ? 1.0f : kUp, minus = r16 < 8 ? -0.0f : -kUp;
 
     // ---- state of the segment
     f32x4_t acc[S::NH][S::EC];
@@ -572,12 +579,12 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       u32x4_t pf;
 #pragma unroll
       for (int i = 0; i < 4; ++i) pf[i] = h2<PDT>(w[2 * i], w[2 * i + 1]);
-      if (two) {  // minus: 1 in the columns of the remainders, else 0
+      if (two) {  // (w - hi) up in the columns of the remainders, else w
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t hi = pf[i];
-          pf[i] = h2<PDT>(__builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi)), minus, w[2 * i]),
-                          __builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi >> 16)), minus, w[2 * i + 1]));
+          pf[i] = h2<PDT>(__builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi)), minus, w[2 * i] * up),
+                          __builtin_fmaf(load16<PDT>(static_cast<uint16_t>(hi >> 16)), minus, w[2 * i + 1] * up));
         }
       }
 #pragma unroll
@@ -702,7 +709,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
         const float x = s_o[w][d * LDH + hd];
         o += x;
         // (a seen infinity: its weight's remainder may be 0 or of the other sign, the sum is that of x)
-        if (two && __builtin_fabsf(x) < kInf) o += s_o[w][d * LDH + hd + 8];
+        if (two && __builtin_fabsf(x) < kInf) o += s_o[w][d * LDH + hd + 8] * (1.0f / kUp);
       }
       const int hq = hk * a.g + ht * 16 + hd;
       if (all) {
@@ -728,8 +735,9 @@ template <int DT, int DP>
 __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, const float* __restrict__ part, int32_t nht,
                                                                int32_t gh, int32_t grid, int32_t start) {
   constexpr int G = kThreads / DP;  // threads that share an element's parts
-  constexpr int kBatch = 8;         // parts of a thread in flight
-  constexpr int kFew = 4;
+  constexpr int kBatch = 8;         // parts of a thread in flight (2: 2 x 131072 tokens 106 us, not 103)
+  constexpr int kFew = 4;           // parts that all elements are joined of at once: 64 x 16384 in int8 160 us
+                                    // by the general loop, 151 so
   __shared__ int32_t s_sum[2][kWaves];
   __shared__ float s_m[G][DP], s_l[G][DP], s_o[G][DP];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -852,6 +860,13 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   }
 }
 
+// Whether a segment is one workgroup's whatever its length, with no plan and no join: a table that
+// reaches 4 units at most, or 8 with a segment for each CU.  us split and joined, and so: one sequence of
+// 250 tokens (8 segments) 10.5 and 7.1, of 510 10.7 and 9.5, of 880 10.7 and 13.0; 32 of up to 500 (256
+// segments) 15.4 and 11.0, up to 1000 18.5 and 16.6, up to 2000 25 and 27; 64 of 1000 33 and 25, of 2000
+// 48 and 43; 37 of up to 1000 with 16 heads 16.6 and 15.1, up to 2000 20.6 and 25.5.
+bool single_of(int64_t segments, int64_t reach) { return reach <= (segments >= 256 ? 8 : 4) * kUnit; }
+
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 template <int MODE, int DT, int DP, bool PAD>
@@ -859,7 +874,7 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   const int nht = (a.g + 15) / 16, gh = a.g < 16 ? a.g : 16;
   const int64_t reach = static_cast<int64_t>(a.bt.width) << a.c.page_log;
   const int64_t segments = static_cast<int64_t>(a.B) * a.c.Hkv * nht;
-  const bool single = reach <= kUnit;
+  const bool single = single_of(segments, reach);
   if (single) {
     decode_kernel<MODE, DT, DP, PAD><<<static_cast<uint32_t>(segments), kThreads, 0, s>>>(a, part, nht, gh, true);
     return hipGetLastError();
@@ -868,7 +883,9 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   decode_kernel<MODE, DT, DP, PAD><<<grid, kThreads, 0, s>>>(a, part, nht, gh, false);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // (enough workgroups of the join to fill the device, at most one a head)
+  // Enough workgroups of the join to fill the device, at most one a head.  us with one a segment, and so:
+  // 2 sequences of up to 131072, 8 heads each on 8: 128 and 103; 16 of up to 8192, 32 heads on 1: 61 and
+  // 26; 8 of up to 1500: 19 and 15; 128 of up to 16384 the same.
   const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
   decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid, Shape<MODE, DP, PAD>::start);
   return hipGetLastError();
@@ -897,8 +914,8 @@ hipError_t by_dtype(const DecodeArgs& a, float* part, hipStream_t s) {
 }  // namespace
 
 uint64_t attn_decode_workspace(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t max_tokens) {
-  if (B == 0 || max_tokens <= kUnit) return 0;
   const int g = Hq / Hkv, gh = g < 16 ? g : 16;
+  if (B == 0 || single_of(static_cast<int64_t>(B) * Hkv * ceil_div(g, 16), max_tokens)) return 0;
   return static_cast<uint64_t>(kMaxGrid) * 2 * gh * (padded(D) + 2) * sizeof(float);
 }
 

@@ -24,6 +24,21 @@
 // A weight of 0 times an infinite or NaN value of a hidden key in a partly masked tile is NaN.
 // The walk ignores that; if a result is not finite, the workgroup walks again, this time taking
 // such values out of the masked tiles' products and adding them to the rows that do see them.
+//
+// What bounds it: one 32768-row prompt, 8 heads on one cache head of 128, takes 2.0 ms (1.10 to 1.17
+// PFLOP/s; a large library product reaches 1.25 to 1.39 here) with the matrix cores busy 61% of the
+// time at a clock of 1.80 GHz, which the power of products, LDS reads, copies and exponentials together
+// sets: without any one of them the rate is 1.25 to 1.27, without all but the products 1.67.  Smaller
+// calls run at 2.0 GHz and 47%: nine packed prompts of 242 to 4096 rows, 32 heads, 315 us (905 TFLOP/s),
+// where a workgroup spends 3.4 us before its first and after its last tile each (places, query rows,
+// rows out) and 1.76 us a tile; four chunks of 313 to 1024 rows behind 2507 to 8192 keys, 215 us (855),
+// where the device's 512 places are 81% busy, the longest walk being 133 tiles and the mean 97.
+// Tile and schedule, TFLOP/s on those three (prompt, packed, chunks) and 2 x 8192 rows of 64:
+//   128 rows, 4 waves (this)                                          1128  867  669*  826
+//   256 rows, 8 waves                                                 1167  847  611*  795
+//   64 rows a wave, each LDS fragment for two products, 1 wave a SIMD  221  179  144   511
+//   scores of the next 32 keys under the softmax of these              1015  811  800   758  (this: 1077 887 855 870)
+// (*: before walks were ordered by length.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -36,7 +51,7 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
-constexpr int kAhead = 4;           // fragments read ahead of their products
+constexpr int kAhead = 4;           // fragments read ahead of their products (2, 6 and 8: the same to 2% slower)
 constexpr int kMaxParts = 8, kMinChunk = 16, kEnough = 512;  // see parts_of()
 constexpr float kLazy = 8.0f;
 constexpr float kInf = __builtin_inff();
@@ -67,9 +82,10 @@ __device__ __forceinline__ i32x4_t rsrc4(const void* p, uint32_t bytes) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // One LDS-DMA load: lane l's 16 bytes at rs + voff go to LDS lds + 16 l.  (As inline assembly: the
-// compiler would wait for every such load before any LDS read.)
+// compiler would wait for every such load before any LDS read.  A load that takes its place from m0
+// needs one wait state after m0's write.)
 __device__ __forceinline__ void dma16(uint32_t lds, uint32_t voff, i32x4_t rs) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

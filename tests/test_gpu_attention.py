@@ -95,6 +95,24 @@ def test_decode_split_over_the_length(mode):
     _decode([5000, 1, 0, 2500], 8, 2, 128, 64, mode, "bf16", seed=3)
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("Hq,H,D,P", [(4, 4, 64, 16), (14, 2, 96, 16), (3, 3, 256, 64), (20, 1, 128, 128), (5, 1, 160, 16), (8, 8, 128, 32)])
+def test_decode_split_with_short_sequences_between(mode, Hq, H, D, P):
+    """A table too long for a workgroup a sequence: sequences of one to nineteen units, split at any place, whole ones and
+    empty ones between them."""
+    say(f"[gpu] decode split {mode} Hq={Hq} H={H} D={D} P={P}")
+    _decode([640, 1, 0, 129, 300, 2400, 17, 128, 0, 33, 1025, 2], Hq, H, D, P, mode, "bf16", seed=11)
+
+
+@pytest.mark.parametrize("mode,H,D", [("same", 8, 64), ("int8", 16, 128), ("e4m3", 8, 64), ("int4", 8, 128), ("fp4", 8, 32)])
+@pytest.mark.parametrize("most", [1000, 1100])
+def test_decode_of_many_sequences(mode, H, D, most):
+    """More sequences and heads than there are CUs, below and above the length up to which each is one workgroup's."""
+    say(f"[gpu] decode many {mode} H={H} D={D} most={most}")
+    lens = [(most * (i * i + 1) // 1090) % (most + 1) for i in range(33)] + [most]
+    _decode(lens, 2 * H, H, D, 16, mode, "f16", seed=12)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("D", [8, 24, 40, 112, 200])
 def test_decode_odd_head_sizes(dt, D):
