@@ -52,7 +52,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kAhead = 4;           // fragments read ahead of their products (2, 6 and 8: the same to 2% slower)
-constexpr int kMaxParts = 8, kMinChunk = 16, kEnough = 512;  // see parts_of()
+constexpr int kMaxParts = 32, kMinChunk = 8, kEnough = 512;  // see parts_of()
 constexpr float kLazy = 8.0f;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
@@ -448,8 +448,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
   }
 }
 
-// Joins the parts of the walks that were split: a workgroup per 128 rows and head, a thread per
-// row and half of the elements.
+// Joins the parts of the walks that were split: a workgroup per 128 rows, head and 32 elements, a thread
+// per row and 16 elements.
 template <int DT, int DP>
 __global__ __launch_bounds__(kThreads) void prefill_join_kernel(PrefillArgs a, int parts, const float* __restrict__ ws) {
   const Place pl = place_of(a, blockIdx.x, parts);
@@ -457,36 +457,37 @@ __global__ __launch_bounds__(kThreads) void prefill_join_kernel(PrefillArgs a, i
   const int tiles = key_tiles(a, pl.lk - pl.lq, pl.lk, pl.lq, pl.tile);
   if (tiles <= pl.chunk) return;
   const int n = (tiles + pl.chunk - 1) / pl.chunk;
-  const int r = threadIdx.x % kRows, hf = threadIdx.x / kRows, row = pl.tile * kRows + r;
-  if (row >= pl.lq) return;
+  const int r = threadIdx.x % kRows, row = pl.tile * kRows + r, e = 32 * blockIdx.y + 16 * (threadIdx.x / kRows);
+  if (row >= pl.lq || e >= a.D) return;
   // part i of this workgroup's rows was number (rank parts + i) Hq + head's place of the first launch
   const int64_t first = static_cast<int64_t>(blockIdx.x / a.Hq) * parts * a.Hq + blockIdx.x % a.Hq;
-  auto at = [&](int i) { return ws + (first + static_cast<int64_t>(i) * a.Hq) * ((DP + 2) * kRows) + r; };
-  float m = -kInf, l = 0.0f, f[kMaxParts];
-  for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[DP * kRows]);
+  const float* p = ws + first * ((DP + 2) * kRows) + r;
+  float m = -kInf, l = 0.0f, o[16];
 #pragma unroll
-  for (int i = 0; i < kMaxParts; ++i) {
-    if (i >= n) break;
-    const float mi = at(i)[DP * kRows], li = at(i)[(DP + 1) * kRows];
-    f[i] = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
-    if (li != 0.0f) l += li * f[i];  // (nothing seen, or NaN)
+  for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+  for (int i = 0; i < n; ++i, p += static_cast<int64_t>(a.Hq) * ((DP + 2) * kRows)) {
+    const float mi = p[DP * kRows], li = p[(DP + 1) * kRows];
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = p[(e + j) * kRows];
+    const float mn = fmaxf(m, mi);
+    const float f0 = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn), f1 = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - mn);
+    m = mn;
+    l = li == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li * f1);  // (nothing seen, or NaN)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = __builtin_fmaf(o[j], f0, x[j] * f1);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* const out = a.out.p + (pl.q0 + row) * a.out.row + pl.head * a.out.head;
-  for (int e = 8 * hf; e < a.D; e += 16) {
-    float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  uint16_t* const out = a.out.p + (pl.q0 + row) * a.out.row + pl.head * a.out.head + e;
 #pragma unroll
-    for (int i = 0; i < kMaxParts; ++i) {
-      if (i >= n) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf(at(i)[(e + j) * kRows], f[i], o[j]);
-    }
+  for (int h = 0; h < 2; ++h) {
+    if (e + 8 * h >= a.D) break;
     u32x4_t w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = round16x2<DT>(o[2 * j] * inv, o[2 * j + 1] * inv);
-    *reinterpret_cast<u32x4_t*>(out + e) = w;
+    for (int j = 0; j < 4; ++j) w[j] = round16x2<DT>(o[8 * h + 2 * j] * inv, o[8 * h + 2 * j + 1] * inv);
+    *reinterpret_cast<u32x4_t*>(out + 8 * h) = w;
   }
-  if (a.lse && hf == 0)
+  if (a.lse && e == 0)
     a.lse[static_cast<int64_t>(pl.q0 + row) * a.Hq + pl.head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
 }
 
@@ -496,15 +497,18 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 int64_t workgroups(int64_t Tq, int64_t B, int64_t Hq) { return (Tq / kRows + B) * Hq; }
 
 // Parts that the longest walk may be cut into.  The device runs 512 workgroups at a time (two a CU);
-// with fewer, the longest walk alone is the whole time.  128 rows behind 32768 keys, 32 heads (64
-// workgroups): 546 us in one part, 125 in 8; 512 behind 16384, 64 heads (320): 315 against 281.  A
-// part's sums go through memory (66 KB at 128), so nothing is split once the device is full: chunks
-// of 313 to 1024 rows behind up to 8192 keys, 32 heads (736): 204 whole, 227 in two parts, 261 in
-// three.  Nor is a walk of 16 tiles, which takes as long as a join: 1024 rows, 8 heads 23 and 28 us.
+// with fewer, the longest walk alone is the whole time.  us in up to 8, 16, 32 and 64 parts: 128 rows
+// behind 32768 keys, 32 heads (64 workgroups) 97, 96, 96, 96 (546 in one); 64 rows, 8 heads 82, 53, 46, 46;
+// 16 rows behind 131072, 8 heads 284, 157, 105, 124.  In one part and so: 512 rows behind 16384, 64 heads (320)
+// 315 and 281.  A part's sums go through memory (66 KB at 128), so nothing is split once the device is full:
+// chunks of 313 to 1024 rows behind up to 8192 keys, 32 heads (736): 204 whole, 227 in two parts, 261 in three
+// (cut at the mean load alone 226; dealt out in equal runs 241, as walks that no longer go side by side
+// share fewer keys in L2).  Parts of 8 tiles at least: 1024 rows, 8 heads 19 us, of 16 tiles 23.  Few keys
+// for so many sequences are short walks, which a second launch would only hold up.
 int parts_of(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, bool causal) {
   const int64_t w = workgroups(Tq, B, Hq);
-  if (!causal || B > 64 || w >= kEnough) return 1;
-  return static_cast<int>(std::min({int64_t(kMaxParts), (kEnough + w - 1) / w, std::max(int64_t(1), ceil_div(Tk, kKeys * kMinChunk))}));
+  if (!causal || B > 64 || w >= kEnough || Tk <= kKeys * kMinChunk * std::min<int64_t>(B, 4)) return 1;
+  return static_cast<int>(std::min({int64_t(kMaxParts), ceil_div(kEnough, w), ceil_div(Tk, kKeys * kMinChunk)}));
 }
 
 template <int DT, int DP, bool PAD>
@@ -514,7 +518,7 @@ hipError_t go(const PrefillArgs& a, float* ws, hipStream_t s) {
   prefill_kernel<DT, DP, PAD><<<static_cast<uint32_t>(w * parts), kThreads, 0, s>>>(a, parts, ws);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || parts == 1) return err;
-  prefill_join_kernel<DT, DP><<<static_cast<uint32_t>(w), kThreads, 0, s>>>(a, parts, ws);
+  prefill_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(w), static_cast<uint32_t>(ceil_div(a.D, 32))), kThreads, 0, s>>>(a, parts, ws);
   return hipGetLastError();
 }
 

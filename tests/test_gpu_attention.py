@@ -339,6 +339,15 @@ def test_prefill_strided_rows_of_a_fused_projection():
     assert torch.equal(fq.attn_prefill(qh, kh, vh, cu), a)
 
 
+@pytest.mark.parametrize("D", [64, 128, 200])
+@pytest.mark.parametrize("lq,lk", [([3], [20000]), ([1, 130, 2], [17000, 300, 9]), ([40], [600]), ([0, 150, 1], [0, 100, 4100])])
+def test_prefill_few_rows_behind_many_keys(lq, lk, D):
+    """Walks cut into up to 32 parts of 8 tiles and joined, with short and empty ones, and rows that see nothing, beside them."""
+    say(f"[gpu] prefill {lq} over {lk} D={D}")
+    _prefill(lq, lk, 4, 2, D, "bf16", seed=9)
+    _prefill(lq, lk, 3, 1, D, "f16", seed=10)
+
+
 def test_prefill_future_infinities_and_nan_stay_hidden():
     """Keys and values after a row, and other sequences' rows, never reach it, whatever they hold."""
     g = torch.Generator().manual_seed(5)
