@@ -70,7 +70,7 @@ struct PrefillArgs {
   int32_t B, Tq, Tk, Hq, g, D, dtype, causal;
   float scale;
 };
-uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D, bool causal);
+uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D);
 hipError_t launch_attn_prefill(const PrefillArgs& a, void* ws, hipStream_t s);
 
 }  // namespace fq

@@ -267,12 +267,12 @@ static bool prefill_sizes(const fq_tensor* q, const fq_tensor* k, const fq_tenso
          (Tq / 128 + B) * Hq < (int64_t(1) << 28);  // workgroups (a row tile and head each), cut into up to 8 parts
 }
 
-fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t causal,
+fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t /*causal*/,
                                              uint64_t* workspaceSize) {
   clear_last_error();
   if (!q || !k || !cu_q || !workspaceSize) return FQ_ERR_PARAM_NULLPTR;
   if (!prefill_sizes(q, k, cu_q)) return FQ_ERR_PARAM_INVALID;
-  *workspaceSize = attn_prefill_workspace(q->shape[0], k->shape[0], cu_q->shape[0] - 1, q->shape[1], q->shape[2], causal != 0);
+  *workspaceSize = attn_prefill_workspace(q->shape[0], k->shape[0], cu_q->shape[0] - 1, q->shape[1], q->shape[2]);
   return FQ_SUCCESS;
 }
 
@@ -294,7 +294,7 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
     return FQ_ERR_PARAM_INVALID;
   // a tile of 64 key rows within 31-bit offsets
   if (Tk > 1 && (k->strides[0] > (int64_t(1) << 23) || v->strides[0] > (int64_t(1) << 23))) return FQ_ERR_PARAM_INVALID;
-  const uint64_t need = attn_prefill_workspace(Tq, Tk, B, Hq, D, causal != 0);
+  const uint64_t need = attn_prefill_workspace(Tq, Tk, B, Hq, D);
   if (need > 0 && !workspace) return FQ_ERR_PARAM_NULLPTR;
   if (workspaceSize < need || (need > 0 && !aligned(workspace, 16))) return FQ_ERR_PARAM_INVALID;
   if (Tq == 0) return FQ_SUCCESS;

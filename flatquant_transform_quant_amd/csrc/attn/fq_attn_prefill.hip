@@ -170,6 +170,7 @@ __device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int part
       kn = max(0, min(a.cu_k[b + 1], a.Tk) - ks);
     }
     const int nt = (n + kRows - 1) / kRows;
+    if (parts > 1) p.chunk = max(kMinChunk, (wave_top(nt > 0 ? key_tiles(a, kn - n, kn, n, nt - 1) : 0) + parts - 1) / parts);
     int w;
     if (a.causal && a.B <= 64) {
       const int total = wave_total(nt);
@@ -178,7 +179,6 @@ __device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int part
       auto above = [&](int level) { return max(0, min(nt, first + nt - level)); };  // this sequence's tiles at or above
       int lo = 0, hi = 1 << 24;  // tiles at or above lo: more than rank; at or above hi: not
       hi = wave_top(first + nt);
-      if (parts > 1) p.chunk = max(kMinChunk, (wave_top(nt > 0 ? key_tiles(a, kn - n, kn, n, nt - 1) : 0) + parts - 1) / parts);
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (wave_total(above(mid)) > rank) lo = mid; else hi = mid;
@@ -505,16 +505,16 @@ int64_t workgroups(int64_t Tq, int64_t B, int64_t Hq) { return (Tq / kRows + B) 
 // (cut at the mean load alone 226; dealt out in equal runs 241, as walks that no longer go side by side
 // share fewer keys in L2).  Parts of 8 tiles at least: 1024 rows, 8 heads 19 us, of 16 tiles 23.  Few keys
 // for so many sequences are short walks, which a second launch would only hold up.
-int parts_of(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, bool causal) {
+int parts_of(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq) {
   const int64_t w = workgroups(Tq, B, Hq);
-  if (!causal || B > 64 || w >= kEnough || Tk <= kKeys * kMinChunk * std::min<int64_t>(B, 4)) return 1;
+  if (B > 64 || w >= kEnough || Tk <= kKeys * kMinChunk * std::min<int64_t>(B, 4)) return 1;
   return static_cast<int>(std::min({int64_t(kMaxParts), ceil_div(kEnough, w), ceil_div(Tk, kKeys * kMinChunk)}));
 }
 
 template <int DT, int DP, bool PAD>
 hipError_t go(const PrefillArgs& a, float* ws, hipStream_t s) {
   const int64_t w = workgroups(a.Tq, a.B, a.Hq);
-  const int parts = parts_of(a.Tq, a.Tk, a.B, a.Hq, a.causal);
+  const int parts = parts_of(a.Tq, a.Tk, a.B, a.Hq);
   prefill_kernel<DT, DP, PAD><<<static_cast<uint32_t>(w * parts), kThreads, 0, s>>>(a, parts, ws);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || parts == 1) return err;
@@ -533,8 +533,8 @@ hipError_t by_size(const PrefillArgs& a, float* ws, hipStream_t s) {
 
 }  // namespace
 
-uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D, bool causal) {
-  const int parts = Tq == 0 ? 1 : parts_of(Tq, Tk, B, Hq, causal);
+uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D) {
+  const int parts = Tq == 0 ? 1 : parts_of(Tq, Tk, B, Hq);
   if (parts == 1) return 0;
   return static_cast<uint64_t>(workgroups(Tq, B, Hq)) * parts * (padded(static_cast<int>(D)) + 2) * kRows * sizeof(float);
 }

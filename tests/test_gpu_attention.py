@@ -346,6 +346,7 @@ def test_prefill_few_rows_behind_many_keys(lq, lk, D):
     say(f"[gpu] prefill {lq} over {lk} D={D}")
     _prefill(lq, lk, 4, 2, D, "bf16", seed=9)
     _prefill(lq, lk, 3, 1, D, "f16", seed=10)
+    _prefill(lq, lk, 4, 2, D, "f16", causal=False, seed=11)
 
 
 def test_prefill_future_infinities_and_nan_stay_hidden():
