@@ -253,6 +253,17 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     b = blockIdx.x / per_b;
     u = blockIdx.x - b * per_b;
     u_end = u + 1;
+  } else if (a.B <= 64) {  // the plan below with a sequence a lane, by each wave for itself (1 us less a call)
+    const int32_t n = lane < a.B ? length_of(a, lane) : 0;
+    s_len[lane] = n;
+    const int weight = weight_of(n, S::start), incl = wave_scan(weight);
+    const Runs run(__builtin_amdgcn_readlane(incl, 63) * per_b, gridDim.x);
+    if (blockIdx.x >= run.runs) return;
+    const int first = __builtin_amdgcn_readfirstlane(run.start(blockIdx.x)), last = __builtin_amdgcn_readfirstlane(run.start(blockIdx.x + 1));
+    b = __builtin_ctzll(__ballot(incl * per_b > first));
+    const int at = __builtin_amdgcn_readlane(incl - weight, b) * per_b;
+    u = first - at;
+    u_end = last - at;
   } else {
     // the units of all sequences, then the sequence that holds the first unit: scans over the
     // lengths, 256 at a time; the first pass over them keeps the first scan
@@ -730,44 +741,53 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 }
 
 // Joins the parts of the segments that were split, and writes the rows of empty sequences.  One
-// workgroup per segment and, with gridDim.y > 1, every gridDim.y-th of its heads.
+// workgroup per segment and, with gridDim.y > 1, every gridDim.y-th of its heads; with gridDim.z > 1 that
+// part of the elements, whose threads then share the parts among more groups.
 template <int DT, int DP>
 __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, const float* __restrict__ part, int32_t nht,
                                                                int32_t gh, int32_t grid, int32_t start) {
-  constexpr int G = kThreads / DP;  // threads that share an element's parts
+  const int E = DP / gridDim.z, G = kThreads / E;  // its elements; threads that share an element's parts
   constexpr int kBatch = 8;         // parts of a thread in flight (2: 2 x 131072 tokens 106 us, not 103)
   constexpr int kFew = 4;           // parts that all elements are joined of at once: 64 x 16384 in int8 160 us
                                     // by the general loop, 151 so
   __shared__ int32_t s_sum[2][kWaves];
-  __shared__ float s_m[G][DP], s_l[G][DP], s_o[G][DP];
+  __shared__ float s_m[kThreads], s_l[kThreads], s_o[kThreads];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int per_b = a.c.Hkv * nht, D = a.c.D;
   const int b = blockIdx.x / per_b, seg = blockIdx.x - b * per_b, hk = seg / nht, ht = seg - hk * nht;
   const int heads = min(16, a.g - ht * 16);
-  const int d = tid % DP, gr = tid / DP;
+  const int at = tid & (E - 1), d = E * blockIdx.z + at, gr = tid / E;
   const int32_t n = length_of(a, b);
-  int sum = 0, before = 0;
-  for (int i = tid; i < a.B; i += kThreads) {
-    const int k = weight_of(length_of(a, i), start);
-    sum += k;
-    if (i < b) before += k;
+  int sum = 0, before = 0;  // of all sequences, of those before b
+  if (a.B <= 64) {
+    const int weight = lane < a.B ? weight_of(length_of(a, lane), start) : 0, incl = wave_scan(weight);
+    sum = __builtin_amdgcn_readlane(incl, 63);
+    before = __builtin_amdgcn_readlane(incl - weight, b);
+  } else {
+    for (int i = tid; i < a.B; i += kThreads) {
+      const int k = weight_of(length_of(a, i), start);
+      sum += k;
+      if (i < b) before += k;
+    }
+    sum = wave_scan(sum);
+    before = wave_scan(before);
+    if (lane == 63) {
+      s_sum[0][wv] = sum;
+      s_sum[1][wv] = before;
+    }
+    __syncthreads();
+    sum = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
+    before = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
   }
   for (int hd = blockIdx.y; n == 0 && hd < heads; hd += gridDim.y) {
     const int hq = hk * a.g + ht * 16 + hd;
     if (gr == 0 && d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = 0;
-    if (a.lse && tid == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
+    if (a.lse && gr == 0 && d == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = -kInf;
   }
   if (n == 0) return;
-  sum = wave_scan(sum);
-  before = wave_scan(before);
-  if (lane == 63) {
-    s_sum[0][wv] = sum;
-    s_sum[1][wv] = before;
-  }
-  __syncthreads();
-  const Runs run((s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3]) * per_b, grid);
+  const Runs run(sum * per_b, grid);
   const int nw = weight_of(n, start);
-  const uint32_t ua = (s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3]) * per_b + seg * nw;
+  const uint32_t ua = before * per_b + seg * nw;
   const int i0 = run.of(ua + start), i1 = run.of(ua + nw - 1);
   if (i0 == i1) return;  // one workgroup had it all and wrote the rows
   const int np = i1 - i0 + 1;
@@ -776,6 +796,7 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
   const float* const p0 = part + (static_cast<int64_t>(i0) * 2 + (run.start(i0) < ua ? 1 : 0)) * pitch;
   const float* const p1 = part + static_cast<int64_t>(i0) * 2 * pitch;  // + 2 i pitch for run i0 + i
   if (np <= kFew) {  // (short segments: all parts of four elements of a thread in flight)
+    if (blockIdx.z > 0) return;
     for (int e0 = blockIdx.y * 4 * kThreads + tid; e0 < heads * DP; e0 += gridDim.y * 4 * kThreads) {
       float pm[4][kFew], pl[4][kFew], po[4][kFew];
 #pragma unroll
@@ -835,27 +856,25 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
       }
       m = mn;
     }
-    if constexpr (G > 1) {
-      s_m[gr][d] = m;
-      s_l[gr][d] = l;
-      s_o[gr][d] = o;
+    if (G > 1) {
+      s_m[tid] = m;
+      s_l[tid] = l;
+      s_o[tid] = o;
       __syncthreads();
       float mn = m;
-#pragma unroll
-      for (int g = 0; g < G; ++g) mn = fmaxf(mn, s_m[g][d]);
+      for (int g = 0; g < G; ++g) mn = fmaxf(mn, s_m[g * E + at]);
       l = o = 0.0f;
-#pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float w = s_m[g][d] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(s_m[g][d] - mn);
-        l += s_l[g][d] * w;
-        o += s_o[g][d] * w;
+        const float mg = s_m[g * E + at], w = mg == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mg - mn);
+        l += s_l[g * E + at] * w;
+        o += s_o[g * E + at] * w;
       }
       m = mn;
       __syncthreads();
     }
     const int hq = hk * a.g + ht * 16 + hd;
     if (gr == 0 && d < D) a.out.p[b * a.out.row + hq * a.out.head + d] = round16<DT>(l == 0.0f ? 0.0f : o / l);
-    if (a.lse && tid == 0)
+    if (a.lse && gr == 0 && d == 0)
       a.lse[static_cast<int64_t>(b) * a.Hq + hq] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
   }
 }
@@ -887,7 +906,12 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   // 2 sequences of up to 131072, 8 heads each on 8: 128 and 103; 16 of up to 8192, 32 heads on 1: 61 and
   // 26; 8 of up to 1500: 19 and 15; 128 of up to 16384 the same.
   const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
-  decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny), kThreads, 0, s>>>(a, part, nht, gh, grid, Shape<MODE, DP, PAD>::start);
+  // And where that leaves few, slices of 16 elements at least: one sequence of 131072 tokens, 8 heads on 1, 74
+  // us whole and 25 so, of 8192, 32 on 8, 18.6 and 15.4; the two of up to 131072 103 and 101; 8 of up to 1500
+  // 14.5 and 14.6 (15.1 at 512 workgroups).
+  uint32_t nz = 1;
+  while (nz < DP / 16 && segments * ny * nz * 2 <= 256) nz *= 2;
+  decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny, nz), kThreads, 0, s>>>(a, part, nht, gh, grid, Shape<MODE, DP, PAD>::start);
   return hipGetLastError();
 }
 

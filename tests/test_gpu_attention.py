@@ -104,6 +104,14 @@ def test_decode_split_with_short_sequences_between(mode, Hq, H, D, P):
     _decode([640, 1, 0, 129, 300, 2400, 17, 128, 0, 33, 1025, 2], Hq, H, D, P, mode, "bf16", seed=11)
 
 
+@pytest.mark.parametrize("mode,Hq,H,D", [("same", 8, 1, 64), ("int8", 4, 2, 128), ("int4", 3, 1, 96), ("e4m3", 17, 1, 256), ("fp4", 2, 1, 128)])
+def test_decode_of_one_long_sequence(mode, Hq, H, D):
+    """More parts than a join takes at once, with its elements in slices; and a batch past 64, planned by whole workgroups."""
+    say(f"[gpu] decode one long {mode} Hq={Hq} H={H} D={D}")
+    _decode([9001], Hq, H, D, 32, mode, "bf16", seed=13)
+    _decode([4100] + [0, 3, 130] * 25, Hq, H, D, 32, mode, "f16", seed=14)
+
+
 @pytest.mark.parametrize("mode,H,D", [("same", 8, 64), ("int8", 16, 128), ("e4m3", 8, 64), ("int4", 8, 128), ("fp4", 8, 32)])
 @pytest.mark.parametrize("most", [1000, 1100])
 def test_decode_of_many_sequences(mode, H, D, most):
