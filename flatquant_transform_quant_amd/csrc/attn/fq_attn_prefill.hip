@@ -503,12 +503,15 @@ int64_t workgroups(int64_t Tq, int64_t B, int64_t Hq) { return (Tq / kRows + B) 
 // 315 and 281.  A part's sums go through memory (66 KB at 128), so nothing is split once the device is full:
 // chunks of 313 to 1024 rows behind up to 8192 keys, 32 heads (736): 204 whole, 227 in two parts, 261 in three
 // (cut at the mean load alone 226; dealt out in equal runs 241, as walks that no longer go side by side
-// share fewer keys in L2).  Parts of 8 tiles at least: 1024 rows, 8 heads 19 us, of 16 tiles 23.  Few keys
-// for so many sequences are short walks, which a second launch would only hold up.
+// share fewer keys in L2).  Parts of 8 tiles at least: 1024 rows, 8 heads 19 us, of 16 tiles 23.  Where two
+// a CU would be shorter, one a CU: 1000 rows, 32 heads 26 us, in two parts each 31; 1855, 8 heads of 256 43
+// and 63; 200 behind 2800, 32 heads 28 and 31.  Few keys for so many sequences are short walks, which a
+// second launch would only hold up.
 int parts_of(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq) {
   const int64_t w = workgroups(Tq, B, Hq);
   if (B > 64 || w >= kEnough || Tk <= kKeys * kMinChunk * std::min<int64_t>(B, 4)) return 1;
-  return static_cast<int>(std::min({int64_t(kMaxParts), ceil_div(kEnough, w), ceil_div(Tk, kKeys * kMinChunk)}));
+  const int64_t two = ceil_div(kEnough, w), one = ceil_div(kEnough / 2, w), least = Tk / (kKeys * kMinChunk);
+  return static_cast<int>(std::min(int64_t(kMaxParts), std::max(int64_t(1), two <= least ? two : std::min(one, least + 1))));
 }
 
 template <int DT, int DP, bool PAD>
