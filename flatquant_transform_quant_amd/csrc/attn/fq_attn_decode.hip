@@ -4,11 +4,11 @@
 // p[t, h] v_t.  Every cached byte is used for g <= 16 heads at once, so the products run on the
 // matrix cores with the heads as the 16 columns of a tile (heads beyond 16 take further tiles)
 // and the kernel is bound by reading the cache: int8, 8 cache heads of 128, 64 query heads, 64
-// sequences of 1024 to 16384 tokens (756 MB) 151 us, 5.0 TB/s, two of up to 131072 (492 MB) 100 us, 4.9;
+// sequences of 1024 to 16384 tokens (756 MB) 151 us, 5.0 TB/s, two of up to 131072 (492 MB) 97 us, 5.0;
 // a large copy moves 5.2.  4 bits are bound by the vector instructions that widen them: 128 sequences
 // (783 MB) 209 us in int4, 187 in E2M1, 3.7 and 4.2 TB/s.  Small calls are a chain of latencies: workgroups
 // start over 2 to 4 us, a run's plan takes 1.5 to 3, its pages and first keys 3, a step of 128 tokens 2 (3 at
-// full bandwidth), the join 5 (37 sequences of up to 2000 tokens, E4M3, 45 MB: 21 us).
+// full bandwidth), the join 5 (37 sequences of up to 2000 tokens, E4M3, 39 MB: 20.4 us).
 //
 // One wave and 32 tokens (two subtiles of 16), v_mfma_f32_16x16x32:
 //   S^T = K Q^T: the A operand's row is a token, so a lane reads pieces of one key row straight

@@ -25,8 +25,8 @@
 // The walk ignores that; if a result is not finite, the workgroup walks again, this time taking
 // such values out of the masked tiles' products and adding them to the rows that do see them.
 //
-// What bounds it: one 32768-row prompt, 8 heads on one cache head of 128, takes 2.0 ms (1.10 to 1.17
-// PFLOP/s; a large library product reaches 1.25 to 1.39 here) with the matrix cores busy 61% of the
+// What bounds it: one 32768-row prompt, 8 heads on one cache head of 128, takes 1.93 to 2.03 ms (1.08 to
+// 1.14 PFLOP/s; a large library product reaches 1.25 to 1.39 here) with the matrix cores busy 61% of the
 // time at a clock of 1.80 GHz, which the power of products, LDS reads, copies and exponentials together
 // sets: without any one of them the rate is 1.25 to 1.27, without all but the products 1.67.  Smaller
 // calls run at 2.0 GHz and 47%: nine packed prompts of 242 to 4096 rows, 32 heads, 315 us (905 TFLOP/s),
