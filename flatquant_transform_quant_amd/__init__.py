@@ -504,15 +504,27 @@ class KVCache:
     scales; ``int8`` torch.int8 and ``e4m3`` torch.float8_e4m3fn (or uint8) [pages, Hkv, P, D],
     ``int4`` uint8 [pages, Hkv, P, D/2], each with float32 scales [pages, Hkv, P]; ``fp4`` uint8
     [pages, Hkv, P, D/2] with uint8 e8m0 scales [pages, Hkv, P, 2 * ceilDiv(D, 64)].  The
-    first dimension may be strided (both sides in one allocation)."""
+    first dimension may be strided (both sides in one allocation).
+
+    ``k``, ``v``, ``k_scale`` and ``v_scale`` are the tensors it was made of and cannot be replaced (other
+    tensors are another cache); memory that one of them moves to (``resize_``, ``set_``) is followed."""
 
     def __init__(self, mode: str, k, v, k_scale=None, v_scale=None):
         if mode not in KV_MODES:
             raise ValueError(f"unknown cache mode {mode!r}")
-        torch = _torch()
         _same_device(k, v, k_scale, v_scale)
-        self.mode, self.k, self.v, self.k_scale, self.v_scale = mode, k, v, k_scale, v_scale
-        self.device = k.device
+        self.mode, self.device = mode, k.device
+        self._tensors = (k, v, k_scale, v_scale)
+        self._describe()
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+
+    def _describe(self):
+        torch = _torch()
+        mode, (k, v, k_scale, v_scale) = self.mode, self._tensors
         codes = {"f16": (torch.float16,), "bf16": (torch.bfloat16,), "int8": (torch.int8, torch.uint8),
                  "e4m3": (torch.float8_e4m3fn, torch.uint8)}.get(mode, (torch.uint8,))
         scales = None if mode in ("f16", "bf16") else torch.uint8 if mode == "fp4" else torch.float32
@@ -529,10 +541,22 @@ class KVCache:
                 st = [2 * n for n in st[:3]] + [1 if st[3] == 1 else 2 * st[3]]
             return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _Desc(s.data_ptr(), sdt, s.shape, s.stride())
 
+        at = self._addresses()
         (self._kc, self._ks), (self._vc, self._vs) = side(k, k_scale), side(v, v_scale)
         self.pages, self.heads, self.page_size = k.shape[:3]
         self.head_dim = k.shape[3] * (2 if mode in ("int4", "fp4") else 1)
         self._ptrs = (self._kc.ptr, self._ks.ptr if self._ks else None, self._vc.ptr, self._vs.ptr if self._vs else None)
+        self._at = at
+
+    def _addresses(self):
+        k, v, ks, vs = self._tensors
+        return k.data_ptr(), v.data_ptr(), None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr()
+
+    def _args(self):
+        """Addresses of the four descriptors of a call (built anew where a tensor's memory has moved)."""
+        if self._addresses() != self._at:
+            self._describe()
+        return self._ptrs
 
 
 def empty_kv_cache(pages: int, heads: int, page_size: int, head_dim: int, mode: str, device="cuda") -> KVCache:
@@ -559,7 +583,7 @@ def kv_write(cache: KVCache, k, v, slots, clip_ratio: float = 1.0, dst_type_max:
     page * page_size + offset; negative: not written)."""
     _same_device(cache.k, k, v, slots)
     d = _Descs(k, v, slots)
-    _call(lib.fq_kv_write, "fq_kv_write", cache.device, *d.ptrs, clip_ratio, dst_type_max, *cache._ptrs, _stream(stream, cache.device))
+    _call(lib.fq_kv_write, "fq_kv_write", cache.device, *d.ptrs, clip_ratio, dst_type_max, *cache._args(), _stream(stream, cache.device))
 
 
 def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=None, v_out=None, stream=None):
@@ -578,7 +602,7 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
         raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
     _same_device(cache.k, block_table, cu_seqlens, k_out, v_out)
     d = _Descs(block_table, cu_seqlens, k_out, v_out)
-    _call(lib.fq_kv_read, "fq_kv_read", cache.device, *cache._ptrs, *d.ptrs, _stream(stream, cache.device))
+    _call(lib.fq_kv_read, "fq_kv_read", cache.device, *cache._args(), *d.ptrs, _stream(stream, cache.device))
     return k_out, v_out
 
 
@@ -611,9 +635,10 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
     _same_device(cache.k, q, block_table, lengths, out, lse, workspace)
     d = _Descs(q, block_table, lengths, out, lse)
     qp, bp, lp, op, sp = d.ptrs
+    held = cache._args()
     ws, ptr, size = _workspace(lib.fq_attn_decode_get_workspace_size, "fq_attn_decode_get_workspace_size", cache.device, stream,
-                               workspace, qp, cache._kc.ptr, bp)
-    _call(lib.fq_attn_decode, "fq_attn_decode", cache.device, qp, *cache._ptrs, bp, lp, scale, op, sp, ptr, size,
+                               workspace, qp, held[0], bp)
+    _call(lib.fq_attn_decode, "fq_attn_decode", cache.device, qp, *held, bp, lp, scale, op, sp, ptr, size,
           _stream(stream, cache.device))
     return out
 
@@ -621,7 +646,7 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
 def attn_decode_workspace_size(q, cache: KVCache, block_table) -> int:
     size = ctypes.c_uint64(0)
     d = _Descs(q, block_table)
-    st = lib.fq_attn_decode_get_workspace_size(d.ptrs[0], cache._kc.ptr, d.ptrs[1], ctypes.byref(size))
+    st = lib.fq_attn_decode_get_workspace_size(d.ptrs[0], cache._args()[0], d.ptrs[1], ctypes.byref(size))
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_attn_decode_get_workspace_size")
     return size.value
