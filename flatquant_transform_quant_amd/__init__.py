@@ -336,6 +336,7 @@ class Executor:
 def quantize(x, p1, p2, out, quant_scale, mode: str, clip_ratio: float = 1.0,
              dst_type_max: float = 0.0, stream=None, kernel: int = KERNEL_AUTO) -> None:
     """One fused call: plan (single-use executor) and enqueue on `stream`."""
+    _same_gpu(stream, x, p1, None if p2 is None or p2.numel() == 0 else p2, out, quant_scale)
     ex = Executor(x, p1, p2, out, quant_scale, mode, clip_ratio, dst_type_max, kernel=kernel,
                   repeatable=False)
     ex.run(stream)
@@ -346,6 +347,7 @@ def dequantize(codes, quant_scale, mode: str, M: int, N: int, dtype, out=None, s
     (torch.bfloat16 or torch.float16): a [K, M, N] tensor, ``out`` when given."""
     torch = _torch()
     K = codes.shape[0]
+    _same_gpu(stream, codes, quant_scale, out)
     if out is None:
         out = torch.empty((K, M, N), dtype=dtype, device=codes.device)
     dt = {torch.float16: DT_FLOAT16, torch.bfloat16: DT_BFLOAT16}.get(out.dtype, -1)
@@ -365,6 +367,7 @@ def mx_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=None
     for t in (a_codes, a_scale, w_codes, w_scale):
         if not t.is_contiguous():
             raise ValueError("mx_gemm operands must be contiguous")
+    _same_gpu(stream, a_codes, a_scale, w_codes, w_scale, out)
     T, O = a_codes.shape[0], w_codes.shape[0]
     if out is None:
         out = torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
@@ -389,6 +392,7 @@ def int4_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=No
     for t in (a_codes, a_scale, w_codes, w_scale):
         if not t.is_contiguous():
             raise ValueError("int4_gemm operands must be contiguous")
+    _same_gpu(stream, a_codes, a_scale, w_codes, w_scale, out)
     T, O = a_codes.shape[0], w_codes.shape[0]
     if out is None:
         out = torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
@@ -459,6 +463,16 @@ def _same_device(first, *others):
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+
+def _same_gpu(stream, first, *others):
+    """The checks of a launching call: all tensors on one GPU (a host address must not reach a kernel), the
+    caller's stream one of that GPU's."""
+    if first.device.type != "cuda":
+        raise ValueError(f"tensors on {first.device}: this call runs on a GPU")
+    _same_device(first, *others)
+    if stream is not None and stream.device != first.device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
 
 
 def _call(fn, name, device, *args):
@@ -581,7 +595,7 @@ def empty_kv_cache(pages: int, heads: int, page_size: int, head_dim: int, mode: 
 def kv_write(cache: KVCache, k, v, slots, clip_ratio: float = 1.0, dst_type_max: float = 0.0, stream=None) -> None:
     """Quantize rows k, v [T, Hkv, D] (bfloat16 or float16) into the cache at slots [T] (int32:
     page * page_size + offset; negative: not written)."""
-    _same_device(cache.k, k, v, slots)
+    _same_gpu(stream, cache.k, k, v, slots)
     d = _Descs(k, v, slots)
     _call(lib.fq_kv_write, "fq_kv_write", cache.device, *d.ptrs, clip_ratio, dst_type_max, *cache._args(), _stream(stream, cache.device))
 
@@ -600,7 +614,7 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
         _record(stream, k_out, v_out)
     elif k_out.dtype != dtype or v_out.dtype != dtype or k_out.shape[0] != total or v_out.shape[0] != total:
         raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
-    _same_device(cache.k, block_table, cu_seqlens, k_out, v_out)
+    _same_gpu(stream, cache.k, block_table, cu_seqlens, k_out, v_out)
     d = _Descs(block_table, cu_seqlens, k_out, v_out)
     _call(lib.fq_kv_read, "fq_kv_read", cache.device, *cache._args(), *d.ptrs, _stream(stream, cache.device))
     return k_out, v_out
@@ -632,7 +646,7 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _record(stream, out)
-    _same_device(cache.k, q, block_table, lengths, out, lse, workspace)
+    _same_gpu(stream, cache.k, q, block_table, lengths, out, lse, workspace)
     d = _Descs(q, block_table, lengths, out, lse)
     qp, bp, lp, op, sp = d.ptrs
     held = cache._args()
@@ -674,7 +688,7 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
         _record(stream, out)
     if cu_k is None:
         cu_k = cu_q
-    _same_device(q, k, v, cu_q, cu_k, out, lse, workspace)
+    _same_gpu(stream, q, k, v, cu_q, cu_k, out, lse, workspace)
     d = _Descs(q, k, v, cu_q, cu_k, out, lse)
     qp, kp, vp, ap, bp, op, sp = d.ptrs
     causal = 1 if causal else 0

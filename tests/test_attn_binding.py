@@ -47,3 +47,65 @@ def test_memory_that_is_given_up_is_not_used():
     q, table, lens = torch.empty(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     d = fq._Descs(q, table, lens, q)
     assert fq.lib.fq_attn_decode(d.ptrs[0], *cache._args(), d.ptrs[1], d.ptrs[2], 0.0, d.ptrs[3], None, None, size, None) == fq.FQ_ERR_PARAM_NULLPTR
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Names of the launching calls of the library that the binding made; none is made in earnest."""
+    made, real = [], fq.lib
+
+    class Library:
+        def __getattr__(self, name):
+            if name in ("fq_kv_write", "fq_kv_read", "fq_attn_decode", "fq_attn_prefill", "fq_run", "fq_dequant", "fq_int4_gemm", "fq_mx_gemm"):
+                return lambda *a: made.append(name) or fq.FQ_SUCCESS
+            return getattr(real, name)
+
+    monkeypatch.setattr(fq, "lib", Library())
+    return made
+
+
+class _Stream:
+    cuda_stream = 0x1234
+
+    def __init__(self, device="cuda:0"):
+        self.device = torch.device(device)
+
+
+def _calls(stream):
+    """Every launching call of the package on host tensors."""
+    b16, i32, u8, f32 = (lambda *s, t=t: torch.zeros(s, dtype=t) for t in (torch.bfloat16, torch.int32, torch.uint8, torch.float32))
+    cache = fq.empty_kv_cache(4, 2, 16, 64, "int8", "cpu")
+    rows, q, one, table = b16(3, 2, 64), b16(1, 4, 64), i32(1), i32(1, 2)
+    cu = torch.tensor([0, 3], dtype=torch.int32)
+    out, sc = fq.empty_outputs(4, 64, 64, "int4", device="cpu")
+    x, p = b16(4, 64, 64), b16(64, 64)
+    return {
+        "kv_write": lambda: fq.kv_write(cache, rows, rows, i32(3), stream=stream),
+        "kv_read": lambda: fq.kv_read(cache, table, cu, 3, torch.bfloat16, rows, rows.clone(), stream=stream),
+        "attn_decode": lambda: fq.attn_decode(q, cache, table, one, out=q.clone(), stream=stream),
+        "attn_prefill": lambda: fq.attn_prefill(rows, rows, rows, cu, out=rows.clone(), stream=stream),
+        "quantize": lambda: fq.quantize(x, p, p, out, sc, "int4", stream=stream),
+        "dequantize": lambda: fq.dequantize(out, sc, "int4", 64, 64, torch.bfloat16, out=x.clone(), stream=stream),
+        "int4_gemm": lambda: fq.int4_gemm(u8(4, 64), f32(4), u8(8, 64), f32(8), 128, out=b16(4, 8), stream=stream),
+        "mx_gemm": lambda: fq.mx_gemm(u8(4, 64), u8(4, 2, 2), u8(8, 64), u8(8, 2, 2), 128, out=b16(4, 8), stream=stream),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls(None)))
+def test_host_tensors_never_reach_a_launch(launches, name):
+    """Also with a stream in hand, whose presence says nothing about where the tensors are."""
+    with pytest.raises(ValueError, match="GPU"):
+        _calls(_Stream())[name]()
+    assert not launches
+
+
+def test_a_stream_of_another_device_is_refused():
+    class On:  # a tensor of cuda:0, as far as the check looks
+        device = torch.device("cuda:0")
+
+        def get_device(self):
+            return 0
+
+    fq._same_gpu(_Stream("cuda:0"), On(), None, On())
+    with pytest.raises(ValueError, match="stream"):
+        fq._same_gpu(_Stream("cuda:1"), On())
