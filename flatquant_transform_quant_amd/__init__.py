@@ -19,6 +19,10 @@ Output storage in torch:
 
 A paged key-value cache in the same formats is a :class:`KVCache` (``empty_kv_cache`` allocates
 one); ``kv_write``, ``kv_read``, ``attn_decode`` and ``attn_prefill`` are the calls on it.
+
+Streams: a call runs on the current stream, or on ``stream``.  Results and workspaces that a call allocates
+come from that stream's memory; another stream reads a result after waiting for it.  Tensors that the caller
+passes in are the caller's to keep in order (and, if freed early, to ``record_stream``).
 """
 from __future__ import annotations
 
@@ -337,8 +341,8 @@ def quantize(x, p1, p2, out, quant_scale, mode: str, clip_ratio: float = 1.0,
              dst_type_max: float = 0.0, stream=None, kernel: int = KERNEL_AUTO) -> None:
     """One fused call: plan (single-use executor) and enqueue on `stream`."""
     _same_gpu(stream, x, p1, None if p2 is None or p2.numel() == 0 else p2, out, quant_scale)
-    ex = Executor(x, p1, p2, out, quant_scale, mode, clip_ratio, dst_type_max, kernel=kernel,
-                  repeatable=False)
+    ex = _new(stream, lambda: Executor(x, p1, p2, out, quant_scale, mode, clip_ratio, dst_type_max, kernel=kernel,
+                                       repeatable=False), result=False)  # (its workspace)
     ex.run(stream)
 
 
@@ -349,7 +353,7 @@ def dequantize(codes, quant_scale, mode: str, M: int, N: int, dtype, out=None, s
     K = codes.shape[0]
     _same_gpu(stream, codes, quant_scale, out)
     if out is None:
-        out = torch.empty((K, M, N), dtype=dtype, device=codes.device)
+        out = _new(stream, lambda: torch.empty((K, M, N), dtype=dtype, device=codes.device))
     dt = {torch.float16: DT_FLOAT16, torch.bfloat16: DT_BFLOAT16}.get(out.dtype, -1)
     st = fq_dequant(describe_out(codes, mode, K, M, N), describe_scale(quant_scale, mode),
                     make_tensor(out.data_ptr(), dt, out.shape, out.stride()),
@@ -370,7 +374,7 @@ def mx_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=None
     _same_gpu(stream, a_codes, a_scale, w_codes, w_scale, out)
     T, O = a_codes.shape[0], w_codes.shape[0]
     if out is None:
-        out = torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
+        out = _new(stream, lambda: torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device))
     cdt = {torch.bfloat16: DT_BFLOAT16, torch.float32: DT_FLOAT32}.get(out.dtype, -1)
     G = -(-H // 64)
     st = fq_mx_gemm(make_tensor(a_codes.data_ptr(), DT_FLOAT4_E2M1, (T, H)),
@@ -395,7 +399,7 @@ def int4_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=No
     _same_gpu(stream, a_codes, a_scale, w_codes, w_scale, out)
     T, O = a_codes.shape[0], w_codes.shape[0]
     if out is None:
-        out = torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device)
+        out = _new(stream, lambda: torch.empty((T, O), dtype=out_dtype or torch.bfloat16, device=a_codes.device))
     cdt = {torch.bfloat16: DT_BFLOAT16, torch.float32: DT_FLOAT32}.get(out.dtype, -1)
     st = fq_int4_gemm(make_tensor(a_codes.data_ptr(), DT_INT4, (T, H)),
                       make_tensor(a_scale.data_ptr(), DT_FLOAT32, (T,)),
@@ -501,11 +505,22 @@ def _stream(stream, device):
     return _raw_stream[0](device.index) or None
 
 
-def _record(stream, *tensors):
-    """Tensors allocated here on the current stream and used on the caller's `stream`."""
-    for t in tensors:
-        if stream is not None and t is not None and stream != _torch().cuda.current_stream(t.device):
-            t.record_stream(stream)
+def _new(stream, make, result=True):
+    """What ``make()`` allocates, for work on the caller's `stream`: out of that stream's own pool, so that
+    whatever held the memory before is done when the work begins (a block of the current stream's pool may
+    still be in use by kernels that the caller's stream does not wait for).  A result is read on the current
+    stream as a rule, so its memory also waits for that one when it is freed."""
+    torch = _torch()
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if result:
+        t.record_stream(current)
+    return t
 
 
 KV_MODES = ("f16", "bf16", "int8", "e4m3", "int4", "fp4")
@@ -607,16 +622,15 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
     torch = _torch()
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
+    _same_gpu(stream, cache.k, block_table, cu_seqlens, k_out, v_out)
+    held = cache._args()
     if k_out is None:
-        shape = (total, cache.heads, cache.head_dim)
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
-        _record(stream, k_out, v_out)
+        make = lambda: torch.empty((total, cache.heads, cache.head_dim), dtype=dtype, device=cache.device)  # noqa: E731
+        k_out, v_out = _new(stream, make), _new(stream, make)
     elif k_out.dtype != dtype or v_out.dtype != dtype or k_out.shape[0] != total or v_out.shape[0] != total:
         raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
-    _same_gpu(stream, cache.k, block_table, cu_seqlens, k_out, v_out)
     d = _Descs(block_table, cu_seqlens, k_out, v_out)
-    _call(lib.fq_kv_read, "fq_kv_read", cache.device, *cache._args(), *d.ptrs, _stream(stream, cache.device))
+    _call(lib.fq_kv_read, "fq_kv_read", cache.device, *held, *d.ptrs, _stream(stream, cache.device))
     return k_out, v_out
 
 
@@ -631,8 +645,7 @@ def _workspace(fn, name, device, stream, given, *args):
     if size.value == 0:
         return None, None, 0
     torch = _torch()
-    ws = torch.empty((size.value,), dtype=torch.uint8, device=device)
-    _record(stream, ws)
+    ws = _new(stream, lambda: torch.empty((size.value,), dtype=torch.uint8, device=device), result=False)
     return ws, ws.data_ptr(), size.value
 
 
@@ -643,10 +656,9 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
     1/sqrt(D).  ``lse`` (float32 [B, Hq]), when given, receives the log of the softmax's sum.
     ``workspace`` (uint8, at least attn_decode_workspace_size) may be passed to reuse one."""
     torch = _torch()
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _record(stream, out)
     _same_gpu(stream, cache.k, q, block_table, lengths, out, lse, workspace)
+    if out is None:
+        out = _new(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
     d = _Descs(q, block_table, lengths, out, lse)
     qp, bp, lp, op, sp = d.ptrs
     held = cache._args()
@@ -683,12 +695,11 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
     1/sqrt(D).  ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least
     attn_prefill_workspace_size) may be passed to reuse one."""
     torch = _torch()
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _record(stream, out)
     if cu_k is None:
         cu_k = cu_q
     _same_gpu(stream, q, k, v, cu_q, cu_k, out, lse, workspace)
+    if out is None:
+        out = _new(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
     d = _Descs(q, k, v, cu_q, cu_k, out, lse)
     qp, kp, vp, ap, bp, op, sp = d.ptrs
     causal = 1 if causal else 0

@@ -109,3 +109,70 @@ def test_a_stream_of_another_device_is_refused():
     fq._same_gpu(_Stream("cuda:0"), On(), None, On())
     with pytest.raises(ValueError, match="stream"):
         fq._same_gpu(_Stream("cuda:1"), On())
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """A stand-in for torch's streams: two of them, the current one, and which was current at each allocation."""
+    main, side, state = _Stream(), _Stream(), {"made": [], "recorded": []}
+    state.update(main=main, side=side, current=main)
+
+    class Inside:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.s
+
+        def __exit__(self, *_):
+            state["current"] = self.before
+
+    real = torch.empty, torch.empty_like
+
+    def noted(f):
+        def make(*a, **k):
+            state["made"].append(state["current"])
+            return f(*a, **k)
+        return make
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state["current"])
+    monkeypatch.setattr(torch.cuda, "stream", Inside)
+    monkeypatch.setattr(torch, "empty", noted(real[0]))
+    monkeypatch.setattr(torch, "empty_like", noted(real[1]))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: state["recorded"].append((t.data_ptr(), s)))
+    monkeypatch.setattr(fq, "_same_gpu", lambda *a: None)
+    monkeypatch.setattr(fq, "_raw_stream", [lambda index: state["current"].cuda_stream])
+    return state
+
+
+def test_memory_of_a_call_comes_from_the_stream_it_runs_on(streams, launches):
+    """Results and workspaces of a call on the caller's stream: a block of the current stream's pool may still be written by
+    kernels that the caller's stream does not wait for."""
+    main, side = streams["main"], streams["side"]
+    b16, i32 = (lambda *s, t=t: torch.zeros(s, dtype=t) for t in (torch.bfloat16, torch.int32))
+    cache = fq.empty_kv_cache(4, 2, 16, 64, "int8", "cpu")
+    long = i32(1, 64)
+    cq, ck = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([0, 8192], dtype=torch.int32)
+    u8, f32 = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4)
+    e8, made = torch.zeros(4, 2, 2, dtype=torch.uint8), streams["made"]
+
+    def on(stream, count, results, f):
+        made.clear()
+        streams["recorded"].clear()
+        f()
+        assert made == [stream] * count and streams["current"] is main
+        # (a result's memory waits for the current stream too when it is freed; a workspace's needs not)
+        if results is not None:
+            assert [s for _, s in streams["recorded"]] == ([main] * results if stream is side else [])
+
+    for s, at in ((side, side), (None, main), (main, main)):
+        on(at, 2, 2, lambda: fq.kv_read(cache, i32(1, 2), cq, 3, torch.bfloat16, stream=s))
+        on(at, 2, 1, lambda: fq.attn_decode(b16(1, 4, 64), cache, long, i32(1), stream=s))
+        on(at, 2, 1, lambda: fq.attn_prefill(b16(3, 4, 64), b16(8192, 2, 64), b16(8192, 2, 64), cq, ck, stream=s))
+        on(at, 1, 1, lambda: fq.dequantize(torch.zeros(4, 64, 32, dtype=torch.uint8), f32, "int4", 64, 64, torch.bfloat16, stream=s))
+        on(at, 1, 1, lambda: fq.int4_gemm(u8, f32, u8, f32, 128, stream=s))
+        on(at, 1, 1, lambda: fq.mx_gemm(u8, e8, u8, e8, 128, stream=s))
+        x, p = b16(4, 256, 256), b16(256, 256)
+        out, sc = fq.empty_outputs(4, 256, 256, "int4", device="cpu")
+        on(at, 1, None, lambda: fq.quantize(x, p, p, out, sc, "int4", 0.95, stream=s))
+    assert launches.count("fq_attn_decode") == 3
