@@ -36,6 +36,17 @@ bool rows_ok(const fq_tensor& t, int64_t n, int64_t heads, int64_t D, int32_t dt
          t.strides[0] < lim && t.strides[1] < lim && aligned(t.data, 16);
 }
 
+// The same of rows that are written: no two elements at one place, so that nothing depends on the order of the writes.
+bool out_rows_ok(const fq_tensor& t, int64_t n, int64_t heads, int64_t D, int32_t dtype, Rows16* r) {
+  if (!rows_ok(t, n, heads, D, dtype, r)) return false;
+  if (empty(t) || (n == 1 && heads == 1)) return true;
+  if (n == 1) return r->head >= D;
+  if (heads == 1) return r->row >= D;
+  // (below 2^57: strides below 2^40, at most 2^17 heads; for the rows compare by division)
+  return r->row >= r->head ? r->head >= D && r->row >= (heads - 1) * r->head + D
+                           : r->row >= D && (r->head - D) / r->row >= n - 1;
+}
+
 bool i32_vec(const fq_tensor& t, int64_t n) {
   return strides_ok(t) && t.dtype == FQ_DT_INT32 && shape_is(t, 1, n) && is_contiguous(t) && aligned(t.data, 4);
 }
@@ -183,8 +194,8 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
   Rows16 kr, vr;
   BlockTable bt;
   if (B < 0 || B > 65536 || T < 0 || T >= (int64_t(1) << 31) - 65536 || row_dtype(k_out->dtype) == 0 ||
-      !table_ok(*block_table, B, &bt) || !i32_vec(*cu, B + 1) || !rows_ok(*k_out, T, c.Hkv, c.D, k_out->dtype, &kr) ||
-      !rows_ok(*v_out, T, c.Hkv, c.D, k_out->dtype, &vr))
+      !table_ok(*block_table, B, &bt) || !i32_vec(*cu, B + 1) || !out_rows_ok(*k_out, T, c.Hkv, c.D, k_out->dtype, &kr) ||
+      !out_rows_ok(*v_out, T, c.Hkv, c.D, k_out->dtype, &vr))
     return FQ_ERR_PARAM_INVALID;
   if (c.mode == kKv16 && c.dtype != row_dtype(k_out->dtype)) return FQ_ERR_PARAM_INVALID;
   c.dtype = row_dtype(k_out->dtype);
@@ -238,7 +249,7 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
     return FQ_ERR_PARAM_INVALID;
   const int64_t B = q->shape[0], Hq = q->shape[1], D = q->shape[2];
   if (!table_ok(*block_table, B, &a.bt) || !i32_vec(*lengths, B) || !rows_ok(*q, B, Hq, D, q->dtype, &a.q) ||
-      !rows_ok(*out, B, Hq, D, q->dtype, &a.out) || !lse_ok(lse, B, Hq))
+      !out_rows_ok(*out, B, Hq, D, q->dtype, &a.out) || !lse_ok(lse, B, Hq))
     return FQ_ERR_PARAM_INVALID;
   if (a.c.mode == kKv16 && a.c.dtype != row_dtype(q->dtype)) return FQ_ERR_PARAM_INVALID;
   a.c.dtype = row_dtype(q->dtype);
@@ -288,7 +299,7 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
   const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
   const int64_t B = cu_q->shape[0] - 1;
   PrefillArgs a;
-  if (!rows_ok(*q, Tq, Hq, D, q->dtype, &a.q) || !rows_ok(*out, Tq, Hq, D, q->dtype, &a.out) ||
+  if (!rows_ok(*q, Tq, Hq, D, q->dtype, &a.q) || !out_rows_ok(*out, Tq, Hq, D, q->dtype, &a.out) ||
       !rows_ok(*k, Tk, Hkv, D, q->dtype, &a.k) || !rows_ok(*v, Tk, Hkv, D, q->dtype, &a.v) || !i32_vec(*cu_q, B + 1) ||
       !i32_vec(*cu_k, B + 1) || !lse_ok(lse, Tq, Hq))
     return FQ_ERR_PARAM_INVALID;

@@ -261,8 +261,10 @@ fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tens
  * lengths on the device, where every index is checked: one outside the cache is never followed.
  *
  * 16-bit row tensors (k, v, q, outputs) are FLOAT16 | BFLOAT16 [rows, heads, D] with innermost
- * stride 1, the other strides multiples of 8 elements and data 16-byte aligned; an empty one
- * (a dimension of 0) may have NULL data, and a call with no rows does nothing.
+ * stride 1, the other strides multiples of 8 elements (below 2^40) and data 16-byte aligned; an
+ * empty one (a dimension of 0) may have NULL data, and a call with no rows does nothing.  Strides
+ * of inputs may be 0; the elements of an output lie apart from each other (its smaller outer stride
+ * at least D, the larger one at least what the smaller one spans).
  * Errors of all these calls: a required tensor or data pointer NULL -> FQ_ERR_PARAM_NULLPTR;
  * any dtype, shape, stride, alignment or scalar outside the above -> FQ_ERR_PARAM_INVALID (no
  * HIP call is made before these checks); not a gfx950 device, or a launch failure ->
