@@ -131,6 +131,14 @@ fq_status cache_of(const fq_tensor* k, const fq_tensor* ks, const fq_tensor* v, 
   return st != FQ_SUCCESS ? st : side_of(v, vs, false, c, &c->v);
 }
 
+// Workgroups of a launch: all kernels here have 256 threads, and a grid has fewer than 2^32 of them in x.
+constexpr int64_t kWorkgroups = (int64_t(1) << 24) - 1;
+
+// T tokens as the cache kernels deal them out: D / 8 lanes, rounded up to 8, 16 or 32, a token
+bool tokens_ok(int64_t T, int64_t D) {
+  return T >= 0 && T <= kWorkgroups * (D <= 64 ? 32 : D <= 128 ? 16 : 8);
+}
+
 int32_t row_dtype(int32_t t) { return t == FQ_DT_FLOAT16 ? kF16 : t == FQ_DT_BFLOAT16 ? kBF16 : 0; }
 
 bool table_ok(const fq_tensor& t, int64_t B, BlockTable* bt) {
@@ -166,7 +174,7 @@ fq_status fq_kv_write(const fq_tensor* k, const fq_tensor* v, const fq_tensor* s
   if (k->ndim != 3) return FQ_ERR_PARAM_INVALID;
   const int64_t T = k->shape[0];
   Rows16 kr, vr;
-  if (row_dtype(k->dtype) == 0 || T < 0 || T >= (int64_t(1) << 31) - 65536 ||
+  if (row_dtype(k->dtype) == 0 || !tokens_ok(T, c.D) ||
       !rows_ok(*k, T, c.Hkv, c.D, k->dtype, &kr) || !rows_ok(*v, T, c.Hkv, c.D, k->dtype, &vr) || !i32_vec(*slots, T))
     return FQ_ERR_PARAM_INVALID;
   if (c.mode == kKv16 && c.dtype != row_dtype(k->dtype)) return FQ_ERR_PARAM_INVALID;
@@ -193,7 +201,7 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
   const int64_t B = block_table->shape[0], T = k_out->shape[0];
   Rows16 kr, vr;
   BlockTable bt;
-  if (B < 0 || B > 65536 || T < 0 || T >= (int64_t(1) << 31) - 65536 || row_dtype(k_out->dtype) == 0 ||
+  if (B < 0 || B > 65536 || !tokens_ok(T, c.D) || row_dtype(k_out->dtype) == 0 ||
       !table_ok(*block_table, B, &bt) || !i32_vec(*cu, B + 1) || !out_rows_ok(*k_out, T, c.Hkv, c.D, k_out->dtype, &kr) ||
       !out_rows_ok(*v_out, T, c.Hkv, c.D, k_out->dtype, &vr))
     return FQ_ERR_PARAM_INVALID;
@@ -215,9 +223,10 @@ static bool decode_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_
     return false;
   *reach = block_table->shape[1] * P;
   if (*reach >= (int64_t(1) << 31) - 65536) return false;  // (a step past the last token stays within 31 bits)
-  // units of work (128 tokens of a sequence, cache head and 16 query heads, and up to 3 a sequence
-  // more for its start) counted in 31 bits
-  return B * Hkv * ceil_div(Hq / Hkv, 16) * (ceil_div(*reach, 128) + 3) < (int64_t(1) << 31);
+  // segments (a sequence, cache head and 16 query heads: a workgroup each of the join, or of calls without
+  // one), and units of work (128 tokens of a segment, and up to 3 more for its start) counted in 31 bits
+  const int64_t segments = B * Hkv * ceil_div(Hq / Hkv, 16);
+  return segments <= kWorkgroups && segments * (ceil_div(*reach, 128) + 3) < (int64_t(1) << 31);
 }
 
 fq_status fq_attn_decode_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table,
@@ -275,7 +284,7 @@ static bool prefill_sizes(const fq_tensor* q, const fq_tensor* k, const fq_tenso
   const int64_t B = cu_q->shape[0] - 1, lim = (int64_t(1) << 31) - 65536;
   return B >= 1 && B <= 65536 && Tq >= 0 && Tk >= 0 && Tq < lim && Tk < lim && Hq >= 1 && Hq <= 65536 && Hkv >= 1 &&
          Hkv <= 1024 && Hq % Hkv == 0 && D >= 8 && D <= 256 && D % 8 == 0 &&
-         (Tq / 128 + B) * Hq < (int64_t(1) << 28);  // workgroups (a row tile and head each), cut into up to 8 parts
+         (Tq / 128 + B) * Hq <= kWorkgroups;  // (a row tile and head each; only few are cut into parts)
 }
 
 fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t /*causal*/,

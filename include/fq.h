@@ -270,6 +270,8 @@ fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tens
  * HIP call is made before these checks); not a gfx950 device, or a launch failure ->
  * FQ_ERR_RUNTIME.
  *
+ * A call writes or reads at most (2^24 - 1) * 32 tokens with D up to 64, * 16 up to 128, * 8 up to 256.
+ *
  * fq_kv_write: rows k[i], v[i] ([T, Hkv, D]) go to slot slots[i] = page * P + offset (INT32
  * [T]).  A negative slot, or one beyond the cache, writes nothing (padding).  No slot may occur
  * twice in a call.  clipRatio in (0, 1] acts on the per-token formats, dstTypeMax (0, or 6 to
@@ -293,8 +295,8 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
  * with g = Hq / Hkv (a whole number) query heads sharing a cache head.  q, out FLOAT16 |
  * BFLOAT16 [B, Hq, D] of one dtype (a 16-bit cache must have it too), lengths INT32 [B] (the
  * newest token included; capped at the table's reach), block_table as above, 1 <= Hq <= 65536;
- * reach = the table's width * P < 2^31 - 65536 and B * Hkv * ceilDiv(g, 16) * (ceilDiv(reach, 128)
- * + 3) < 2^31.
+ * reach = the table's width * P < 2^31 - 65536, B * Hkv * ceilDiv(g, 16) < 2^24 and that times
+ * (ceilDiv(reach, 128) + 3) < 2^31.
  * `lse`, when not NULL, is FLOAT32 [B, Hq] (contiguous) and receives log sum_t exp(scale *
  * <q, k[t]>).  A length of 0 (an idle place of a fixed batch) gives zeros and lse = -infinity.
  * A token whose table entry is outside the cache is left out of the sum; cache contents past a
@@ -321,8 +323,8 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
  * With causal == 0 it sees all Lk.  A row that sees no key gives zeros and lse = -infinity.
  * Infinities and NaN in keys and values reach only the rows that see them.  The row strides of
  * k and v are at most 2^23 elements.
- * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536.  Rows of
- * out past cu_q[B] are not written.  A call with few rows over many keys splits the keys and joins
+ * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536 and
+ * (floor(Tq / 128) + B) * Hq < 2^24.  Rows of out past cu_q[B] are not written.  A call with few rows over many keys splits the keys and joins
  * the parts in `workspace` (as for fq_attn_decode, of the size that
  * fq_attn_prefill_get_workspace_size gives for the same tensors; 0 for most calls). */
 fq_status fq_attn_prefill_get_workspace_size(const fq_tensor* q, const fq_tensor* k, const fq_tensor* cu_q, int32_t causal,

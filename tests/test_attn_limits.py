@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import flatquant_transform_quant_amd as fq
-from test_attn_api import B, D, H, HQ, INVAL, OK, RUNTIME, T, decode, decode_args, no_gpu, prefill, prefill_args, read, read_args, ref, tens, with_, write, write_args
+from test_attn_api import B, D, DUMMY, H, HQ, INVAL, OK, RUNTIME, T, decode, decode_args, no_gpu, prefill, prefill_args, read, read_args, ref, tens, with_, write, write_args
 
 BF16 = fq.DT_BFLOAT16
 # name, key, rows, heads, call
@@ -41,3 +41,38 @@ def test_the_stride_of_a_single_row_or_head_does_not_count():
         a = prefill_args(hq=1, h=1)
         assert prefill(with_(a, out=tens(BF16, (T, 1, D), (D, 0, 1)))) == RUNTIME
         assert prefill(with_(a, out=tens(BF16, (T, 1, D), (D - 8, 0, 1)))) == INVAL
+
+
+@no_gpu
+@pytest.mark.parametrize("d,most", [(64, 32 * (2 ** 24 - 1)), (72, 16 * (2 ** 24 - 1)), (128, 16 * (2 ** 24 - 1)), (256, 8 * (2 ** 24 - 1))])
+def test_rows_that_a_cache_launch_can_hold(d, most):
+    """A launch has fewer than 2^32 threads: 2^24 - 1 workgroups, of 32, 16 or 8 tokens each."""
+    for n, want in ((most, RUNTIME), (most + 1, INVAL)):
+        rows = tens(BF16, (n, 1, d))
+        assert write(with_(write_args(h=1, d=d), k=rows, v=rows, slots=tens(fq.DT_INT32, (n,)))) == want
+        assert read(with_(read_args(h=1, d=d), k=rows, v=rows)) == want
+
+
+@no_gpu
+@pytest.mark.parametrize("width", [2, 40])  # a workgroup a segment; a workgroup of the join a segment
+def test_segments_that_a_decode_launch_can_hold(width):
+    size = ctypes.c_uint64()
+    for b, hq, h, want in ((65536, 255, 255, True), (65536, 256, 256, False), (16383, 1024, 1024, True), (16384, 1024, 1024, False),
+                           (8191, 32768, 1024, True), (8192, 32768, 1024, False), (65536, 2000, 2, True)):
+        rows = tens(BF16, (b, hq, 8))
+        a = with_(decode_args(width=width, h=h, d=8), q=rows, out=rows, bt=tens(fq.DT_INT32, (b, width)), lens=tens(fq.DT_INT32, (b,)), ws=DUMMY,
+                  size=2 ** 40)
+        query = fq.lib.fq_attn_decode_get_workspace_size(ref(a["q"]), ref(a["kc"]), ref(a["bt"]), ctypes.byref(size))
+        assert query == (OK if want else INVAL), (b, hq, h)
+        assert decode(a) == (RUNTIME if want else INVAL), (b, hq, h)
+
+
+@no_gpu
+def test_workgroups_that_a_prompt_launch_can_hold():
+    size = ctypes.c_uint64()
+    for tq, b, hq, want in ((100, 65536, 255, True), (100, 65536, 256, False), (128 * 16383 - 129, 1, 1024, True), (128 * 16383, 1, 1024, False),
+                            (127, 2 ** 14 - 1, 1024, True), (128, 2 ** 14 - 1, 1024, False)):
+        a = prefill_args(tq=tq, tk=100, hq=hq, h=1, d=8, b=b)
+        query = fq.lib.fq_attn_prefill_get_workspace_size(ref(a["q"]), ref(a["k"]), ref(a["cq"]), 1, ctypes.byref(size))
+        assert query == (OK if want else INVAL), (tq, b, hq)
+        assert prefill(a) == (RUNTIME if want else INVAL), (tq, b, hq)
