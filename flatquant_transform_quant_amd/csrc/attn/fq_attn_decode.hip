@@ -447,7 +447,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 
     // ---- q as the B operand, and the column's constants
     u32x4_t qf[S::KS];
-    float cq = a.scale * 1.44269504f * kCode;
+    float cq = a.scale * 1.44269504f;  // (times kCode with q's exponent below: that product alone could overflow)
     {
       const uint16_t* qp = a.q.p + b0 * a.q.row + static_cast<int64_t>(hk * a.g + (my_head ? head : 0)) * a.q.head;
       u32x4_t raw[S::KS];
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 #pragma unroll
           for (int i = 0; i < 4; ++i) qf[ks][i] = h2<kF16>(y[2 * i], y[2 * i + 1]);
         }
-        cq = __builtin_amdgcn_ldexpf(cq, e - 13);
+        cq = __builtin_amdgcn_ldexpf(cq, e - 13 + (kCode == 512.0f ? 9 : 0));
       }
     }
 

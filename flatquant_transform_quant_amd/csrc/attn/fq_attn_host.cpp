@@ -151,6 +151,16 @@ bool table_ok(const fq_tensor& t, int64_t B, BlockTable* bt) {
   return empty(t) || ((t.shape[1] == 1 || t.strides[1] == 1) && aligned(t.data, 4));
 }
 
+// The scale of the scores in fp32.  The kernels multiply by scale * log2(e), which has to stay finite, and a
+// scale too small for fp32 is its smallest number, not 0: a masked score is -infinity times it, and the
+// weights come out as 1 either way.
+bool scale_ok(double scale, int64_t D, float* out) {
+  if (!(std::fabs(scale) <= 0x1p127)) return false;
+  const float f = scale == 0.0 ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(scale);
+  *out = std::fabs(f) > 0.0f ? f : std::copysign(0x1p-149f, static_cast<float>(scale));
+  return true;
+}
+
 bool lse_ok(const fq_tensor* t, int64_t n, int64_t heads) {
   return !t || (strides_ok(*t) && t->dtype == FQ_DT_FLOAT32 && shape_is(*t, 2, n, heads) && is_contiguous(*t) && aligned(t->data, 4));
 }
@@ -253,8 +263,8 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
   st = cache_of(k_cache, k_scale, v_cache, v_scale, &a.c);
   if (st != FQ_SUCCESS) return st;
   int64_t reach;
-  if (!decode_sizes(q, k_cache, block_table, &reach) || row_dtype(q->dtype) == 0 || !std::isfinite(scale) ||
-      !std::isfinite(static_cast<float>(scale)))
+  if (!decode_sizes(q, k_cache, block_table, &reach) || row_dtype(q->dtype) == 0 ||
+      !scale_ok(scale, q->shape[2], &a.scale))
     return FQ_ERR_PARAM_INVALID;
   const int64_t B = q->shape[0], Hq = q->shape[1], D = q->shape[2];
   if (!table_ok(*block_table, B, &a.bt) || !i32_vec(*lengths, B) || !rows_ok(*q, B, Hq, D, q->dtype, &a.q) ||
@@ -267,7 +277,6 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
   a.B = static_cast<int32_t>(B);
   a.Hq = static_cast<int32_t>(Hq);
   a.g = static_cast<int32_t>(Hq / a.c.Hkv);
-  a.scale = scale == 0.0 ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(scale);
   const uint64_t need = attn_decode_workspace(a.B, a.Hq, a.c.Hkv, a.c.D, reach);
   if (need > 0 && !workspace) return FQ_ERR_PARAM_NULLPTR;
   if (workspaceSize < need || (need > 0 && !aligned(workspace, 16))) return FQ_ERR_PARAM_INVALID;
@@ -303,11 +312,10 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
   for (const fq_tensor* t : {q, k, v, cu_q, cu_k, out})
     if (missing(t)) return FQ_ERR_PARAM_NULLPTR;
   if (lse && missing(lse)) return FQ_ERR_PARAM_NULLPTR;
-  if (!prefill_sizes(q, k, cu_q) || row_dtype(q->dtype) == 0 || !std::isfinite(scale) || !std::isfinite(static_cast<float>(scale)))
-    return FQ_ERR_PARAM_INVALID;
+  PrefillArgs a;
+  if (!prefill_sizes(q, k, cu_q) || row_dtype(q->dtype) == 0 || !scale_ok(scale, q->shape[2], &a.scale)) return FQ_ERR_PARAM_INVALID;
   const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
   const int64_t B = cu_q->shape[0] - 1;
-  PrefillArgs a;
   if (!rows_ok(*q, Tq, Hq, D, q->dtype, &a.q) || !out_rows_ok(*out, Tq, Hq, D, q->dtype, &a.out) ||
       !rows_ok(*k, Tk, Hkv, D, q->dtype, &a.k) || !rows_ok(*v, Tk, Hkv, D, q->dtype, &a.v) || !i32_vec(*cu_q, B + 1) ||
       !i32_vec(*cu_k, B + 1) || !lse_ok(lse, Tq, Hq))
@@ -330,7 +338,6 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
   a.D = static_cast<int32_t>(D);
   a.dtype = row_dtype(q->dtype);
   a.causal = causal ? 1 : 0;
-  a.scale = scale == 0.0 ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(scale);
   const hipError_t err = launch_attn_prefill(a, workspace, stream);
   return err == hipSuccess ? FQ_SUCCESS : fail_runtime("prompt attention kernel launch", err);
 }

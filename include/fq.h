@@ -300,7 +300,7 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
  * `lse`, when not NULL, is FLOAT32 [B, Hq] (contiguous) and receives log sum_t exp(scale *
  * <q, k[t]>).  A length of 0 (an idle place of a fixed batch) gives zeros and lse = -infinity.
  * A token whose table entry is outside the cache is left out of the sum; cache contents past a
- * sequence's length are never used, whatever they hold.  scale is finite; 0 means 1/sqrt(D).
+ * sequence's length are never used, whatever they hold.  |scale| <= 2^127; 0 means 1/sqrt(D).
  * Codes enter the products exactly; scores, softmax statistics and sums are fp32.  Results do
  * not depend on the run: the same inputs give the same bits.
  * The cache is read once, split over its length across the device and joined; the partial sums

@@ -76,3 +76,11 @@ def test_workgroups_that_a_prompt_launch_can_hold():
         query = fq.lib.fq_attn_prefill_get_workspace_size(ref(a["q"]), ref(a["k"]), ref(a["cq"]), 1, ctypes.byref(size))
         assert query == (OK if want else INVAL), (tq, b, hq)
         assert prefill(a) == (RUNTIME if want else INVAL), (tq, b, hq)
+
+
+@no_gpu
+def test_scales_at_the_ends_of_the_range():
+    for scale, want in ((2.0 ** 127, RUNTIME), (-2.0 ** 127, RUNTIME), (1e-300, RUNTIME), (-5e-324, RUNTIME), (1.001 * 2.0 ** 127, INVAL),
+                        (-3e38, INVAL)):
+        assert decode(with_(decode_args(), scale=scale)) == want
+        assert prefill(with_(prefill_args(), scale=scale)) == want
