@@ -521,6 +521,41 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       }
     };
 
+    // 16-bit values that are infinite or NaN.  Their products are formed apart, with weights of 1 (0 for a score
+    // of -infinity), and they are left out of the weighted ones: a weight that rounds to 0 would make a NaN of
+    // an infinity that every weight above 0 keeps.
+    auto take_odd = [&](Values<MODE, DP, PAD>& x, const float (&s)[8]) __attribute__((always_inline)) {
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+          for (int w = 0; w < S::VW; ++w) odd |= not_finite16<DT>(x.w[i][h][w]);
+      if (!__any(odd != 0)) return;
+      u32x4_t one;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) one[i] = h2<DT>(s[2 * i] > -kInf ? 1.0f : 0.0f, s[2 * i + 1] > -kInf ? 1.0f : 0.0f);
+#pragma unroll
+      for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+        for (int w = 0; w < S::VW; ++w) {  // elements 2 w, 2 w + 1
+          uint32_t a[4], b[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint32_t& y0 = x.w[2 * p][h][w];
+            uint32_t& y1 = x.w[2 * p + 1][h][w];
+            const uint32_t m0 = not_finite16_mask<DT>(y0), m1 = not_finite16_mask<DT>(y1);
+            a[p] = __builtin_amdgcn_perm(y1 & m1, y0 & m0, 0x05040100u);
+            b[p] = __builtin_amdgcn_perm(y1 & m1, y0 & m0, 0x07060302u);
+            y0 &= ~m0;
+            y1 &= ~m1;
+          }
+          acc[h][2 * w] = mfma16x16x32<DT>(u32x4_t{a[0], a[1], a[2], a[3]}, one, acc[h][2 * w]);
+          acc[h][2 * w + 1] = mfma16x16x32<DT>(u32x4_t{b[0], b[1], b[2], b[3]}, one, acc[h][2 * w + 1]);
+        }
+    };
+
     // their weights p = exp2(s - m), the running maximum and sum moved along
     auto weigh = [&](float (&s)[8]) __attribute__((always_inline)) {
       float top = s[0];
@@ -528,7 +563,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
       if (__any(top > m + kLazy)) {
         const float mn = fmaxf(m, column_max(top));
-        const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        const float f = mn == -kInf ? 1.0f : rescale(m, mn);
         m = mn;
         l *= f;
 #pragma unroll
@@ -664,6 +699,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
                            __builtin_amdgcn_readlane(pages, 2 * idx + 1) >= 0;
         score(kx, i, idx, whole, s);
         if (i + 1 < steps) load_keys(kx, i + 1, idx + 1);
+        if constexpr (MODE == kKv16) take_odd(vx, s);
         weigh(s);
         add(vx, i, idx, whole, s);
         if (i + 1 < steps) load_values(vx, i + 1, idx + 1);
@@ -691,7 +727,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       float mx = -kInf;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][er]);
-      float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mx);
+      float f = m == -kInf ? 0.0f : rescale(m, mx);
       if (m != m || mx == kInf) f = __builtin_nanf("");
       if (MODE != kKv16) f *= kCode;
       const int e = kScaled ? (ref < -1000 ? 0 : ref) : MODE == kKvFp4 ? (ref < -1000 ? 0 : ref - 127) : 0;
@@ -719,7 +755,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
         ls += s_l[w][hd] == 0.0f ? 0.0f : s_l[w][hd] * __builtin_amdgcn_exp2f(mw - mx);  // (nothing seen, or NaN)
         const float x = s_o[w][d * LDH + hd];
         o += x;
-        // (a seen infinity: its weight's remainder may be 0 or of the other sign, the sum is that of x)
+        // (a seen infinity stands in both columns, the sum is that of x)
         if (two && __builtin_fabsf(x) < kInf) o += s_o[w][d * LDH + hd + 8] * (1.0f / kUp);
       }
       const int hq = hk * a.g + ht * 16 + hd;
@@ -819,7 +855,7 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
         for (int i = 0; i < kFew; ++i) m = fmaxf(m, pm[x][i]);
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
-          const float w = pm[x][i] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(pm[x][i] - m);
+          const float w = pm[x][i] == -kInf ? 0.0f : rescale(pm[x][i], m);
           l += pl[x][i] * w;
           o += po[x][i] * w;
         }
@@ -845,12 +881,12 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
       float mn = m;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, pm[j]);
-      const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+      const float f = m == -kInf ? 0.0f : rescale(m, mn);
       l *= f;
       o *= f;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const float w = pm[j] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(pm[j] - mn);
+        const float w = pm[j] == -kInf ? 0.0f : rescale(pm[j], mn);
         l += pl[j] * w;
         o += po[j] * w;
       }
@@ -865,7 +901,7 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
       for (int g = 0; g < G; ++g) mn = fmaxf(mn, s_m[g * E + at]);
       l = o = 0.0f;
       for (int g = 0; g < G; ++g) {
-        const float mg = s_m[g * E + at], w = mg == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mg - mn);
+        const float mg = s_m[g * E + at], w = mg == -kInf ? 0.0f : rescale(mg, mn);
         l += s_l[g * E + at] * w;
         o += s_o[g * E + at] * w;
       }

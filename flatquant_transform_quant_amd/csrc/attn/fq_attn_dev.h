@@ -59,6 +59,21 @@ __device__ __forceinline__ void kv_decode8(const u32x4_t w, float scale, uint32_
   }
 }
 
+// Bit 15 of each half that is infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite16(uint32_t x) {
+  constexpr uint32_t e = DT == kBF16 ? 0x7F807F80u : 0x7C007C00u, one = DT == kBF16 ? 0x00800080u : 0x04000400u;
+  return ((x & e) + one) & 0x80008000u;
+}
+// All bits of each half that is infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite16_mask(uint32_t x) { return (not_finite16<DT>(x) >> 15) * 0xFFFFu; }
+
+// Factor of sums when the softmax's maximum moves up from `m` to `to`.  A sum may hold the infinity of an element that
+// was seen, which has to stay one however far the maximum moves: never 0 (what 2^-126 leaves of a finite sum is far
+// below one rounding of any weight near the maximum).
+__device__ __forceinline__ float rescale(float m, float to) { return fmaxf(__builtin_amdgcn_exp2f(m - to), 0x1p-126f); }
+
 // The codes of elements 8c .. 8c+7 of a row.
 template <int MODE>
 __device__ __forceinline__ u32x4_t kv_load8(const uint8_t* row, int c) {

@@ -21,9 +21,10 @@
 // the accumulators are rescaled a few times a walk instead of every tile.
 // Tiles of all sequences are handed out longest walk first; where they do not fill the device, the
 // long walks are cut into parts whose sums a second launch joins.
-// A weight of 0 times an infinite or NaN value of a hidden key in a partly masked tile is NaN.
-// The walk ignores that; if a result is not finite, the workgroup walks again, this time taking
-// such values out of the masked tiles' products and adding them to the rows that do see them.
+// A weight of 0 times an infinite or NaN value is NaN: for a key that is hidden, in a partly masked tile, and for
+// one whose weight rounds to 0, where the infinity should stay.  The walk ignores that; if a result is not
+// finite, the workgroup walks again, this time taking such values out of the products and adding them to the
+// rows that do see them.
 //
 // What bounds it: one 32768-row prompt, 8 heads on one cache head of 128, takes 1.93 to 2.03 ms (1.08 to
 // 1.14 PFLOP/s; a large library product reaches 1.25 to 1.39 here) with the matrix cores busy 61% of the
@@ -99,13 +100,6 @@ __device__ __forceinline__ float half_max(float v) {  // with lane ^ 32
 __device__ __forceinline__ float half_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-// Bit 15 of each half that is infinite or NaN.
-template <int DT>
-__device__ __forceinline__ uint32_t not_finite16(uint32_t x) {
-  constexpr uint32_t e = DT == kBF16 ? 0x7F807F80u : 0x7C007C00u, one = DT == kBF16 ? 0x00800080u : 0x04000400u;
-  return ((x & e) + one) & 0x80008000u;
 }
 
 // Inclusive sum over the lanes before and at each lane (DPP row shifts, then the rows' last lanes).
@@ -208,8 +202,9 @@ __device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int part
   return p;
 }
 
+// (heads of 64: registers for three workgroups a CU, which the plain walk alone would leave, and the careful one not)
 template <int DT, int DP, bool PAD>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(PrefillArgs a, int parts, float* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void prefill_kernel(PrefillArgs a, int parts, float* __restrict__ ws) {
   constexpr int KS = DP / 16;            // products of a score block
   constexpr int DB = DP / 32;            // 32-row blocks of O^T
   constexpr int kRowB = DP * 2;          // bytes of a tile row
@@ -344,12 +339,24 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
           for (int i = 0; i < 16; ++i)
             if (32 * b + 8 * (i / 4) + i % 4 > left) s[b][i] = -kInf;
       }
+      uint64_t seen = 0;  // CAREFUL: keys of the tile with a score above -infinity for this lane's row
+      if constexpr (CAREFUL) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t w = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w |= (s[b][i] > -kInf ? 1u : 0u) << (8 * (i / 4) + i % 4);
+          w <<= 4 * hf;
+          w |= __shfl_xor(w, 32);
+          seen |= static_cast<uint64_t>(w) << (32 * b);
+        }
+      }
       float top = s[0][0];
 #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
       if (__any(top * c > m + kLazy)) {
         const float mn = fmaxf(m, half_max(top) * c);
-        const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        const float f = mn == -kInf ? 1.0f : CAREFUL ? rescale(m, mn) : __builtin_amdgcn_exp2f(m - mn);
         m = mn;
         l *= f;
 #pragma unroll
@@ -369,21 +376,26 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
           l += x + y;
         }
       __builtin_amdgcn_sched_barrier(0);
+      uint32_t odd = 0;
       static_for<0, 4 * DB>([&](auto ic) __attribute__((always_inline)) {
         constexpr int i = decltype(ic)::value;
         if constexpr (i + kAhead < 4 * DB) vf[i + kAhead] = value((i + kAhead) % DB, (i + kAhead) / DB);
         if constexpr (CAREFUL) {
-          if (masked)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) vf[i][j] &= ~((not_finite16<DT>(vf[i][j]) >> 15) * 0xFFFFu);
+          for (int j = 0; j < 4; ++j) {
+            odd |= not_finite16<DT>(vf[i][j]);
+            vf[i][j] &= ~not_finite16_mask<DT>(vf[i][j]);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
         acc[i % DB] = mfma32x32x16<DT>(vf[i], pf[i / DB], acc[i % DB]);
         __builtin_amdgcn_sched_barrier(0);
       });
       if constexpr (CAREFUL) {
-        for (int j = 0; masked && j < kKeys; ++j) {
+        const bool any = __any(odd != 0);
+        for (int j = 0; any && j < kKeys; ++j) {
           if (t * kKeys + j > lim) break;
+          const float w = (seen >> j) & 1 ? 1.0f : 0.0f;
 #pragma unroll
           for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -391,7 +403,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void prefill_kernel(Pr
               const int e = 32 * d + 8 * (i / 4) + 4 * hf + i % 4;
               const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(
                   vt + j * kRowB + 16 * ((e / 8) ^ (4 * (DP == 64 ? (j >> 1) & 1 : j & 3))) + 2 * (e % 8));
-              if (not_finite16<DT>(v)) acc[d][i] += load16<DT>(v);
+              if (not_finite16<DT>(v)) acc[d][i] += w * load16<DT>(v);
             }
         }
       }
@@ -471,7 +483,7 @@ __global__ __launch_bounds__(kThreads) void prefill_join_kernel(PrefillArgs a, i
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] = p[(e + j) * kRows];
     const float mn = fmaxf(m, mi);
-    const float f0 = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - mn), f1 = mi == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mi - mn);
+    const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mi == -kInf ? 0.0f : rescale(mi, mn);
     m = mn;
     l = li == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li * f1);  // (nothing seen, or NaN)
 #pragma unroll

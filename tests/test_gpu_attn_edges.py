@@ -66,3 +66,76 @@ def test_the_largest_scales(mode):
                 got.append(fq.attn_prefill(qd, kd, vd, _i32(0, 1), _i32(0, n), scale=scale))
             for o in got:  # (the output's rounding to bf16, and 40 terms' in fp32)
                 assert ((o[0, 0].cpu().double() - seen).abs() <= seen.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+
+
+def _one_low_key(n, H, Hq, D, dt, at, nats, sign, seed):
+    """Keys whose scores are 0 but that of token `at`, `nats` below; its value's element 3 of head 0 is infinite."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = torch.ones(1, Hq, D), torch.zeros(n, H, D)
+    k[at] = -nats / math.sqrt(D)
+    v = torch.randn(n, H, D, generator=g)
+    v[at, 0, 3] = sign * math.inf
+    return (t.to(TDT[dt]).to(DEV) for t in (q, k, v))
+
+
+def _check_infinity(o, v, at, Hq, H, sign, dt, label):
+    """Element 3 of head 0's group is infinite, everything else the mean of the other tokens' values (the low one's weight is
+    below their rounding: e^-12 / 40 = 1.5e-7)."""
+    rest = torch.cat([v[:at], v[at + 1:]]).double().cpu()
+    mean = rest.mean(0).repeat_interleave(Hq // H, 0)
+    o = o.double().cpu()
+    hit = torch.zeros(o.shape, dtype=torch.bool)
+    hit[: Hq // H, 3] = True
+    assert (o[hit] == sign * math.inf).all(), (label, o[hit])
+    tol = 2.0 ** (-8 if dt == "bf16" else -11) * mean.abs() + 2.0 ** -17 * 4.0
+    assert ((o - mean).abs() <= tol)[~hit].all(), label
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,H,D", [(2, 2, 64), (8, 1, 128), (8, 2, 96), (12, 1, 64), (20, 1, 256), (4, 1, 256), (40, 2, 128)])
+def test_an_infinity_with_a_small_weight_stays_one(dt, Hq, H, D):
+    """However small the weight of the token that holds it (one that f16, and one that fp32, has no number for), wherever it
+    lies: before the maximum moves, after it, in a part of its own."""
+    for n, P in ((40, 16), (300, 32), (2100, 16)):
+        for at in (0, n // 2, n - 1):
+            for nats in (12.0, 17.5, 40.0, 100.0, 400.0):
+                sign = 1.0 if at else -1.0
+                label = f"decode {dt} Hq={Hq} H={H} D={D} n={n} at={at} nats={nats}"
+                q, k, v = _one_low_key(n, H, Hq, D, dt, at, nats, sign, n + at)
+                cache, table = _cached(k, v, dt, P)
+                wide = torch.cat([table, torch.full((1, 40), -1, dtype=torch.int32, device=DEV)], 1)
+                for t in (table, wide):  # (a workgroup a segment where the table is short; split and joined)
+                    _check_infinity(fq.attn_decode(q, cache, t, _i32(n))[0], v, at, Hq, H, sign, dt, label)
+    say(f"[gpu] {label}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,H,D", [(2, 2, 64), (8, 1, 128), (4, 1, 96), (3, 1, 256)])
+def test_a_prompts_infinity_with_a_small_weight_stays_one(dt, Hq, H, D):
+    """In whole and in partly masked tiles, and in walks cut into parts; rows before the token do not see it."""
+    for n, rows in ((300, 300), (300, 3), (4000, 1), (4000, 40)):
+        for at in (5, n // 2, n - 2):
+            for nats in (12.0, 17.5, 40.0, 100.0, 400.0):
+                label = f"prompt {dt} Hq={Hq} H={H} D={D} {rows} behind {n} at={at} nats={nats}"
+                q, k, v = _one_low_key(n, H, Hq, D, dt, at, nats, 1.0, n + at)
+                q = q.repeat(rows, 1, 1)
+                o = fq.attn_prefill(q, k, v, _i32(0, rows), _i32(0, n))
+                assert not o.isnan().any(), label
+                first = max(0, at - (n - rows))  # the first row that sees the token
+                assert not o[:first].isinf().any() and (o[first:, : Hq // H, 3] == math.inf).all(), label
+                assert o.isinf().sum() == (rows - first) * (Hq // H), label
+                _check_infinity(o[-1], v, at, Hq, H, 1.0, dt, label)
+                full = fq.attn_prefill(q, k, v, _i32(0, rows), _i32(0, n), causal=False)
+                _check_infinity(full[0], v, at, Hq, H, 1.0, dt, label)
+    say(f"[gpu] {label}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_infinities_of_both_signs_give_nan(dt):
+    n, Hq, H, D = 700, 8, 1, 64
+    q, k, v = _one_low_key(n, H, Hq, D, dt, 20, 30.0, 1.0, 1)
+    v[650, 0, 3], v[4, 0, 9], v[40, 0, 60] = -math.inf, math.nan, -math.inf
+    cache, table = _cached(k, v, dt)
+    for o in (fq.attn_decode(q, cache, table, _i32(n)), fq.attn_prefill(q, k, v, _i32(0, 1), _i32(0, n))):
+        odd = o[0].isnan()
+        assert odd[:, [3, 9]].all() and odd.sum() == 2 * Hq and (o[0, :, 60] == -math.inf).all() and o.isinf().sum() == Hq
