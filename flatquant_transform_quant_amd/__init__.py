@@ -472,9 +472,12 @@ def _same_device(first, *others):
 def _same_gpu(stream, first, *others):
     """The checks of a launching call: all tensors on one GPU (a host address must not reach a kernel), the
     caller's stream one of that GPU's."""
-    if first.device.type != "cuda":
+    d = first.get_device()
+    if d < 0:
         raise ValueError(f"tensors on {first.device}: this call runs on a GPU")
-    _same_device(first, *others)
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
     if stream is not None and stream.device != first.device:
         raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
 
@@ -570,20 +573,18 @@ class KVCache:
                 st = [2 * n for n in st[:3]] + [1 if st[3] == 1 else 2 * st[3]]
             return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _Desc(s.data_ptr(), sdt, s.shape, s.stride())
 
-        at = self._addresses()
+        at = tuple(None if t is None else t.data_ptr() for t in self._tensors)
         (self._kc, self._ks), (self._vc, self._vs) = side(k, k_scale), side(v, v_scale)
         self.pages, self.heads, self.page_size = k.shape[:3]
         self.head_dim = k.shape[3] * (2 if mode in ("int4", "fp4") else 1)
         self._ptrs = (self._kc.ptr, self._ks.ptr if self._ks else None, self._vc.ptr, self._vs.ptr if self._vs else None)
         self._at = at
 
-    def _addresses(self):
-        k, v, ks, vs = self._tensors
-        return k.data_ptr(), v.data_ptr(), None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr()
-
     def _args(self):
         """Addresses of the four descriptors of a call (built anew where a tensor's memory has moved)."""
-        if self._addresses() != self._at:
+        k, v, ks, vs = self._tensors
+        a, b, c, d = self._at
+        if k.data_ptr() != a or v.data_ptr() != b or (ks is not None and (ks.data_ptr() != c or vs.data_ptr() != d)):
             self._describe()
         return self._ptrs
 
@@ -658,7 +659,8 @@ def attn_decode(q, cache: KVCache, block_table, lengths, scale: float = 0.0, out
     torch = _torch()
     _same_gpu(stream, cache.k, q, block_table, lengths, out, lse, workspace)
     if out is None:
-        out = _new(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
+        make = lambda: torch.empty_like(q, memory_format=torch.contiguous_format)  # noqa: E731
+        out = make() if stream is None else _new(stream, make)
     d = _Descs(q, block_table, lengths, out, lse)
     qp, bp, lp, op, sp = d.ptrs
     held = cache._args()
@@ -699,7 +701,8 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
         cu_k = cu_q
     _same_gpu(stream, q, k, v, cu_q, cu_k, out, lse, workspace)
     if out is None:
-        out = _new(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
+        make = lambda: torch.empty_like(q, memory_format=torch.contiguous_format)  # noqa: E731
+        out = make() if stream is None else _new(stream, make)
     d = _Descs(q, k, v, cu_q, cu_k, out, lse)
     qp, kp, vp, ap, bp, op, sp = d.ptrs
     causal = 1 if causal else 0
