@@ -29,8 +29,7 @@
 //     the largest of the tile (keys) or to a running reference (values), along with it.
 // A bf16 q is brought to f16 by a power of two per row (28 binades keep full precision).  The
 // value scale of a token multiplies its weight: w = p scale 2^-R rounded to f16, with R a
-// running reference exponent, so that w stays in range; a scale below 2^-24 of the largest
-// one in a sequence loses bits in proportion.
+// running reference exponent, so that w stays in range.
 // The weights' rounding would be most of the result's error.  With at most 8 heads in a group the
 // tile has columns to spare: they take the same heads with the remainders w - f16(w) as weights, so
 // the weights count with twice the bits and the matrix cores have no more to do.  The remainders go in
@@ -64,6 +63,11 @@ constexpr int kMaxGrid = 1024;               // workgroups of a launch at most: 
 constexpr int kHeldLengths = 512;            // lengths kept in LDS (those of later sequences are read again)
 constexpr float kLazy = 8.0f;                // base-2 slack of the running maximum
 constexpr float kInf = __builtin_inff();
+
+// An exponent that widens the range of the f16 weights at no cost (exact, taken off again at the end).  They reach 2^8 above the running maximum's, and at most 2^2 more by a token's value scale
+//     (see ref_lim), so this ends at 2^15.
+template <int MODE, int PDT>
+constexpr int kUpP = PDT != kF16 ? 0 : (MODE == kKv16 || MODE == kKvFp4) ? 7 : 5;
 
 template <int MODE>
 constexpr int kBits = MODE == kKv16 ? 16 : (MODE == kKvInt8 || MODE == kKvE4M3) ? 8 : 4;
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     float m = -kInf, l = 0.0f;
     int ref = -100000;      // exponent R of the value scales (wave-uniform); far below any
     float ref_inv = 0.0f;   // 2^-R
-    float ref_lim = 0.0f;   // a scale at or above 2^(R + 6) moves R
+    float ref_lim = 0.0f;   // a scale at or above 2^(R + 2) moves R
 
     // ---- q as the B operand, and the column's constants
     u32x4_t qf[S::KS];
@@ -571,7 +575,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 #pragma unroll
           for (int j = 0; j < S::EC; ++j) acc[h][j] *= f;
       }
-      const float ms = m == -kInf ? 0.0f : m;
+      const float ms = m == -kInf ? 0.0f : m - kUpP<MODE, PDT>;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s[i] = __builtin_amdgcn_exp2f(s[i] - ms);
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
           if (r > ref && r > -127) {
             move_ref(r);
             ref_inv = pow2(min(-r, 127));
-            ref_lim = r + 6 > 127 ? kInf : pow2(max(r + 6, -126));
+            ref_lim = r + 2 > 127 ? kInf : pow2(max(r + 2, -126));
           }
         }
 #pragma unroll
@@ -717,7 +721,8 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
     // ---- the four waves' sums joined; the whole segment's rows out, or its part to the workspace
     // (lane indices redefined: what derives from them is not kept in registers across the steps)
     const int el = static_cast<int>(here(lane)), er = el & 15, eb = el >> 4;
-    l = column_sum(l);
+    constexpr float down = 1.0f / (1 << kUpP<MODE, PDT>);
+    l = column_sum(l) * down;
     if (eb == 0) {
       s_m[wv][er] = m;
       s_l[wv][er] = l;
@@ -729,7 +734,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][er]);
       float f = m == -kInf ? 0.0f : rescale(m, mx);
       if (m != m || mx == kInf) f = __builtin_nanf("");
-      if (MODE != kKv16) f *= kCode;
+      f *= kCode * down;
       const int e = kScaled ? (ref < -1000 ? 0 : ref) : MODE == kKvFp4 ? (ref < -1000 ? 0 : ref - 127) : 0;
 #pragma unroll
       for (int h = 0; h < S::NH; ++h)

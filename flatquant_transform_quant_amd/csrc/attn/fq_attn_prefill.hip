@@ -55,6 +55,11 @@ constexpr int kKeys = 64;           // keys of a tile
 constexpr int kAhead = 4;           // fragments read ahead of their products (2, 6 and 8: the same to 2% slower)
 constexpr int kMaxParts = 32, kMinChunk = 8, kEnough = 512;  // see parts_of()
 constexpr float kLazy = 8.0f;
+// Weights as they enter the second product are 2^kUp times those above (at most 2^(8 + kUp), f16's largest binade):
+// an f16 weight is then off by 2^-32 of the largest one where it is subnormal, not by 2^-25, which many keys far
+// below one that stands out lost altogether (20000 of them 17.5 nats below: 5e-4 of the weights).
+template <int DT>
+constexpr float kUp = DT == kF16 ? 7.0f : 0.0f;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
 
@@ -364,7 +369,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[d][i] *= f;
       }
-      const float ms = m == -kInf ? 0.0f : m;
+      const float ms = m == -kInf ? 0.0f : m - kUp<DT>;
       u32x4_t pf[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -420,15 +425,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
   }
 
   l = half_sum(l);
+  const float down = DT == kF16 ? 0x1p-7f : 1.0f;  // 2^-kUp
   if (split) {  // the part's sums as they are, [element][row], with m and l
     float* const o = ws + (static_cast<int64_t>(blockIdx.x)) * ((DP + 2) * kRows) + 32 * wv + col;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kRows] = acc[d][i];
+      for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kRows] = acc[d][i] * down;
     if (hf == 0) {
       o[DP * kRows] = m;
-      o[(DP + 1) * kRows] = l;
+      o[(DP + 1) * kRows] = l * down;
     }
     return;
   }
@@ -448,7 +454,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
                   round16x2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
     }
   if (a.lse && hf == 0 && row < lq)
-    a.lse[static_cast<int64_t>(q0 + row) * a.Hq + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l)) * 0.693147181f;
+    a.lse[static_cast<int64_t>(q0 + row) * a.Hq + head] = l == 0.0f ? -kInf : (m + __builtin_amdgcn_logf(l * down)) * 0.693147181f;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 32 * kPieces / 64; ++i) {

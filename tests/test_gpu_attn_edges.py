@@ -139,3 +139,66 @@ def test_infinities_of_both_signs_give_nan(dt):
     for o in (fq.attn_decode(q, cache, table, _i32(n)), fq.attn_prefill(q, k, v, _i32(0, 1), _i32(0, n))):
         odd = o[0].isnan()
         assert odd[:, [3, 9]].all() and odd.sum() == 2 * Hq and (o[0, :, 60] == -math.inf).all() and o.isinf().sum() == Hq
+
+
+# ---- many tokens far below one that stands out ------------------------------------------------------
+
+def _sink(n, H, Hq, D, dt, at, nats, seed):
+    """Token `at` scores `nats` above all others, which score 0, and has a value of 0; the others' values are near 1."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = torch.ones(1, Hq, D), torch.zeros(n, H, D)
+    k[at] = nats / math.sqrt(D)
+    v = 1.0 + 0.25 * torch.rand(n, H, D, generator=g)
+    v[at] = 0.0
+    return (t.to(TDT[dt]).to(DEV) for t in (q, k, v))
+
+
+def _sink_want(k, v, D):
+    """fp64: out [H, D] of the rows as they are kept (q all ones), and the largest |v|."""
+    s = k.double().cpu().sum(-1) / math.sqrt(D)
+    p = torch.softmax(s, 0)
+    return (p[..., None] * v.double().cpu()).sum(0), float(v.double().abs().max())
+
+
+def _sink_check(o, want, vmax, n, dt, p_bits, g, label):
+    """The output's rounding, 2^-11 (2^-8 in bf16) of it; the weights': 2^-11 relative (2^-8 where bf16 products take them
+    once) or `p_bits` bits below the largest, whichever is more; scores of 17 in fp32 to 2^-20, sums of n terms."""
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    tol = want.abs() * (2 * u + 2.0 ** -18 + math.sqrt(n) * 2.0 ** -23) + n * 2.0 ** -p_bits * vmax + 2.0 ** -25
+    o = o.double().cpu()
+    want, tol = (t.repeat_interleave(g, 0) for t in (want, tol))
+    worst = float(((o - want).abs() / tol).max())
+    say(f"[gpu] {label}: worst {worst:.3f} of its bound")
+    assert worst <= 1.0, label
+
+
+@pytest.mark.parametrize("mode", ["f16", "bf16", "int8", "e4m3", "int4", "fp4"])
+@pytest.mark.parametrize("Hq,H,D", [(4, 1, 64), (16, 1, 128), (12, 1, 256), (9, 1, 96)])
+def test_many_tokens_far_below_one(mode, Hq, H, D):
+    """20000 tokens, each with 2.5e-8 of the largest weight, make 5e-4 of the sum: below f16's smallest number one by one.
+    Weights are held to 2^-32 of the largest (2^-30 with a scale a token) and in two parts with up to 8 heads a group.  Alone
+    the sequence is cut into many runs, most without the large weight; 520 times (in the same pages) into few."""
+    n, nats = 20000, 17.5
+    for dt in ("f16", "bf16") if mode not in ("f16", "bf16") else (mode,):
+        for at in (0, 10007):
+            q, k, v = _sink(n, H, Hq, D, dt, at, nats, 3)
+            cache, table = _cached(k, v, mode, 64)
+            kk, vv = (k, v) if mode == dt else fq.kv_read(cache, table, _i32(0, n), n, torch.float16)
+            want, vmax = _sink_want(kk, vv, D)
+            bits = 35 if Hq <= 8 else 32 if mode in ("f16", "bf16", "fp4") else 30
+            for B in (1, 520):
+                o = fq.attn_decode(q.repeat(B, 1, 1), cache, table.repeat(B, 1), _i32(n).repeat(B))
+                for b in {0, B // 2, B - 1}:
+                    _sink_check(o[b], want, vmax, n, dt, bits, Hq // H, f"{mode} {dt} Hq={Hq} D={D} at={at} {b} of {B}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,H,D", [(2, 1, 64), (2, 2, 128), (1, 1, 200)])
+def test_a_prompts_many_tokens_far_below_one(dt, Hq, H, D):
+    n, nats = 20000, 17.5
+    for at in (0, 10007):
+        q, k, v = _sink(n, H, Hq, D, dt, at, nats, 4)
+        want, vmax = _sink_want(k, v, D)
+        for rows in (1, 200):
+            o = fq.attn_prefill(q.repeat(rows, 1, 1), k, v, _i32(0, rows), _i32(0, n))
+            _sink_check(o[-1], want, vmax, n, dt, 32, Hq // H, f"prompt {dt} Hq={Hq} D={D} at={at} rows={rows}")
