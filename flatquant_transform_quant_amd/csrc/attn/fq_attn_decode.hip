@@ -64,10 +64,13 @@ constexpr int kHeldLengths = 512;            // lengths kept in LDS (those of la
 constexpr float kLazy = 8.0f;                // base-2 slack of the running maximum
 constexpr float kInf = __builtin_inff();
 
-// An exponent that widens the range of the f16 weights at no cost (exact, taken off again at the end).  They reach 2^8 above the running maximum's, and at most 2^2 more by a token's value scale
+// Exponents that widen the range of the f16 operands at no cost (all exact, taken off again at the end):
+//   kUpP: of the weights.  They reach 2^8 above the running maximum's, and at most 2^2 more by a token's value scale
 //     (see ref_lim), so this ends at 2^15.
+//   kUpK, kUpV: of E2M1 keys and values, at most 6 (values 6 2^1, see ref), so these end below 2^16.
 template <int MODE, int PDT>
 constexpr int kUpP = PDT != kF16 ? 0 : (MODE == kKv16 || MODE == kKvFp4) ? 7 : 5;
+constexpr int kUpK = 13, kUpV = 12;
 
 template <int MODE>
 constexpr int kBits = MODE == kKv16 ? 16 : (MODE == kKvInt8 || MODE == kKvE4M3) ? 8 : 4;
@@ -507,10 +510,10 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
 #pragma unroll
         for (int ks = 0; ks < S::KS; ++ks) {
           constexpr int E = S::CE / 8;
-          const float f = MODE == kKvFp4 ? (x.e8[t][ks / E] == 255u ? __builtin_nanf("") : pow2(static_cast<int>(x.e8[t][ks / E]) - ek)) : 0.0f;
+          const float f = MODE == kKvFp4 ? (x.e8[t][ks / E] == 255u ? __builtin_nanf("") : pow2(static_cast<int>(x.e8[t][ks / E]) - ek + kUpK)) : 0.0f;
           z = mfma16x16x32<PDT>(key_operand<MODE, S::KW>(x.w[t][ks / E], ks % E, f), qf[ks], z);
         }
-        const float cf = MODE == kKvFp4 ? __builtin_amdgcn_ldexpf(cq, ek - 127) : cq;
+        const float cf = MODE == kKvFp4 ? __builtin_amdgcn_ldexpf(cq, ek - 127 - kUpK) : cq;
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[4 * t + i] = z[i] * (kScaled ? cf * x.scale[t][i] : cf);
       }
@@ -599,7 +602,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int h = 0; h < S::NH; ++h) ev = max(ev, x.e8[i][h] == 255u ? 0 : static_cast<int>(x.e8[i][h]));  // (255: NaN)
-        if (__any(ev > ref + 6)) move_ref(__builtin_amdgcn_readfirstlane(wave_imax(ev)));
+        if (__any(ev > ref + 1)) move_ref(__builtin_amdgcn_readfirstlane(wave_imax(ev)));
       }
       if constexpr (kScaled) {
         if (!whole) {  // (the scales of tokens past n may be anything)
@@ -671,8 +674,8 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
                 e1[1] = fp8_to_f16x2<true>(y1[q]);
               } else {
                 const uint32_t b0 = x.e8[2 * p][h], b1 = x.e8[2 * p + 1][h];
-                const float f0 = b0 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b0) - ref);
-                const float f1 = b1 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b1) - ref);
+                const float f0 = b0 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b0) - ref + kUpV);
+                const float f1 = b1 == 255u ? __builtin_nanf("") : pow2(static_cast<int>(b1) - ref + kUpV);
                 e0[0] = q ? fp4_to_f16x2<2>(y0[0], f0) : fp4_to_f16x2<0>(y0[0], f0);
                 e0[1] = q ? fp4_to_f16x2<3>(y0[0], f0) : fp4_to_f16x2<1>(y0[0], f0);
                 e1[0] = q ? fp4_to_f16x2<2>(y1[0], f1) : fp4_to_f16x2<0>(y1[0], f1);
@@ -735,7 +738,7 @@ __global__ __launch_bounds__(kThreads, (Shape<MODE, DP, PAD>::per_cu)) void deco
       float f = m == -kInf ? 0.0f : rescale(m, mx);
       if (m != m || mx == kInf) f = __builtin_nanf("");
       f *= kCode * down;
-      const int e = kScaled ? (ref < -1000 ? 0 : ref) : MODE == kKvFp4 ? (ref < -1000 ? 0 : ref - 127) : 0;
+      const int e = kScaled ? (ref < -1000 ? 0 : ref) : MODE == kKvFp4 ? (ref < -1000 ? 0 : ref - 127 - kUpV) : 0;
 #pragma unroll
       for (int h = 0; h < S::NH; ++h)
 #pragma unroll

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import flatquant_transform_quant_amd as fq
+from attn_ref import bound, softmax_attend
 from gpu_util import DEV, say
 
 pytestmark = pytest.mark.gpu
@@ -202,3 +203,28 @@ def test_a_prompts_many_tokens_far_below_one(dt, Hq, H, D):
         for rows in (1, 200):
             o = fq.attn_prefill(q.repeat(rows, 1, 1), k, v, _i32(0, rows), _i32(0, n))
             _sink_check(o[-1], want, vmax, n, dt, 32, Hq // H, f"prompt {dt} Hq={Hq} D={D} at={at} rows={rows}")
+
+
+@pytest.mark.parametrize("Hq,H,D", [(4, 1, 64), (16, 1, 128), (2, 1, 256), (6, 2, 96)])
+def test_e2m1_groups_of_very_different_sizes(Hq, H, D):
+    """A group of 32 far smaller than its tokens' others counts with all its bits where it is what matters: keys 2^26 smaller,
+    under a q that is 0 for the others; values 2^25 smaller, whose outputs are their own."""
+    n = 200
+    g = torch.Generator().manual_seed(6)
+    code = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])[torch.randint(0, 8, (2, n, H, D), generator=g)]
+    code *= torch.where(torch.rand(code.shape, generator=g) < 0.5, -1.0, 1.0)
+    code[..., ::32] = 6.0  # (the group's largest: its exponent is then the size's)
+    size = torch.ones(2, D)
+    size[0, 32:64], size[1, 32:64] = 2.0 ** -26, 2.0 ** -25
+    k, v = (code[i] * size[i] for i in range(2))
+    q = torch.zeros(1, Hq, D)
+    q[..., 32:64] = 2.0 ** 24 * torch.randn(1, Hq, 32, generator=g)
+    q, k, v = q.bfloat16(), k.bfloat16(), v.bfloat16()
+    cache, table = _cached(k.to(DEV), v.to(DEV), "fp4")
+    kept = fq.kv_read(cache, table, _i32(0, n), n, torch.bfloat16)
+    assert torch.equal(kept[0].cpu(), k) and torch.equal(kept[1].cpu(), v)
+    out, _, absv, top, vmax = softmax_attend(q.double(), k.double(), v.double(), torch.tensor([n]), 1 / math.sqrt(D))
+    o = fq.attn_decode(q.to(DEV), cache, table, _i32(n)).cpu().double()
+    worst = ((o - out).abs() / bound(out, absv, top, vmax, n, D, "bf16", "f16")).max()
+    say(f"[gpu] groups Hq={Hq} H={H} D={D}: worst {float(worst):.3f} of its bound")
+    assert worst <= 1.0
