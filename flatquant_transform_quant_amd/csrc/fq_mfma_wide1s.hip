@@ -72,9 +72,10 @@ __device__ __forceinline__ i32x4 rsrc4(const void* p, uint32_t bytes) {
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// One LDS-DMA load: lane l's 16 bytes at rsrc + voff + soff go to LDS lds + 16 l.
+// One LDS-DMA load: lane l's 16 bytes at rsrc + voff + soff go to LDS lds + 16 l.  (A load that takes its
+// place from m0 needs one wait state after m0's write, which nobody adds inside an assembly block.)
 __device__ __forceinline__ void dma16(uint32_t lds, int voff, i32x4 rs, int soff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rs), "s"(soff)
                : "memory", "m0");
