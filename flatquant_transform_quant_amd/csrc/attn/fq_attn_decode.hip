@@ -1,12 +1,12 @@
 // Attention of one new token per sequence over the paged cache.
 //
 // For a cache head and its g query heads: s[t, h] = <q_h, k_t>, p = softmax over t, o_h = sum_t
-// p[t, h] v_t.  Every cached byte is used for g <= 16 heads at once, so the products run on the
-// matrix cores with the heads as the 16 columns of a tile (heads beyond 16 take further tiles)
-// and the kernel is bound by reading the cache: int8, 8 cache heads of 128, 64 query heads, 64
-// sequences of 1024 to 16384 tokens (756 MB) 151 us, 5.0 TB/s, two of up to 131072 (492 MB) 97 us, 5.0;
-// a large copy moves 5.2.  4 bits are bound by the vector instructions that widen them: 128 sequences
-// (783 MB) 209 us in int4, 187 in E2M1, 3.7 and 4.2 TB/s.  Small calls are a chain of latencies: workgroups
+// p[t, h] v_t.  Every cached byte is used for up to 16 heads at once, so the products run on the
+// matrix cores with the heads as the 16 columns of a tile (heads beyond 16 take further tiles, which read
+// the cache again) and the kernel is bound by reading the cache: int8, 8 cache heads of 128, 64 query heads, 64
+// sequences of 1047 to 16384 tokens (756 MB) 148 us, 5.1 TB/s, two of up to 131072 (492 MB) 97 us, 5.0;
+// a large copy moves 5.2.  4 bits are bound by the vector instructions that widen them: 128 sequences of
+// the same lengths (783 MB) 171 us in int4, 174 in E2M1, 4.6 and 4.5 TB/s.  Small calls are a chain of latencies: workgroups
 // start over 2 to 4 us, a run's plan takes 1.5 to 3, its pages and first keys 3, a step of 128 tokens 2 (3 at
 // full bandwidth), the join 5 (37 sequences of up to 2000 tokens, E4M3, 39 MB: 20.4 us).
 //
@@ -18,7 +18,7 @@
 //     stand (contraction slot j of lane group l / 16 is token 16 (j / 4) + 4 (l / 16) + j % 4).
 //     V^T's row is an element d; a lane reads EC consecutive elements of its 8 tokens and pairs
 //     them across tokens with byte permutes: product jj takes element EC (l % 16) + jj.
-// Codes enter the products exactly, as f16 numbers (16-bit caches: as they are):
+// Codes enter the products as f16 numbers, exactly but for what is said of E2M1 (16-bit caches: as they are):
 //   int8, int4: the code plus 128 or 8 (u >= 0) in the low bits of a half is the f16 subnormal
 //     u 2^-24, so widening costs a byte permute or a mask; one packed fused multiply-add makes it
 //     the number (u - 128) 2^-9 or (u - 8) 2^-9, exactly.  (Subnormals themselves as operands lose
@@ -26,14 +26,19 @@
 //     in and taken off the sums costs as much where a row's codes are small.)  Nibbles masked at
 //     bits 4..7 are 16 u: q carries 1/16 at those elements, the output is divided by 16.
 //   E4M3, E2M1: the converting instructions; E2M1 takes its group's power of two, relative to
-//     the largest of the tile (keys) or to a running reference (values), along with it.
+//     the largest of the 32 tokens (keys) or to a running reference (values), along with it, and 2^13 (2^12) more:
+//     a group 2^26 (2^25) smaller is still of normal f16 numbers, one 2^36 smaller is gone.
 // A bf16 q is brought to f16 by a power of two per row (28 binades keep full precision).  The
 // value scale of a token multiplies its weight: w = p scale 2^-R rounded to f16, with R a
 // running reference exponent, so that w stays in range.
-// The weights' rounding would be most of the result's error.  With at most 8 heads in a group the
+// The weights are the second product's operand and have its type: 11 bits (8 where the cache is bf16), and in f16
+// no less than 2^-24; kUpP below puts them at the upper end of that.  Their rounding would be most of the
+// result's error.  With at most 8 heads in a group the
 // tile has columns to spare: they take the same heads with the remainders w - f16(w) as weights, so
 // the weights count with twice the bits and the matrix cores have no more to do.  The remainders go in
-// times 2^11: those of weights below 2^-14, where f16 has fewer bits, keep theirs.
+// times 2^11: those of weights below 2^-14, where f16 has fewer bits, keep theirs.  With more heads there is no
+// such room: a weight is off by 2^-11 (2^-8) of itself, or 2^-32 of the largest one (2^-30 where it carries a
+// scale), and a token whose scale is below 2^-19 of the largest in its sequence loses bits in proportion.
 // Softmax statistics are fp32: the running maximum m (base-2 scores) is only moved when a score
 // passes m + 8 (weights then reach 2^8, far inside f16's range), so the common tile has no
 // cross-lane step and no rescaling.
@@ -41,8 +46,8 @@
 // Split: the units of work are 128 tokens (4 waves x 32) of a (sequence, cache head, head tile);
 // all units in order are dealt to the grid in equal runs, whatever the lengths; a segment counts two
 // or three units more than it has, for its page lookup, first loads and rows out (else the runs over
-// many short segments end last: 64 sequences of 1024 to 16384 tokens, int8, 157 us without, 152, 151,
-// 152 with one to three; the same of 128 in int4 218, 219, 215 and 210, 208 with four).  A run that
+// many short segments end last: the 64 sequences above, int8, 153 us without, 150, 147, 149, 155 with one
+// to four; the 128 in int4 189, 182, 175, 171, 172, in E2M1 191, 184, 178, 174, 175).  A run that
 // holds only part of a segment leaves its unnormalised sums and (m, l) in the workspace, and a second
 // launch joins them in a fixed order.  A segment's first loads are under way while the rows of the one
 // before are written.
@@ -91,10 +96,11 @@ struct Shape {
   // units that a segment's beginning and end (page lookup, first loads, rows out) count as, see above
   static constexpr int start = bits == 4 ? 3 : 2;
   // Workgroups of a CU (waves of a SIMD): as many as registers and, at 256, LDS hold without spills in
-  // the loop.  us with 1, 2, 3, 4: 64 sequences of up to 16384 tokens, int8 at 128: 212, 158, 170, 455;
-  // 128 of them, int4: 349, 242, 220, 248; 32 of up to 4096, 16 bits at 128: 39, 37, 39, 62, at 256:
-  // 119, 170, 128, 131 and int8 at 256: 75, 68, 97, 109; 64 of up to 8192 at 64, int8: 115, 77, 68, 69,
-  // int4 199, 125, 107, 103, 16 bits 116, 113, 117, 121 -- but 37 short ones at 64: 48, 31, 25, 24.
+  // the loop.  us with 1, 2, 3, 4: the 64 sequences above, int8 at 128: 182, 148, 173, 483; the 128, int4:
+  // 308, 198, 171, 241; 32 of 147 to 4096, 32 heads on 8, 16 bits at 128: 33, 38, 52, 82; 32 of 535 to 4096, 16
+  // heads on 4, at 256, 16 bits: 45, 111, 51, 59, int8: 35, 35, 50, 62, int4: 31, 29, 46, 58; 64 of 1041 to 8192,
+  // 16 heads at 64, int8: 167, 106, 94, 98, int4: 146, 93, 79, 74, 16 bits: 164, 163, 169, 167 -- and 37 of 43 to
+  // 2000 there, E4M3: 29, 21, 20, 20.
   static constexpr int per_cu = DP == 256 ? (bits == 16 ? 1 : 2) : DP == 64 ? 4 : bits == 4 ? 3 : 2;
 };
 
@@ -208,17 +214,6 @@ __device__ __forceinline__ int32_t length_of(const DecodeArgs& a, int b) {
 __device__ __forceinline__ int32_t units_of(int32_t n) { return n / kUnit + (n % kUnit != 0); }
 // what a segment counts as when the work is dealt (see the top)
 __device__ __forceinline__ int32_t weight_of(int32_t n, int start) { return n > 0 ? units_of(n) + start : 0; }
-
-// Inclusive sum over the lanes up to each lane (DPP row shifts, then the rows' last lanes).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
 
 // Workgroup i of `runs` (at most `total`; all below 2^31, which the host checks) has the units from
 // start(i) = i total / runs up to start(i + 1); unit u is in run of(u).
@@ -924,10 +919,11 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
 }
 
 // Whether a segment is one workgroup's whatever its length, with no plan and no join: a table that
-// reaches 4 units at most, or 8 with a segment for each CU.  us split and joined, and so: one sequence of
-// 250 tokens (8 segments) 10.5 and 7.1, of 510 10.7 and 9.5, of 880 10.7 and 13.0; 32 of up to 500 (256
-// segments) 15.4 and 11.0, up to 1000 18.5 and 16.6, up to 2000 25 and 27; 64 of 1000 33 and 25, of 2000
-// 48 and 43; 37 of up to 1000 with 16 heads 16.6 and 15.1, up to 2000 20.6 and 25.5.
+// reaches 4 units at most, or 8 with a segment for each CU.  us a call split and joined, and so (8 of either are
+// the host's): one sequence of 250 tokens, 32 heads on 8 of 128, bf16 (8 segments) 12.2 and 9.5, of 510 12.9
+// and 10.0, of 880 12.5 and 13.2; 32 of 62 to 500 (256 segments) 15.7 and 10.3, of 125 to 1000 19.1 and 17.3, of
+// 250 to 2000 30.0 and 28.5; 64 of 1000, int8, 28.6 and 26.3, of 2000 50.3 and 47.7; 37 of up to 1000, E4M3, 16
+// heads of 64 16.0 and 15.3, of up to 2000 20.3 and 26.6.
 bool single_of(int64_t segments, int64_t reach) { return reach <= (segments >= 256 ? 8 : 4) * kUnit; }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -946,13 +942,13 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   decode_kernel<MODE, DT, DP, PAD><<<grid, kThreads, 0, s>>>(a, part, nht, gh, false);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // Enough workgroups of the join to fill the device, at most one a head.  us with one a segment, and so:
-  // 2 sequences of up to 131072, 8 heads each on 8: 128 and 103; 16 of up to 8192, 32 heads on 1: 61 and
-  // 26; 8 of up to 1500: 19 and 15; 128 of up to 16384 the same.
+  // Enough workgroups of the join to fill the device, at most one a head.  us with one a segment, and so: 2
+  // sequences of 87381 and 131072 tokens, int8, 64 heads on 8: 120 and 93; 16 of 1000 to 8192, 32 heads on 1: 65
+  // and 24; 8 of 190 to 1500, 32 on 8: 18 and 14.
   const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
-  // And where that leaves few, slices of 16 elements at least: one sequence of 131072 tokens, 8 heads on 1, 74
-  // us whole and 25 so, of 8192, 32 on 8, 18.6 and 15.4; the two of up to 131072 103 and 101; 8 of up to 1500
-  // 14.5 and 14.6 (15.1 at 512 workgroups).
+  // And where that leaves few, slices of 16 elements at least: one sequence of 131072 tokens, int4, 8 heads on
+  // 1, 75 us whole and 25 so, of 60883, 16 heads of 64 on 2, 31 and 18, of 8192, 32 on 8, 18.7 and 15.5; the two
+  // long ones 93 and 92; the eight short ones the same.
   uint32_t nz = 1;
   while (nz < DP / 16 && segments * ny * nz * 2 <= 256) nz *= 2;
   decode_join_kernel<DT, DP><<<dim3(static_cast<uint32_t>(segments), ny, nz), kThreads, 0, s>>>(a, part, nht, gh, grid, Shape<MODE, DP, PAD>::start);

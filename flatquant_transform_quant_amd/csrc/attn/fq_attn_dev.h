@@ -12,6 +12,17 @@ namespace fq {
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 
+// Inclusive sum over the lanes up to each lane (DPP row shifts, then the rows' last lanes).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 // Index of token t of a sequence as (page, offset): page < 0 where the table has no page of this
 // cache for it (short table, entry out of range), and such a token is not followed further.
 __device__ __forceinline__ int32_t kv_page(const BlockTable& bt, int64_t b, int32_t t, int32_t page_log, int32_t pages) {

@@ -17,6 +17,9 @@
 // LDS layouts: the 16-byte piece c of tile row r sits at c ^ (r & 15) (keys) or c ^ 4 (r & 3)
 // (values); with rows of 128 bytes, where two rows share the 64 banks, at c ^ ((r >> 1) & 7) and
 // c ^ 4 ((r >> 1) & 1): both kinds of read then touch every bank once.
+// The weights have the values' type, as the instruction asks: 11 bits, in bf16 8 (the sums l take them unrounded).
+// The result's error is 1.0 to 1.4 times what fp32 weights leave, the output's own rounding in both; a second
+// product with the remainders would cost half as much matrix time again.
 // The maximum is moved only when a score passes m + 8 in base-2 units (weights then reach 2^8):
 // the accumulators are rescaled a few times a walk instead of every tile.
 // Tiles of all sequences are handed out longest walk first; where they do not fill the device, the
@@ -28,11 +31,11 @@
 //
 // What bounds it: one 32768-row prompt, 8 heads on one cache head of 128, takes 1.93 to 2.03 ms (1.08 to
 // 1.14 PFLOP/s; a large library product reaches 1.25 to 1.39 here) with the matrix cores busy 61% of the
-// time at a clock of 1.80 GHz, which the power of products, LDS reads, copies and exponentials together
+// time at a clock of 1.8 GHz, which the power of products, LDS reads, copies and exponentials together
 // sets: without any one of them the rate is 1.25 to 1.27, without all but the products 1.67.  Smaller
-// calls run at 2.0 GHz and 47%: nine packed prompts of 242 to 4096 rows, 32 heads, 315 us (905 TFLOP/s),
+// calls run at 2.0 GHz and 47%: nine packed prompts of 242 to 4096 rows, 32 heads, 306 to 314 us (910 to 930 TFLOP/s),
 // where a workgroup spends 3.4 us before its first and after its last tile each (places, query rows,
-// rows out) and 1.76 us a tile; four chunks of 313 to 1024 rows behind 2507 to 8192 keys, 215 us (855),
+// rows out) and 1.76 us a tile; four chunks of 313 to 1024 rows behind 2507 to 8192 keys, 212 to 222 us (830 to 870),
 // where the device's 512 places are 81% busy, the longest walk being 133 tiles and the mean 97.
 // Tile and schedule, TFLOP/s on those three (prompt, packed, chunks) and 2 x 8192 rows of 64:
 //   128 rows, 4 waves (this)                                          1128  867  669*  826
@@ -107,16 +110,6 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Inclusive sum over the lanes before and at each lane (DPP row shifts, then the rows' last lanes).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
 // the largest over the wave
 __device__ __forceinline__ int wave_top(int v) {
   v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xF, 0xF, false));
@@ -176,18 +169,14 @@ __device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int part
       if (rank >= total) return p;
       const int first = max(0, kn - n + kRows - 1) / kRows;  // level of the sequence's tile 0 (0 where no key is ahead)
       auto above = [&](int level) { return max(0, min(nt, first + nt - level)); };  // this sequence's tiles at or above
-      int lo = 0, hi = 1 << 24;  // tiles at or above lo: more than rank; at or above hi: not
-      hi = wave_top(first + nt);
+      int lo = 0, hi = wave_top(first + nt);  // tiles at or above lo: more than rank; at or above hi: not
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (wave_total(above(mid)) > rank) lo = mid; else hi = mid;
       }
       const int in = rank - wave_total(above(lo + 1));  // the in-th sequence with a tile of level lo
-      // (level 0 can hold several tiles of a sequence: those that see no key before the prefix)
-      const int here = above(lo) - above(lo + 1), incl = wave_scan(here);
-      w = __builtin_ctzll(__ballot(incl > in));
-      const int t = max(0, lo - first) + (incl - 1 - in);
-      p.tile = __builtin_amdgcn_readlane(t, w);
+      w = __builtin_ctzll(__ballot(wave_scan(above(lo) - above(lo + 1)) > in));
+      p.tile = lo - __builtin_amdgcn_readlane(first, w);
     } else {
       const int incl = wave_scan(nt), sum = __builtin_amdgcn_readlane(incl, 63);
       if (rank >= sum) {
@@ -514,11 +503,13 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // workgroups of a launch that does not split: tiles of all sequences (at most one partial one each)
 int64_t workgroups(int64_t Tq, int64_t B, int64_t Hq) { return (Tq / kRows + B) * Hq; }
 
-// Parts that the longest walk may be cut into.  The device runs 512 workgroups at a time (two a CU);
-// with fewer, the longest walk alone is the whole time.  us in up to 8, 16, 32 and 64 parts: 128 rows
-// behind 32768 keys, 32 heads (64 workgroups) 97, 96, 96, 96 (546 in one); 64 rows, 8 heads 82, 53, 46, 46;
-// 16 rows behind 131072, 8 heads 284, 157, 105, 124.  In one part and so: 512 rows behind 16384, 64 heads (320)
-// 315 and 281.  A part's sums go through memory (66 KB at 128), so nothing is split once the device is full:
+// Parts that the longest walk may be cut into.  The device runs 512 workgroups at a time (two a CU; 768 of heads
+// of 64); with fewer, the longest walk alone is the whole time.  us in one part and so: 128 rows behind 32768 keys, 32
+// heads (64 workgroups) 546 and 88 (without a mask 538 and 85); 64 rows, 8 heads 540 and 44; 16 rows behind 131072, 8
+// heads 2137 and 97; 200 behind 2800, 32 heads 56 and 26; 512 behind 16384, 64 heads (320) 293 and 268; 1855 rows, 8
+// heads of 256 70 and 41; 1024 rows, 8 heads 23 and 19; 1000, 32 heads 25 and 24.  In up to 8, 16, 32 and 64 parts
+// (on a slower card): 128 rows behind 32768 97, 96, 96, 96; 64 82, 53, 46, 46; 16 behind 131072 284, 157, 105, 124.
+// A part's sums go through memory (66 KB at 128), so nothing is split once the device is full:
 // chunks of 313 to 1024 rows behind up to 8192 keys, 32 heads (736): 204 whole, 227 in two parts, 261 in three
 // (cut at the mean load alone 226; dealt out in equal runs 241, as walks that no longer go side by side
 // share fewer keys in L2).  Parts of 8 tiles at least: 1024 rows, 8 heads 19 us, of 16 tiles 23.  Where two

@@ -301,9 +301,17 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
  * <q, k[t]>).  A length of 0 (an idle place of a fixed batch) gives zeros and lse = -infinity.
  * A token whose table entry is outside the cache is left out of the sum; cache contents past a
  * sequence's length are never used, whatever they hold.  |scale| <= 2^127; 0 means 1/sqrt(D).
- * Codes enter the products exactly; scores, softmax statistics and sums are fp32.  Results do
- * not depend on the run: the same inputs give the same bits.
- * The cache is read once, split over its length across the device and joined; the partial sums
+ * Scores, softmax statistics and sums are fp32.  The products are the matrix cores', of 16-bit
+ * operands.  Codes enter them exactly, but for E2M1 groups more than 2^26 below the largest among the
+ * 32 tokens beside them (keys) or 2^25 below the largest of the sequence (values), which lose bits.
+ * Weights enter with 22 bits (bf16 caches 16) where g <= 8.  With more heads a cache head they are
+ * rounded once: 11 bits (bf16 caches 8), to 2^-32 of the sequence's largest weight at the least (2^-30
+ * in the formats with a scale a token, where it is the weight times the token's value scale that is
+ * rounded).  Results do not depend on the run: the same inputs give the same bits.
+ * An infinite value that is seen with a weight above 0, however small, makes its element infinite (in
+ * a 16-bit cache; the other formats hold none).
+ * The cache is read once for every 16 query heads of a cache head, split over its length across the
+ * device and joined; the partial sums
  * live in `workspace` (device memory, 16-byte aligned, of at least the size that
  * fq_attn_decode_get_workspace_size gives for the same q, cache and table; contents need not be
  * initialised; calls that overlap in time must not share it). */
@@ -321,8 +329,10 @@ fq_status fq_attn_decode(const fq_tensor* q, const fq_tensor* k_cache, const fq_
  * of a sequence sees its keys 0 .. (Lk - Lq) + i: the queries are the sequence's last rows, so
  * a prompt's chunk attends to the part before it (read back with fq_kv_read) and to itself.
  * With causal == 0 it sees all Lk.  A row that sees no key gives zeros and lse = -infinity.
- * Infinities and NaN in keys and values reach only the rows that see them.  The row strides of
- * k and v are at most 2^23 elements.
+ * Infinities and NaN in keys and values reach only the rows that see them, an infinite value with a
+ * weight above 0 as an infinity.  Scores, statistics and sums are fp32; the weights are rounded to q's
+ * dtype for the second product (11 bits and 2^-32 of the row's largest at the least, in bf16 8 bits).
+ * The row strides of k and v are at most 2^23 elements.
  * `lse` (optional) FLOAT32 [Tq, Hq].  g = Hq / Hkv and scale as above; 1 <= B <= 65536 and
  * (floor(Tq / 128) + B) * Hq < 2^24.  Rows of out past cu_q[B] are not written.  A call with few rows over many keys splits the keys and joins
  * the parts in `workspace` (as for fq_attn_decode, of the size that
