@@ -270,7 +270,9 @@ def empty_outputs(K: int, M: int, N: int, mode: str, device="cuda"):
 
 
 class Executor:
-    """A planned call (first stage).  Repeatable: run() may be called many times."""
+    """A planned call (first stage).  Repeatable: run() may be called many times.  Its workspace comes from
+    the memory of the stream that is current when it is planned: a first run on another stream has to
+    come after that stream's work, by the caller's own event or wait (quantize() plans on the stream it runs on)."""
 
     def __init__(self, x, p1, p2, out, quant_scale, mode: str, clip_ratio: float = 1.0,
                  dst_type_max: float = 0.0, kernel: int = KERNEL_AUTO, repeatable: bool = True):
@@ -573,7 +575,7 @@ class KVCache:
                 st = [2 * n for n in st[:3]] + [1 if st[3] == 1 else 2 * st[3]]
             return _Desc(c.data_ptr(), dt, shape, st), None if s is None else _Desc(s.data_ptr(), sdt, s.shape, s.stride())
 
-        at = tuple(None if t is None else t.data_ptr() for t in self._tensors)
+        at = tuple((t.data_ptr, t.data_ptr()) for t in self._tensors if t is not None)
         (self._kc, self._ks), (self._vc, self._vs) = side(k, k_scale), side(v, v_scale)
         self.pages, self.heads, self.page_size = k.shape[:3]
         self.head_dim = k.shape[3] * (2 if mode in ("int4", "fp4") else 1)
@@ -582,10 +584,10 @@ class KVCache:
 
     def _args(self):
         """Addresses of the four descriptors of a call (built anew where a tensor's memory has moved)."""
-        k, v, ks, vs = self._tensors
-        a, b, c, d = self._at
-        if k.data_ptr() != a or v.data_ptr() != b or (ks is not None and (ks.data_ptr() != c or vs.data_ptr() != d)):
-            self._describe()
+        for address, was in self._at:
+            if address() != was:
+                self._describe()
+                break
         return self._ptrs
 
 
@@ -627,7 +629,7 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
     held = cache._args()
     if k_out is None:
         make = lambda: torch.empty((total, cache.heads, cache.head_dim), dtype=dtype, device=cache.device)  # noqa: E731
-        k_out, v_out = _new(stream, make), _new(stream, make)
+        k_out, v_out = (make(), make()) if stream is None else (_new(stream, make), _new(stream, make))
     elif k_out.dtype != dtype or v_out.dtype != dtype or k_out.shape[0] != total or v_out.shape[0] != total:
         raise ValueError("k_out and v_out are [total, Hkv, D] of dtype")
     d = _Descs(block_table, cu_seqlens, k_out, v_out)

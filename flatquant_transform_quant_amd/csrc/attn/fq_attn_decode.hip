@@ -921,9 +921,9 @@ __global__ __launch_bounds__(kThreads) void decode_join_kernel(DecodeArgs a, con
 // Whether a segment is one workgroup's whatever its length, with no plan and no join: a table that
 // reaches 4 units at most, or 8 with a segment for each CU.  us a call split and joined, and so (8 of either are
 // the host's): one sequence of 250 tokens, 32 heads on 8 of 128, bf16 (8 segments) 12.2 and 9.5, of 510 12.9
-// and 10.0, of 880 12.5 and 13.2; 32 of 62 to 500 (256 segments) 15.7 and 10.3, of 125 to 1000 19.1 and 17.3, of
-// 250 to 2000 30.0 and 28.5; 64 of 1000, int8, 28.6 and 26.3, of 2000 50.3 and 47.7; 37 of up to 1000, E4M3, 16
-// heads of 64 16.0 and 15.3, of up to 2000 20.3 and 26.6.
+// and 10.0, of 880 12.5 and 13.2; 32 of 65 to 500 (256 segments) 15.7 and 10.3, of 131 to 1000 19.1 and 17.3, of
+// 261 to 2000 30.0 and 28.5; 64 of 1000, int8, 28.6 and 26.3, of 2000 50.3 and 47.7; 37 of 22 to 1000, E4M3, 16
+// heads of 64 16.0 and 15.3, of 43 to 2000 20.3 and 26.6.
 bool single_of(int64_t segments, int64_t reach) { return reach <= (segments >= 256 ? 8 : 4) * kUnit; }
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -943,8 +943,8 @@ hipError_t go(const DecodeArgs& a, float* part, hipStream_t s) {
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // Enough workgroups of the join to fill the device, at most one a head.  us with one a segment, and so: 2
-  // sequences of 87381 and 131072 tokens, int8, 64 heads on 8: 120 and 93; 16 of 1000 to 8192, 32 heads on 1: 65
-  // and 24; 8 of 190 to 1500, 32 on 8: 18 and 14.
+  // sequences of 87381 and 131072 tokens, int8, 64 heads on 8: 120 and 93; 16 of 1150 to 8192, 32 heads on 1: 65
+  // and 24; 8 of 254 to 1500, 32 on 8: 18 and 14.
   const uint32_t ny = static_cast<uint32_t>(std::min<int64_t>(gh, ceil_div(512, segments)));
   // And where that leaves few, slices of 16 elements at least: one sequence of 131072 tokens, int4, 8 heads on
   // 1, 75 us whole and 25 so, of 60883, 16 heads of 64 on 2, 31 and 18, of 8192, 32 on 8, 18.7 and 15.5; the two
