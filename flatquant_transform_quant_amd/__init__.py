@@ -644,6 +644,8 @@ def _workspace(fn, name, device, stream, given, *args):
     if st != FQ_SUCCESS:
         raise FqError(st, name)
     if given is not None:
+        if not given.is_contiguous():
+            raise ValueError("a workspace is contiguous memory")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if size.value == 0:
         return None, None, 0

@@ -176,3 +176,23 @@ def test_memory_of_a_call_comes_from_the_stream_it_runs_on(streams, launches):
         out, sc = fq.empty_outputs(4, 256, 256, "int4", device="cpu")
         on(at, 1, None, lambda: fq.quantize(x, p, p, out, sc, "int4", 0.95, stream=s))
     assert launches.count("fq_attn_decode") == 3
+
+
+def test_a_workspace_is_contiguous(streams, launches):
+    """One whose elements lie over each other has less memory than it has elements, one with gaps more."""
+    b16, i32 = (lambda *s, t=t: torch.zeros(s, dtype=t) for t in (torch.bfloat16, torch.int32))
+    cache = fq.empty_kv_cache(4, 2, 16, 64, "int8", "cpu")
+    q, table, lens = b16(1, 4, 64), i32(1, 64), i32(1)
+    size = fq.attn_decode_workspace_size(q, cache, table)
+    assert size > 0
+    cu, ck = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([0, 8192], dtype=torch.int32)
+    k = b16(8192, 2, 64)
+    more = fq.attn_prefill_workspace_size(b16(3, 4, 64), k, cu)
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(max(size, more)), torch.zeros(2 * max(size, more), dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.attn_decode(q, cache, table, lens, workspace=bad)
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.attn_prefill(b16(3, 4, 64), k, k, cu, ck, workspace=bad)
+    assert not launches
+    fq.attn_decode(q, cache, table, lens, workspace=torch.zeros(size, dtype=torch.uint8))
+    assert launches == ["fq_attn_decode"]
