@@ -35,7 +35,7 @@
 // sets: without any one of them the rate is 1.25 to 1.27, without all but the products 1.67.  Smaller
 // calls run at 2.0 GHz and 47%: nine packed prompts of 242 to 4096 rows, 32 heads, 306 to 314 us (910 to 930 TFLOP/s),
 // where a workgroup spends 3.4 us before its first and after its last tile each (places, query rows,
-// rows out) and 1.76 us a tile; four chunks of 313 to 1024 rows behind 2507 to 8192 keys, 212 to 222 us (830 to 870),
+// rows out) and 1.76 us a tile; four chunks of 313 to 1024 rows behind 2507 to 8192 keys, 212 to 230 us (800 to 870),
 // where the device's 512 places are 81% busy, the longest walk being 133 tiles and the mean 97.
 // Tile and schedule, TFLOP/s on those three (prompt, packed, chunks) and 2 x 8192 rows of 64:
 //   128 rows, 4 waves (this)                                          1128  867  669*  826
