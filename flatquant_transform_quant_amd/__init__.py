@@ -108,7 +108,9 @@ def _load():
     L.fq_attn_decode.argtypes = [vp] * 7 + [dbl, vp, vp, vp, u64, vp]
     L.fq_attn_prefill_get_workspace_size.argtypes = [vp, vp, vp, ctypes.c_int32, ctypes.POINTER(u64)]
     L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
-    for f in (L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
+    L.fq_qk_rope.argtypes = [vp] * 4 + [dbl, vp, vp, vp, ctypes.c_int32, vp, vp, vp]
+    L.fq_kv_append.argtypes = [vp] * 6 + [dbl, vp, vp, vp, ctypes.c_int32, dbl, dbl] + [vp] * 6
+    for f in (L.fq_qk_rope, L.fq_kv_append, L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
               L.fq_attn_prefill_get_workspace_size, L.fq_attn_prefill):
         f.restype = ctypes.c_int32
     return L
@@ -119,7 +121,7 @@ EXPORTS = ("fq_get_workspace_size", "fq_run", "fq_executor_destroy", "fq_executo
            "fq_executor_set_kernel", "fq_executor_kernel", "fq_status_string", "fq_last_error", "fq_dequant",
            "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc", "fq_kv_write", "fq_kv_read",
            "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill_get_workspace_size",
-           "fq_attn_prefill")
+           "fq_attn_prefill", "fq_qk_rope", "fq_kv_append")
 NO_ALLOC_SCRATCH_BYTES = 64 << 20  # FQ_NO_ALLOC_SCRATCH_BYTES of include/fq.h
 
 
@@ -635,6 +637,52 @@ def kv_read(cache: KVCache, block_table, cu_seqlens, total: int, dtype, k_out=No
     d = _Descs(block_table, cu_seqlens, k_out, v_out)
     _call(lib.fq_kv_read, "fq_kv_read", cache.device, *held, *d.ptrs, _stream(stream, cache.device))
     return k_out, v_out
+
+
+def qk_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, axes=None,
+            q_out=None, k_out=None, stream=None):
+    """Queries q [T, Hq, D] and keys k [T, Hkv, D] (one 16-bit dtype; either may be None), each row divided by its root
+    mean square where its side has a weight [D] (float32 or 16-bit), then the pairs of its first 2 * len(inv_freq) elements
+    turned by positions * inv_freq: pairs (i, i + R/2), or (2i, 2i + 1) interleaved.  positions int32 [T]; with ``axes``
+    (int32 [R/2]: the axis of each pair) int32 [A, T].  inv_freq float32 [R/2].  Returns (q_out, k_out); an output may be
+    its own input."""
+    torch = _torch()
+    if q is None and k is None:
+        raise ValueError("neither queries nor keys")
+    first = q if q is not None else k
+    _same_gpu(stream, first, k, positions, inv_freq, q_weight, k_weight, axes, q_out, k_out)
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+
+    def result(x, out):
+        if x is None or out is not None:
+            return out
+        make = lambda: torch.empty_like(x, memory_format=torch.contiguous_format)  # noqa: E731
+        return make() if stream is None else _new(stream, make)
+
+    q_out, k_out = result(q, q_out), result(k, k_out)
+    d = _Descs(q, k, q_weight, k_weight, positions, inv_freq, axes, q_out, k_out)
+    p = d.ptrs
+    _call(lib.fq_qk_rope, "fq_qk_rope", first.device, *p[:4], eps, *p[4:7], 1 if interleaved else 0, *p[7:], _stream(stream, first.device))
+    return q_out, k_out
+
+
+def kv_append(cache: KVCache, q, k, v, slots, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+              interleaved: bool = False, axes=None, clip_ratio: float = 1.0, dst_type_max: float = 0.0, q_out=None, stream=None):
+    """qk_rope on q (may be None) and k, and kv_write of the turned keys and of v at slots [T], in one launch; the keys are
+    quantized from unrounded rows.  Returns q_out."""
+    torch = _torch()
+    _same_gpu(stream, cache.k, q, k, v, slots, positions, inv_freq, q_weight, k_weight, axes, q_out)
+    if q is None and q_out is not None:
+        raise ValueError("an output without its input")
+    if q is not None and q_out is None:
+        make = lambda: torch.empty_like(q, memory_format=torch.contiguous_format)  # noqa: E731
+        q_out = make() if stream is None else _new(stream, make)
+    d = _Descs(q, k, v, slots, q_weight, k_weight, positions, inv_freq, axes, q_out)
+    p = d.ptrs
+    _call(lib.fq_kv_append, "fq_kv_append", cache.device, *p[:6], eps, *p[6:9], 1 if interleaved else 0, clip_ratio, dst_type_max,
+          *cache._args(), p[9], _stream(stream, cache.device))
+    return q_out
 
 
 def _workspace(fn, name, device, stream, given, *args):

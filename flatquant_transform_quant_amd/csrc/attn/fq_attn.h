@@ -51,6 +51,24 @@ hipError_t launch_kv_write(const KvCache& c, int64_t T, const Rows16& k, const R
 hipError_t launch_kv_read(const KvCache& c, int64_t T, int32_t B, const BlockTable& bt, const int32_t* cu, const Rows16& k,
                           const Rows16& v, hipStream_t s);
 
+// The norm of a head's rows: weights [D] of `dtype` (kF16, kBF16 or kNormF32), null: none
+constexpr int32_t kNormF32 = 3;
+struct RopeNorm {
+  const void* w;
+  int32_t dtype;
+};
+struct RopeArgs {
+  Rows16 q, k, v, q_out, k_out;  // (v: append alone; k_out: not append)
+  RopeNorm qn, kn;
+  const int32_t *pos, *axis, *slots;  // positions [axes, T], pos_axis apart; axis [R / 2] or null
+  int64_t pos_axis, T;
+  const float* inv_freq;  // [R / 2]
+  KvCache c;
+  int32_t dtype, Hq, Hkv, D, R, axes, interleaved, append;
+  float eps, d, dmax;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
 struct DecodeArgs {
   KvCache c;
   BlockTable bt;

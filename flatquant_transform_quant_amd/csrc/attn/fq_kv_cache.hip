@@ -13,28 +13,13 @@
 // device, less than the two calls take on the host (8 us each).
 #include <hip/hip_runtime.h>
 
-#include "fq_attn_dev.h"
+#include "fq_kv_store.h"
 
 namespace fq {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kEnough = 512;   // workgroups of a launch that need no more spreading
-
-// Max over aligned groups of SPAN lanes, as integers: |x| as fp32 bits orders finite values,
-// then infinity, then NaN, so a row that holds either shows it in its maximum.
-template <int SPAN>
-__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
-  v = max(v, dpp_u<kDppQuadXor1>(v));
-  v = max(v, dpp_u<kDppQuadXor2>(v));
-  if constexpr (SPAN >= 8) v = max(v, dpp_u<kDppRowHalfMirror>(v));
-  if constexpr (SPAN >= 16) v = max(v, dpp_u<kDppRowMirror>(v));
-  if constexpr (SPAN >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(r[0], r[1]);
-  }
-  return v;
-}
 
 // Both kernels: a lane group of LPR lanes owns one token of the workgroup's `tokens` and walks the
 // heads, kInFlight heads' keys and values at a time (all loaded before the first is used); with
@@ -45,84 +30,9 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
 // writing 2048 tokens each in int8 34.2, 33.8, 34.1; writing 512 tokens each of 6 in int4 5.7, 5.8, 9.3.
 constexpr int kInFlight = 2;
 
-// How `tokens` is chosen: one a lane group where that gives enough workgroups; fewer spread a small
-// call over more of them, down to a lane group per head.  us without and with: one token, 8 heads of 128,
+// Small calls are spread over more workgroups (tokens_of).  us without and with: one token, 8 heads of 128,
 // int8, written 9.2 and 3.2, 33 read 4.3 and 3.2; 128 written in int4 8.0 and 3.3; 6 x 512 8.7 and 5.8 (spread
 // over 2048 workgroups: 9.1).
-int tokens_of(int64_t T, int Hkv, int lpr) {
-  int tokens = kThreads / lpr;
-  while (tokens > 1 && tokens / 2 * Hkv >= kThreads / lpr && ceil_div(T, tokens) < kEnough) tokens >>= 1;
-  return tokens;
-}
-
-// One 8-element piece of a row quantized and stored: codes and scale rows at `codes`, `scale`.
-template <int MODE, int DT, int LPR, int SV>
-__device__ __forceinline__ void kv_store8(const u32x4_t raw, uint8_t* codes, uint8_t* scale, int ch, int D, float d, float dmax, bool store) {
-  if constexpr (MODE == kKv16) {
-    if (store) *reinterpret_cast<u32x4_t*>(codes + 16 * ch) = raw;
-  } else {
-    float x[8];
-    kv_decode8<kKv16, DT>(raw, 1.0f, 0, x);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = group_umax<MODE == kKvFp4 ? 4 : LPR>(top);
-    const bool finite = top < 0x7F800000u;
-    if constexpr (MODE == kKvFp4) {
-      uint32_t e8 = e8m0_code_v<SV>(__uint_as_float(top), dmax, 0.0f);
-      const float s = e8m0_to_float(e8);
-      uint32_t w = fp4x2<0>(0u, x[0], x[1], s);
-      w = fp4x2<1>(w, x[2], x[3], s);
-      w = fp4x2<2>(w, x[4], x[5], s);
-      w = fp4x2<3>(w, x[6], x[7], s);
-      if (!finite) {
-        w = 0u;
-        e8 = 255u;
-      }
-      if (store) {
-        *reinterpret_cast<uint32_t*>(codes + 4 * ch) = w;
-        if (ch % 4 == 0) {
-          const int n = D / 32;
-          scale[ch / 4] = static_cast<uint8_t>(e8);
-          if ((n & 1) && ch / 4 == n - 1) scale[n] = 0;  // the pad byte of an odd group count
-        }
-      }
-    } else {
-      const float sc = __uint_as_float(top) / d;
-      // q = x / sc, correctly rounded, from one reciprocal a row: with inv the rounded 1 / sc, q0 = x inv
-      // is within an ulp or so, the fused remainder x - q0 sc is exact, and q0 + remainder * inv
-      // rounds to the quotient (Markstein's correction).  Scales near the ends of the exponent range,
-      // where the remainder could underflow, divide.
-      const bool mid = sc > 0x1p-90f && sc < 0x1p100f;
-      const float inv = mid ? 1.0f / sc : 0.0f;
-      float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q0 = x[i] * inv;
-        q[i] = __builtin_fmaf(__builtin_fmaf(-q0, sc, x[i]), inv, q0);
-        if constexpr (MODE == kKvE4M3) q[i] = __builtin_copysignf(q[i], x[i]);  // (the sum of a +0 and a -0 is +0)
-      }
-      if (!mid) {
-        const bool some = finite && sc > 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = some ? x[i] / sc : 0.0f;
-      }
-      if (store) {
-        if constexpr (MODE == kKvInt4) {
-          uint32_t w = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w |= int4_nibble(q[i]) << (4 * i);
-          *reinterpret_cast<uint32_t*>(codes + 4 * ch) = w;
-        } else {
-          constexpr int CM = MODE == kKvInt8 ? kPerTokenInt8 : kPerTokenE4M3;
-          *reinterpret_cast<u32x2_t*>(codes + 8 * ch) =
-              u32x2_t{code8x4<CM>(q[0], q[1], q[2], q[3]), code8x4<CM>(q[4], q[5], q[6], q[7])};
-        }
-        if (ch == 0) *reinterpret_cast<float*>(scale) = sc;
-      }
-    }
-  }
-}
 
 // MODE, the rows' dtype, lanes per row, e8m0 rule (kE8V1 or kE8V2Div)
 template <int MODE, int DT, int LPR, int SV>
@@ -239,20 +149,12 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvCache c, int32_t T,
   }
 }
 
-// f(lanes of a row)
-template <typename F>
-void by_lanes(int D, F&& f) {
-  if (D <= 64) f(std::integral_constant<int, 8>{});
-  else if (D <= 128) f(std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 32>{});
-}
-
 template <int MODE, int DT>
 hipError_t write_mode(const KvCache& c, int64_t T, const Rows16& k, const Rows16& v, const int32_t* slots, float d,
                       float dmax, hipStream_t s) {
   auto go = [&](auto lpr, auto sv) {
     constexpr int L = decltype(lpr)::value, SV = decltype(sv)::value;
-    const int tokens = tokens_of(T, c.Hkv, L);
+    const int tokens = tokens_of(T, c.Hkv, L, kThreads, kEnough);
     kv_write_kernel<MODE, DT, L, SV><<<static_cast<uint32_t>(ceil_div(T, tokens)), kThreads, 0, s>>>(
         c, static_cast<int32_t>(T), tokens, k, v, slots, d, dmax);
   };
@@ -270,7 +172,7 @@ hipError_t read_mode(const KvCache& c, int64_t T, int32_t B, const BlockTable& b
                      const Rows16& v, hipStream_t s) {
   by_lanes(c.D, [&](auto lpr) {
     constexpr int L = decltype(lpr)::value;
-    const int tokens = tokens_of(T, c.Hkv, L);
+    const int tokens = tokens_of(T, c.Hkv, L, kThreads, kEnough);
     kv_read_kernel<MODE, DT, L><<<static_cast<uint32_t>(ceil_div(T, tokens)), kThreads, 0, s>>>(c, static_cast<int32_t>(T), B, tokens,
                                                                                               bt, cu, k, v);
   });

@@ -290,6 +290,37 @@ fq_status fq_kv_read(const fq_tensor* k_cache, const fq_tensor* k_scale, const f
                      const fq_tensor* v_scale, const fq_tensor* block_table, const fq_tensor* cu,
                      const fq_tensor* k_out, const fq_tensor* v_out, hipStream_t stream);
 
+/* ---- norms and rotation of queries and keys -------------------------------------------------
+ * What stands between the projection and the attention.  A row (one token's D elements of one head) is
+ * first, where the side has a weight [D], divided by its root mean square,
+ *     y = x / sqrt(mean(x^2) + eps) * w
+ * (eps from 2^-126 to 2^127; a NULL weight: no norm), and then the pairs (a, b) of its first R elements
+ * are turned by the token's position,
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),   t = position * inv_freq[i],
+ * pair i of R / 2 being elements (i, i + R / 2), or (2 i, 2 i + 1) with interleaved != 0.
+ *   inv_freq   FLOAT32 [R / 2]: R a multiple of 8, at most D; empty: no rotation
+ *   positions  INT32 [T] (contiguous); with axes [A, T], 1 <= A <= 16, innermost stride 1
+ *   axes       NULL, or INT32 [R / 2]: the row of positions that turns each pair (time, height and width of
+ *              a video, say); a pair whose axis is not in 0 .. A-1 is not turned
+ *   weights    FLOAT32 | FLOAT16 | BFLOAT16 [D], contiguous
+ * All of it is fp32, the angle's product with the position fp64 before its whole turns are taken off, and rounded
+ * once at the end.  Squares have to sum within fp32's range (|x| up to 1e18).
+ *
+ * fq_qk_rope: q, k (either may be NULL with its output) to q_out, k_out, 16-bit rows as above, of one dtype, each with heads
+ * of its own, 0 to 65536.  An output may be its own input (the same tensor, that is); it must not overlap otherwise.
+ *
+ * fq_kv_append: the same on q (may be NULL with q_out) and k, and k and v written to the cache as by fq_kv_write, in
+ * one launch.  The keys' codes come from the unrounded rows; the values' are fq_kv_write's.  A token whose slot is negative
+ * or beyond the cache still has its q turned. */
+fq_status fq_qk_rope(const fq_tensor* q, const fq_tensor* k, const fq_tensor* q_weight, const fq_tensor* k_weight, double eps,
+                     const fq_tensor* positions, const fq_tensor* inv_freq, const fq_tensor* axes, int32_t interleaved,
+                     const fq_tensor* q_out, const fq_tensor* k_out, hipStream_t stream);
+fq_status fq_kv_append(const fq_tensor* q, const fq_tensor* k, const fq_tensor* v, const fq_tensor* slots,
+                       const fq_tensor* q_weight, const fq_tensor* k_weight, double eps, const fq_tensor* positions,
+                       const fq_tensor* inv_freq, const fq_tensor* axes, int32_t interleaved, double clipRatio,
+                       double dstTypeMax, const fq_tensor* k_cache, const fq_tensor* k_scale, const fq_tensor* v_cache,
+                       const fq_tensor* v_scale, const fq_tensor* q_out, hipStream_t stream);
+
 /* ---- attention of one new token over the cache --------------------------------------------
  *     out[b, h] = sum_t p[t] v[t, h / g],  p = softmax over t < lengths[b] of scale * <q[b, h], k[t, h / g]>
  * with g = Hq / Hkv (a whole number) query heads sharing a cache head.  q, out FLOAT16 |
