@@ -110,7 +110,9 @@ def _load():
     L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
     L.fq_qk_rope.argtypes = [vp] * 4 + [dbl, vp, vp, vp, ctypes.c_int32, vp, vp, vp]
     L.fq_kv_append.argtypes = [vp] * 6 + [dbl, vp, vp, vp, ctypes.c_int32, dbl, dbl] + [vp] * 6
-    for f in (L.fq_qk_rope, L.fq_kv_append, L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
+    L.fq_attn_chunk_get_workspace_size.argtypes = [vp] * 4 + [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(u64)]
+    L.fq_attn_chunk.argtypes = [vp] * 8 + [ctypes.c_int32, ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
+    for f in (L.fq_attn_chunk_get_workspace_size, L.fq_attn_chunk, L.fq_qk_rope, L.fq_kv_append, L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
               L.fq_attn_prefill_get_workspace_size, L.fq_attn_prefill):
         f.restype = ctypes.c_int32
     return L
@@ -121,7 +123,7 @@ EXPORTS = ("fq_get_workspace_size", "fq_run", "fq_executor_destroy", "fq_executo
            "fq_executor_set_kernel", "fq_executor_kernel", "fq_status_string", "fq_last_error", "fq_dequant",
            "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc", "fq_kv_write", "fq_kv_read",
            "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill_get_workspace_size",
-           "fq_attn_prefill", "fq_qk_rope", "fq_kv_append")
+           "fq_attn_prefill", "fq_qk_rope", "fq_kv_append", "fq_attn_chunk_get_workspace_size", "fq_attn_chunk")
 NO_ALLOC_SCRATCH_BYTES = 64 << 20  # FQ_NO_ALLOC_SCRATCH_BYTES of include/fq.h
 
 
@@ -762,4 +764,34 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
                                workspace, qp, kp, ap, causal)
     _call(lib.fq_attn_prefill, "fq_attn_prefill", q.device, qp, kp, vp, ap, bp, causal, scale, op, sp, ptr, size,
           _stream(stream, q.device))
+    return out
+
+
+def attn_chunk_workspace_size(q, cache: KVCache, block_table, cu_q, window: int = 0, sinks: int = 0) -> int:
+    size = ctypes.c_uint64(0)
+    d = _Descs(q, block_table, cu_q)
+    st = lib.fq_attn_chunk_get_workspace_size(d.ptrs[0], cache._args()[0], d.ptrs[1], d.ptrs[2], window, sinks, ctypes.byref(size))
+    if st != FQ_SUCCESS:
+        raise FqError(st, "fq_attn_chunk_get_workspace_size")
+    return size.value
+
+
+def attn_chunk(q, cache: KVCache, block_table, cu_q, lengths, window: int = 0, sinks: int = 0, scale: float = 0.0, out=None,
+               lse=None, workspace=None, stream=None):
+    """Attention of new tokens over the cache, which holds their keys and values already: q [Tq, Hq, D], sequence b in rows
+    cu_q[b] .. cu_q[b+1]-1 (int32 [B+1]), its last row at the last of its lengths[b] tokens (int32 [B]).  A row sees the keys up to its
+    own position; with ``window`` only the last ``window`` of them and the first ``sinks`` tokens.  scale 0 means 1/sqrt(D).
+    ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least attn_chunk_workspace_size) may be passed to reuse one."""
+    torch = _torch()
+    _same_gpu(stream, cache.k, q, block_table, cu_q, lengths, out, lse, workspace)
+    if out is None:
+        make = lambda: torch.empty_like(q, memory_format=torch.contiguous_format)  # noqa: E731
+        out = make() if stream is None else _new(stream, make)
+    d = _Descs(q, block_table, cu_q, lengths, out, lse)
+    qp, bp, ap, lp, op, sp = d.ptrs
+    held = cache._args()
+    ws, ptr, size = _workspace(lib.fq_attn_chunk_get_workspace_size, "fq_attn_chunk_get_workspace_size", cache.device, stream, workspace,
+                               qp, held[0], bp, ap, window, sinks)
+    _call(lib.fq_attn_chunk, "fq_attn_chunk", cache.device, qp, *held, bp, ap, lp, window, sinks, scale, op, sp, ptr, size,
+          _stream(stream, cache.device))
     return out

@@ -91,4 +91,25 @@ struct PrefillArgs {
 uint64_t attn_prefill_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t D);
 hipError_t launch_attn_prefill(const PrefillArgs& a, void* ws, hipStream_t s);
 
+// New tokens over the cache: rows of a tile are `tokens` neighbouring tokens x `tile_heads` query heads of one cache head,
+// whose g heads take head_tiles such tiles; heads = Hkv * head_tiles.  The work is dealt to at most `runs` workgroups, or each
+// row tile of a (sequence, cache head) has one to itself (single).
+struct ChunkArgs {
+  KvCache c;
+  BlockTable bt;
+  const int32_t *cu_q, *lengths;
+  Rows16 q, out;
+  float* lse;  // [Tq, Hq] or null
+  int32_t B, Tq, Hq, g, reach;
+  int32_t tokens, tile_heads, head_tiles, heads;
+  int32_t window, sinks;  // window 0: none
+  int32_t runs, single;
+  float scale;
+};
+hipError_t launch_attn_chunk_16(const ChunkArgs& a, void* ws, hipStream_t s);
+hipError_t launch_attn_chunk_int8(const ChunkArgs& a, void* ws, hipStream_t s);
+hipError_t launch_attn_chunk_e4m3(const ChunkArgs& a, void* ws, hipStream_t s);
+hipError_t launch_attn_chunk_int4(const ChunkArgs& a, void* ws, hipStream_t s);
+hipError_t launch_attn_chunk_fp4(const ChunkArgs& a, void* ws, hipStream_t s);
+
 }  // namespace fq

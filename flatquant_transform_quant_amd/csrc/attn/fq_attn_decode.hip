@@ -139,25 +139,6 @@ __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t r, uint32_t of
 template <int DT>
 __device__ __forceinline__ uint32_t h2(float a, float b) { return round16x2<DT>(a, b); }
 
-// Two halves u 2^-24 (u the biased code, an f16 subnormal) -> (u - bias) 2^-9, exact.
-__device__ __forceinline__ uint32_t unbias_f16(uint32_t a, uint32_t minus) {
-  typedef __attribute__((ext_vector_type(2))) _Float16 h16x2;
-  const h16x2 up = __builtin_bit_cast(h16x2, 0x78007800u);  // 2^15
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h16x2, a), up, __builtin_bit_cast(h16x2, minus)));
-}
-constexpr uint32_t kMinus8 = 0xA400A400u, kMinus128 = 0xB400B400u;  // -8 2^-9, -128 2^-9
-template <int SEL>
-__device__ __forceinline__ uint32_t fp4_to_f16x2(uint32_t w, float s) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, SEL));
-}
-template <bool HI>
-__device__ __forceinline__ uint32_t fp8_to_f16x2(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
-}
-
-// 2^e as fp32 for e in [-126, 127]; 0 below (e never passes 127 here)
-__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
-
 // Operand of 8 key elements from a piece's dwords (e: which 8); s: the E2M1 group's factor.
 template <int MODE, int KW>
 __device__ __forceinline__ u32x4_t key_operand(const uint32_t (&w)[KW], int e, float s) {
