@@ -101,7 +101,7 @@ struct ChunkArgs {
   Rows16 q, out;
   float* lse;  // [Tq, Hq] or null
   int32_t B, Tq, Hq, g, reach;
-  int32_t tokens, tile_heads, head_tiles, heads;
+  int32_t tile_rows, tokens, tile_heads, head_tiles, heads;  // tile_rows: 32, 64 or 128
   int32_t window, sinks;  // window 0: none
   int32_t runs, single;
   float scale;

@@ -36,7 +36,6 @@ namespace fq {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kStart = 2;           // tiles that a segment's beginning and end count as when the work is dealt
 constexpr int kAhead = 4;           // fragments read ahead of their products
@@ -55,6 +54,14 @@ constexpr int kLeastRef = -82, kMostRef = 120;
 // weights enter the second product 2^kUpW times above the row's reference
 template <int MODE, int DT>
 constexpr float kUpW = MODE == kKv16 ? kUp<DT> : 5.0f;
+
+// The lane's number, opaque to the compiler from here on: what is formed from it is not kept from before (a kernel's phases each have
+// many addresses that depend on the lane alone; all of them held through the walk were more registers than there are).
+__device__ __forceinline__ int lane_here() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane & 63;  // (so that its range stays known)
+}
 
 // ---- the plan ------------------------------------------------------------------------------
 
@@ -237,471 +244,813 @@ __device__ __forceinline__ int lanes_max(int v) {
   return v;
 }
 
-// What of a tile's low-bit rows one wave brings: its 16 rows' pieces and scales of both sides.
-template <int MODE, int DP, bool PAD>
-struct Low {
+// Rows of a tile that one wave brings through registers, NR of them (16 a page): their pieces and scales, of both sides.
+template <int MODE, int DP, bool PAD, int NR>
+struct Rows {
   static constexpr int bits = kCodeBits<MODE>;
   static constexpr int CE = PAD ? 8 : (128 / bits < DP / 4 ? 128 / bits : DP / 4);  // elements of a piece
-  static constexpr int LPR = DP / CE;         // lanes of a row
-  static constexpr int N = 16 * LPR / 64;     // pieces of a lane and side
-  static constexpr int W = CE * bits / 32;    // dwords of a piece
+  static constexpr int LPR = DP / CE;        // lanes of a row
+  static constexpr int N = NR * LPR / 64;    // pieces of a lane and side
+  static constexpr int NH = 16 * LPR / 64;   // of one page
+  static constexpr int W = CE * bits / 32;   // dwords of a piece
   uint32_t w[2][N][W];
   uint32_t e8[2][MODE == kKvFp4 ? N : 1];
-  float scale[2];  // of row lane % 16
+  float scale[2][NR / 16];                   // of row lane % 16 of a page
 };
 
-// ---- the walk ----------------------------------------------------------------------------------
+// LDS places of 16-byte pieces: piece c of a key row r sits at c ^ key_swz, of a value row at c ^ value_swz.
+template <int DP>
+__device__ __forceinline__ int key_swz(int r) { return DP == 64 ? (r >> 1) & 7 : r & 15; }
+template <int DP>
+__device__ __forceinline__ int value_swz(int r) { return 4 * (DP == 64 ? (r >> 1) & 1 : r & 3); }
+
+// Loads of page `pg` (below 0: none, zeros come) into the pieces of half `half`: `rows` rows from row `r` of the side on.
+template <int MODE, int DP, bool PAD, int NR>
+__device__ __forceinline__ void load_rows(Rows<MODE, DP, PAD, NR>& x, const KvCache& c, int lane, int half, int pg, int64_t r, int rows, int rowb, int sb, int D) {
+  using R = Rows<MODE, DP, PAD, NR>;
+  const int64_t at = max(pg, 0);
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const KvSide& sd = side ? c.v : c.k;
+    const auto rc = __builtin_amdgcn_make_buffer_rsrc(sd.codes + (at * sd.page_b + r * rowb), static_cast<int16_t>(0), pg < 0 ? 0 : rows * rowb,
+                                                      kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < R::NH; ++i) {
+      const int rr = (64 * i + lane) / R::LPR, p = (64 * i + lane) % R::LPR;
+      load_piece<R::W>(rc, !PAD || R::CE * p < D ? static_cast<uint32_t>(rr * rowb + p * (R::CE * R::bits / 8)) : kOut, x.w[side][half * R::NH + i]);
+    }
+    if constexpr (MODE != kKv16) {
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(sd.scale + (at * sd.scale_page_b + r * sb), static_cast<int16_t>(0), pg < 0 ? 0 : rows * sb,
+                                                        kBufferWord3);
+      if constexpr (MODE == kKvFp4) {
+#pragma unroll
+        for (int i = 0; i < R::NH; ++i) {
+          const int rr = (64 * i + lane) / R::LPR, p = (64 * i + lane) % R::LPR;
+          x.e8[side][half * R::NH + i] =
+              __builtin_amdgcn_raw_buffer_load_b8(rs, !PAD || R::CE * p < D ? static_cast<uint32_t>(rr * sb + R::CE * p / 32) : kOut, 0, 0);
+        }
+      } else {
+        x.scale[side][half] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (lane & 15), 0, 0));
+      }
+    }
+  }
+}
+
+// The rows, widened, to LDS: keys from row `row0` of the tile at kt on, values of that at vt, their factors to ks and vs.
+// Returns the largest value scale (neither infinity nor NaN) of them.  Values that are not finite become f16 NaN, with a factor of 0 or
+// of the row's other groups.
+template <int MODE, int DP, bool PAD, int NR>
+__device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, int lane, uint8_t* kt, uint8_t* vt, float* ks, float* vs, int row0) {
+  using R = Rows<MODE, DP, PAD, NR>;
+  float big = 0.0f;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+#pragma unroll
+    for (int i = 0; i < R::N; ++i) {
+      const int half = i / R::NH, rr = (64 * (i % R::NH) + lane) / R::LPR, p = (64 * i + lane) % R::LPR, r = row0 + 16 * half + rr;
+      float s = 1.0f;
+      bool nan = false;  // the piece's values are NaN
+      if constexpr (MODE == kKvFp4) {
+        const int e = static_cast<int>(x.e8[side][i]);
+        nan = e == 255;
+        const int top = max(kLeastE, lanes_max<R::LPR>(nan ? 0 : e));
+        s = pow2(max(e - top + kUpE, -126));
+        float f = pow2(top - 127 - (side == 0 ? kUpE : 0));
+        if (side == 0) {
+          if (lanes_max<R::LPR>(nan ? 1 : 0)) f = __builtin_nanf("");
+        } else {
+          big = fmaxf(big, f);
+        }
+        if (p == 0) (side == 0 ? ks : vs)[r] = f;
+      } else if (MODE != kKv16 && side == 1) {
+        nan = !(__shfl(__builtin_fabsf(x.scale[1][half]), rr) < kInf);
+      }
+      uint8_t* const to = (side == 0 ? kt : vt) + r * (2 * DP);
+      const int sw = side == 0 ? key_swz<DP>(r) : value_swz<DP>(r);
+      if constexpr (MODE == kKv16) {
+        *reinterpret_cast<u32x4_t*>(to + 16 * (p ^ sw)) = u32x4_t{x.w[side][i][0], x.w[side][i][1], x.w[side][i][2], x.w[side][i][3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < R::CE / 8; ++e) {
+          u32x4_t o = widened<MODE>(x.w[side][i], e, s);
+          if (side == 1 && nan) o = u32x4_t{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
+          *reinterpret_cast<u32x4_t*>(to + 16 * (((R::CE / 8) * p + e) ^ sw)) = o;
+        }
+      }
+    }
+    if constexpr (MODE != kKv16 && MODE != kKvFp4) {
+#pragma unroll
+      for (int h = 0; h < NR / 16; ++h) {
+        const bool fine = side == 0 || __builtin_fabsf(x.scale[1][h]) < kInf;
+        if (lane < 16) (side == 0 ? ks : vs)[row0 + 16 * h + lane] = fine ? x.scale[side][h] : 0.0f;
+        if (side == 1) big = fmaxf(big, fine ? __builtin_fabsf(x.scale[1][h]) : 0.0f);
+      }
+    }
+  }
+  if constexpr (MODE != kKv16) {
+    big = fmaxf(big, dpp_f<kDppQuadXor1>(big));
+    big = fmaxf(big, dpp_f<kDppQuadXor2>(big));
+    big = fmaxf(big, dpp_f<kDppRowHalfMirror>(big));
+    big = fmaxf(big, dpp_f<kDppRowMirror>(big));
+    if constexpr (MODE == kKvFp4) {  // (the others have the same 16 scales in every row of 16 lanes)
+      big = half_max(big);
+      big = fmaxf(big, __shfl_xor(big, 16));
+    }
+  }
+  return big;
+}
+
+// ---- a segment's rows and pages ------------------------------------------------------------------
+
+// 32 query rows of a row tile: what a lane knows of its own (column lane % 32 of the products), and the wave of all.
+struct Place {
+  bool mine;       // not a repeated row
+  int token, head; // of the sequence, of all query heads
+  int lim, lo;     // the last key seen, the first in the window
+  int lim_first, lim_last, lo_first, lo_last;  // of the first and last of the wave's rows
+};
+__device__ __forceinline__ Place place_of_rows(const ChunkArgs& a, const Segment& sg, const Walk& wk, int lane, int row0) {
+  const int hk = sg.head / a.head_tiles, ht = sg.head - hk * a.head_tiles;
+  const int hn = min(a.tile_heads, a.g - ht * a.tile_heads);  // heads of this tile
+  const int row = row0 + (lane & 31);
+  const int tok = wk.row0 + row / a.tile_heads, hr = row % a.tile_heads;
+  Place p;
+  p.mine = tok <= wk.row1 && row < a.tokens * a.tile_heads && hr < hn;
+  p.token = min(tok, wk.row1);
+  p.head = hk * a.g + ht * a.tile_heads + min(hr, hn - 1);
+  const int off = sg.s.off;
+  auto low_of = [&](int l) __attribute__((always_inline)) { return a.window > 0 ? max(0, l - a.window + 1) : 0; };
+  p.lim = off + p.token;
+  p.lo = low_of(p.lim);
+  p.lim_first = off + min(wk.row0 + row0 / a.tile_heads, wk.row1);
+  p.lim_last = off + min(wk.row0 + (row0 + 31) / a.tile_heads, wk.row1);
+  p.lo_first = low_of(p.lim_first);
+  p.lo_last = low_of(p.lim_last);
+  return p;
+}
+
+// The pages of 16 tiles of a walk at a time: lane 4 i + w has that of the w-th 16 keys of the i-th tile.
+struct Pages {
+  int page, from;  // from: the walk's tile of lane 0
+  uint64_t there;  // keys with a page (or past the sequence's end), a bit a lane
+  __device__ __forceinline__ void need(const ChunkArgs& a, const Segment& sg, const Walk& wk, int u) {
+    if (u >= from && u < from + 16) return;
+    const int lane = threadIdx.x & 63, i = u + (lane >> 2);
+    const int t = i < wk.n ? wk.tile(i) * kKeys + 16 * (lane & 3) : a.reach;
+    page = t < sg.s.lk ? kv_page(a.bt, sg.b, t, a.c.page_log, a.c.pages) : -1;
+    there = __ballot(page >= 0 || t >= sg.s.lk);
+    from = u;
+  }
+  __device__ __forceinline__ int of(int u, int sub) const { return __builtin_amdgcn_readlane(page, 4 * (u - from) + sub); }
+  __device__ __forceinline__ uint32_t bits(int u) const { return static_cast<uint32_t>(there >> (4 * (u - from))) & 15u; }
+};
+// rows that a page's 16 keys from key k on have, and the row of a side that they begin at
+__device__ __forceinline__ int rows_at(const Segment& sg, int k) { return __builtin_amdgcn_readfirstlane(max(0, min(16, sg.s.lk - k))); }
+__device__ __forceinline__ int64_t row_at(const ChunkArgs& a, int hk, int k) {
+  return (static_cast<int64_t>(hk) << a.c.page_log) + (k & ((1 << a.c.page_log) - 1));
+}
+
+// ---- the products of 32 keys with 32 query rows ------------------------------------------------------
 
 template <int MODE, int DT, int DP, bool PAD>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_kernel(ChunkArgs a, float* __restrict__ ws) {
-  constexpr bool kLow = MODE != kKv16;
-  constexpr int ODT = kLow ? kF16 : DT;  // the operands' type
-  constexpr bool kOdd = MODE == kKv16 || MODE == kKvFp4;  // values may be infinite or NaN one by one
-  constexpr float kW = kUpW<MODE, DT>;
-  constexpr int KS = DP / 16;            // products of a score block
-  constexpr int DB = DP / 32;            // 32-row blocks of O^T
-  constexpr int kRowB = DP * 2;          // bytes of a tile row
+struct Block {
+  static constexpr bool kLow = MODE != kKv16;
+  static constexpr int ODT = kLow ? kF16 : DT;  // the operands' type
+  static constexpr int KS = DP / 16;            // products of a score block
+  static constexpr int DB = DP / 32;            // 32-row blocks of O^T
+  static constexpr int kRowB = DP * 2;          // bytes of a tile row
+  static constexpr float kW = kUpW<MODE, DT>;
+
+  u32x4_t qf[KS];  // the query rows as B operands
+  float c;         // base-2 scores' factor
+  f32x16_t acc[DB];
+  float m, l;
+  int ref;  // R
+
+  __device__ __forceinline__ void load_q(const ChunkArgs& a, const Segment& sg, const Place& p, int lane) {
+    const int hf = lane >> 5, D = PAD ? a.c.D : DP;
+    c = __builtin_fabsf(a.scale) * 1.44269504f;
+    const uint16_t* const qp = a.q.p + (sg.s.q0 + p.token) * a.q.row + p.head * a.q.head;
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // (a negative scale goes into the rows' sign)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int d = 16 * ks + 8 * hf;
+      qf[ks] = u32x4_t{0u, 0u, 0u, 0u};
+      if (!PAD || d < D) qf[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
+      qf[ks] ^= u32x4_t{sign, sign, sign, sign};
+    }
+    if constexpr (kLow && DT == kBF16) {
+      uint32_t top = 0;  // the largest exponent, in place
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(qf[ks][i] & 0x7F800000u, (qf[ks][i] << 16) & 0x7F800000u));
+      const int e = min(static_cast<int>(__float_as_uint(half_max(__uint_as_float(top))) >> 23), 254) - 127;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qf[ks][i] = round16x2<kF16>(__builtin_amdgcn_ldexpf(__uint_as_float(qf[ks][i] << 16), 14 - e),
+                                      __builtin_amdgcn_ldexpf(__uint_as_float(qf[ks][i] & 0xFFFF0000u), 14 - e));
+      c = __builtin_amdgcn_ldexpf(c, e - 14);
+    }
+    c = fminf(fmaxf(c * kUnitK<MODE>, 0x1p-126f), 0x1.fffffep127f);  // (a hidden score is -infinity times it)
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    m = -kInf;
+    l = 0.0f;
+    ref = kLow ? kLeastRef : 0;
+  }
+
+  // Whether some of the wave's rows see a key of k0 .. k0 + n - 1.
+  static __device__ __forceinline__ bool sees(const Place& p, int sinks, int k0, int n) {
+    return k0 <= p.lim_last && (k0 + n > p.lo_first || k0 < sinks);
+  }
+
+  // Keys k0 .. k0 + 32 NB - 1, their rows at kt and vt in LDS (from a multiple of 32 on), their factors at ks and vs.  in: which 16
+  // of them have a page; big: the largest value scale; least: what a rescaling factor is at least.  `scored` is called when
+  // the scores have been formed, before a value is read.
+  template <int NB, typename F>
+  __device__ __forceinline__ void step(const Place& p, int lane, int sinks, int k0, uint32_t in, float big, float least, const lds_u8* kt, const lds_u8* vt,
+                                       const float* ks_, const float* vs_, F&& scored) {
+    const int col = lane & 31, hf = lane >> 5;
+    const uint32_t krd = col * kRowB, kx = hf ^ key_swz<DP>(col);
+    const int rj = (lane & 15) >> 2;
+    const uint32_t vrd = (4 * hf + rj) * kRowB + 32 * ((lane >> 4) & 1) + 8 * (lane & 3), vx = DP == 64 ? rj >> 1 : rj;
+    auto key = [&](int ks, int b) __attribute__((always_inline)) {
+      return *(const __attribute__((address_space(3))) u32x4_t*)(kt + krd + 16 * (kx ^ (2 * ks)) + b * 32 * kRowB);
+    };
+    auto value = [&](int d, int g) __attribute__((always_inline)) {
+      const lds_u8* const q = vt + vrd + 64 * (d ^ vx) + 16 * g * kRowB;
+      const u32x2_t lo2 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)q));
+      const u32x2_t hi2 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(q + 8 * kRowB)));
+      return u32x4_t{lo2[0], lo2[1], hi2[0], hi2[1]};
+    };
+    // the factors of the keys of registers 4 j .. 4 j + 3 of the scores
+    auto factors = [&](const float* f, int j) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4_t*>(f + 8 * j + 4 * hf); };
+
+    f32x16_t s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+    {
+      u32x4_t kf[NB * KS];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) kf[i] = key(i / NB, i % NB);
+      static_for<0, NB * KS>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i + kAhead < NB * KS) kf[i + kAhead] = key((i + kAhead) / NB, (i + kAhead) % NB);
+        __builtin_amdgcn_sched_barrier(0);
+        s[i % NB] = mfma32x32x16<ODT>(kf[i], qf[i / NB], s[i % NB]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+    if constexpr (kLow) {
+#pragma unroll
+      for (int j = 0; j < 4 * NB; ++j) {
+        const f32x4_t f = factors(ks_, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[j / 4][4 * (j % 4) + i] *= f[i];
+      }
+    }
+    scored();
+    u32x4_t vf[2 * NB * DB];
+#pragma unroll
+    for (int i = 0; i < kAhead && i < 2 * NB * DB; ++i) vf[i] = value(i % DB, i / DB);
+    __builtin_amdgcn_sched_barrier(0);
+    const bool masked = k0 + 32 * NB - 1 > p.lim_first || (k0 < p.lo_last && k0 + 32 * NB > sinks) || in != (1u << (2 * NB)) - 1u;
+    if (masked) {
+      // this lane's places (4 hf less than the key among these): seen up to `left`, and from `from` on or below `sk`
+      const int left = p.lim - k0 - 4 * hf, from = p.lo - k0 - 4 * hf, sk = sinks - k0 - 4 * hf;
+#pragma unroll
+      for (int i = 0; i < 16 * NB; ++i) {
+        const int place = 8 * (i / 4) + i % 4;
+        const bool seen = place <= left && (place >= from || place < sk) && ((in >> (i / 8)) & 1u);
+        if (!seen) s[i / 16][i % 16] = -kInf;
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16 * NB; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    int ev = kLeastRef;  // exponent of the largest value scale that is seen
+    if constexpr (kLow) {
+      if (masked) {
+        big = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4 * NB; ++j) {
+          const f32x4_t f = factors(vs_, j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) big = fmaxf(big, s[j / 4][4 * (j % 4) + i] == -kInf ? 0.0f : __builtin_fabsf(f[i]));
+        }
+      }
+      ev = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+    }
+    if (__any(top * c > m + kLazy || (kLow && ev > ref + 1))) {
+      const float mn = fmaxf(m, half_max(top) * c);
+      int rn = ref;
+      if constexpr (kLow) {
+        const auto r = __builtin_amdgcn_permlane32_swap(ev, ev, false, false);
+        rn = max(ref, min(kMostRef, max(static_cast<int>(r[0]), static_cast<int>(r[1]))));
+      }
+      const float f = mn == -kInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((m + static_cast<float>(ref)) - (mn + static_cast<float>(rn))), least);
+      m = mn;
+      ref = rn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] *= f;
+    }
+    const float ms = m == -kInf ? 0.0f : m + static_cast<float>(ref) - kW;
+    u32x4_t pf[2 * NB];
+#pragma unroll
+    for (int g = 0; g < 2 * NB; ++g) {
+      f32x4_t vs[2];
+      if constexpr (kLow) {
+        vs[0] = factors(vs_, 2 * g);
+        vs[1] = factors(vs_, 2 * g + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 8 * (g % 2) + 2 * i;
+        float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][e], c, -ms));
+        float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][e + 1], c, -ms));
+        l += x0 + x1;
+        if constexpr (kLow) {
+          x0 *= vs[i / 2][2 * (i % 2)];
+          x1 *= vs[i / 2][2 * (i % 2) + 1];
+        }
+        pf[g][i] = round16x2<ODT>(x0, x1);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<0, 2 * NB * DB>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      if constexpr (i + kAhead < 2 * NB * DB) vf[i + kAhead] = value((i + kAhead) % DB, (i + kAhead) / DB);
+      __builtin_amdgcn_sched_barrier(0);
+      acc[i % DB] = mfma32x32x16<ODT>(vf[i], pf[i / DB], acc[i % DB]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  // The walk again, with values that are infinite or NaN in it: they are added to the rows that see them (a seen infinity
+  // stays one, however small its weight) ...
+  __device__ __forceinline__ void add_odd(const Place& p, int sinks, int k0, uint32_t in, const lds_u8* vt) {
+    const int lane = lane_here(), hf = lane >> 5;
+    for (int j = 0; j < 32; ++j) {
+      bool odd = false;
+      for (int e = 2 * lane; e < DP; e += 128)
+        odd |= not_finite16<ODT>(*(const __attribute__((address_space(3))) uint32_t*)(vt + j * kRowB + 2 * e)) != 0;
+      if (!__any(odd) || !((in >> (j / 16)) & 1u)) continue;
+      const int k = k0 + j;
+      const bool seen = k <= p.lim && (k >= p.lo || k < sinks);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 32 * d + 8 * (i / 4) + 4 * hf + i % 4;
+          const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(vt + j * kRowB + 16 * ((e / 8) ^ value_swz<DP>(j)) + 2 * (e % 8));
+          if (seen && not_finite16<ODT>(v)) acc[d][i] += load16<ODT>(v);
+          if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (registers: few of these reads at a time)
+        }
+    }
+  }
+  // ... and taken out of the products, `rows` rows at vt.
+  static __device__ __forceinline__ void drop_odd(lds_u8* vt, int rows) {
+    for (int i = lane_here(); i < rows * (DP / 2); i += 64) {
+      __attribute__((address_space(3))) uint32_t* const at = (__attribute__((address_space(3))) uint32_t*)(vt + 4 * i);
+      const uint32_t v = *at;
+      *at = v & ~not_finite16_mask<ODT>(v);
+    }
+  }
+  // whether a sum is infinite or NaN
+  __device__ __forceinline__ bool odd() const {
+    float o = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o = __builtin_fmaf(acc[d][i], 0.0f, o);
+    return o != o;
+  }
+};
+
+// A part's sums for the join: [element][row] of TR rows, then m + R and l.
+template <int DP, int TR>
+constexpr int kPart = (DP + 2) * TR;
+
+// The workgroup's run of places.
+struct Run {
+  int i, first, last;  // last <= first: none
+};
+__device__ __forceinline__ Run run_of(const ChunkArgs& a) {
+  // (neighbouring runs, which share keys, on one XCD's L2)
+  const Deal deal(all_places(a), a.single ? ~0u : a.runs);
+  const int per_xcd = (deal.runs + 7) / 8, i = static_cast<int>(blockIdx.x & 7) * per_xcd + static_cast<int>(blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per_xcd || i >= static_cast<int>(deal.runs)) return Run{0, 0, 0};
+  return Run{i, deal.start(i), deal.start(i + 1)};
+}
+// What of a segment's walk is this run's: tiles u0 .. u1 - 1; whole: all of it (an empty walk is its first place's run's).
+struct Share {
+  int u0, u1;
+  bool whole;
+};
+__device__ __forceinline__ Share share_of(const ChunkArgs& a, const Run& r, const Segment& sg, const Walk& wk) {
+  const int base = sg.at + kStart;  // the place of the first tile
+  Share s;
+  s.u0 = a.single ? 0 : min(wk.n, max(0, r.first - base));
+  s.u1 = a.single ? wk.n : max(s.u0, min(wk.n, r.last - base));
+  s.whole = wk.n == 0 ? sg.at >= r.first && sg.at < r.last : s.u0 == 0 && s.u1 == wk.n;
+  return s;
+}
+// The segment behind sg; false: it is not this run's.
+__device__ __forceinline__ bool next_segment(const ChunkArgs& a, const Run& r, Segment& sg) {
+  sg.at += places_before(a, sg.s.off, sg.s.lk, sg.tile + 1) - places_before(a, sg.s.off, sg.s.lk, sg.tile);
+  if (sg.at >= r.last) return false;
+  if (++sg.tile == sg.s.tiles) {
+    sg.tile = 0;
+    if (++sg.head == a.heads) {
+      sg.head = 0;
+      do sg.s = seq_of(a, ++sg.b); while (sg.s.tiles == 0 && sg.b < a.B);
+      sg.s = lane_seq(sg.s, 0);
+    }
+  }
+  return true;
+}
+
+// ---- row tiles of 128 or 64: 32 rows a wave, the tile's keys shared -------------------------------------
+
+// RB blocks of 32 rows: 4, a wave each; or 2, where waves 2 and 3 have the same rows as 0 and 1 and the tile's other 32 keys, and
+// their sums are joined at the segment's end.
+template <int MODE, int DT, int DP, bool PAD, int RB>
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel(ChunkArgs a, float* __restrict__ ws) {
+  using BK = Block<MODE, DT, DP, PAD>;
+  using RW = Rows<MODE, DP, PAD, 16>;
+  constexpr bool kLow = BK::kLow;
+  constexpr int DB = BK::DB, kRowB = BK::kRowB, kTR = 32 * RB;
   constexpr int kTileB = kKeys * kRowB;  // bytes of a tile (keys or values)
   constexpr int kPieces = DP / 8;        // 16-byte pieces of a row
   constexpr int NL = kTileB / 1024 / kWaves;
-  using L = Low<kLow ? MODE : kKvInt8, DP, PAD>;
   __shared__ __align__(16) uint8_t lds[4 * kTileB];  // buffer b: keys at 2 b, values at 2 b + 1
   __shared__ __align__(16) float s_scale[kLow ? 2 : 1][2][kLow ? kKeys : 1];  // [buffer][keys, values]
   __shared__ __align__(16) float s_top[kLow ? 2 : 1][kWaves];                 // largest value scale of 16 keys
-  const lds_u8* const lds_l = (const lds_u8*)lds;
+  __shared__ float s_m[2][RB == 2 ? 64 : 1];                                   // of waves 2 and 3: m + R, l
+  lds_u8* const lds_l = (lds_u8*)lds;
   const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
 
   const KvCache& cc = a.c;
-  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hf = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = PAD ? cc.D : DP;
   const int rowb = static_cast<int>(kv_row_bytes(MODE, D)), sb = static_cast<int>(kv_scale_bytes(MODE, D));
-
-  // ---- this workgroup's run (neighbouring runs, which share keys, on one XCD's L2)
-  const Deal deal(all_places(a), a.single ? ~0u : a.runs);
-  const int per_xcd = (deal.runs + 7) / 8, run = static_cast<int>(blockIdx.x & 7) * per_xcd + static_cast<int>(blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= per_xcd || run >= static_cast<int>(deal.runs)) return;
-  const int first = deal.start(run), last = deal.start(run + 1);
-  Segment sg = segment_at(a, first);
+  const Run run = run_of(a);
+  if (run.last <= run.first) return;
+  Segment sg = segment_at(a, run.first);
 
   // LDS-DMA of 16-bit rows: load i of a wave fills the 16-byte places 64 (NL w + i) + lane of a tile, its 16 rows in all
   uint32_t koff[NL], voff[NL];
   if constexpr (!kLow) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int at = 64 * (NL * wv + i) + lane, r = at / kPieces, p = at % kPieces;
-      const int kp = p ^ (DP == 64 ? (r >> 1) & 7 : r & 15), vp = p ^ (4 * (DP == 64 ? (r >> 1) & 1 : r & 3));
+      const int at = 64 * (NL * wv + i) + (threadIdx.x & 63), r = at / kPieces, p = at % kPieces;
+      const int kp = p ^ key_swz<DP>(r), vp = p ^ value_swz<DP>(r);
       koff[i] = !PAD || 8 * kp < D ? static_cast<uint32_t>((r & 15) * rowb + 16 * kp) : kOut;
       voff[i] = !PAD || 8 * vp < D ? static_cast<uint32_t>((r & 15) * rowb + 16 * vp) : kOut;
     }
   }
-  int step = 0;  // of this workgroup; tile of step s is in buffer s % 2
+  int step = 0;  // of this workgroup; the tile of step s is in buffer s % 2
 
-  for (;;) {
+  do {
     const Walk wk = walk_of(a, sg.s, sg.tile);
-    const int base = sg.at + kStart;  // the place of the segment's first key tile
-    const int u0 = a.single ? 0 : min(wk.n, max(0, first - base)), u1 = a.single ? wk.n : max(u0, min(wk.n, last - base));
-    const bool whole = wk.n == 0 ? sg.at >= first && sg.at < last : u0 == 0 && u1 == wk.n;
-    if (whole || u0 < u1) {
-      const int hk = sg.head / a.head_tiles, ht = sg.head - hk * a.head_tiles;
-      const int hn = min(a.tile_heads, a.g - ht * a.tile_heads);  // heads of this tile
-      const int lk = sg.s.lk, off = sg.s.off;
-      // this lane's row: a token of the sequence and a head (rows past the last token or head repeat it)
-      const int row = 32 * wv + col;
-      const int tok = wk.row0 + row / a.tile_heads, hr = row % a.tile_heads;
-      const bool mine = tok <= wk.row1 && row < a.tokens * a.tile_heads && hr < hn;
-      const int token = min(tok, wk.row1), head = hk * a.g + ht * a.tile_heads + min(hr, hn - 1);
-      auto token_of = [&](int r) __attribute__((always_inline)) { return min(wk.row0 + r / a.tile_heads, wk.row1); };
-      const int first_tok = token_of(32 * wv), last_tok = token_of(32 * wv + 31);
-      // keys that this lane's row sees: from lo up to lim, and below the sinks
-      const int lim = off + token;
-      const int lim_first = off + first_tok, lim_last = off + last_tok;
-      auto low_of = [&](int l) __attribute__((always_inline)) { return a.window > 0 ? max(0, l - a.window + 1) : 0; };
-      const int lo = low_of(lim), lo_first = low_of(lim_first), lo_last = low_of(lim_last);
-
-      // ---- the query rows as B operands (a negative scale goes into their sign); c: base-2 scores' factor
-      float c = __builtin_fabsf(a.scale) * 1.44269504f;
-      u32x4_t qf[KS];
-      {
-        const uint16_t* qp = a.q.p + (sg.s.q0 + token) * a.q.row + head * a.q.head;
-        const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+    const Share sh = share_of(a, run, sg, wk);
+    if (!sh.whole && sh.u0 >= sh.u1) continue;
+    const int hk = sg.head / a.head_tiles, lane = lane_here();
+    const Place pl = place_of_rows(a, sg, wk, lane, 32 * (wv % RB));
+    BK bk;
+    bk.load_q(a, sg, pl, lane);
+    Pages pages{-1, -(1 << 30), 0};
+    auto dma = [&](int u, int buf) __attribute__((always_inline)) {
+      pages.need(a, sg, wk, u);
+      const int64_t pg = pages.of(u, wv);
+      const int k = wk.tile(u) * kKeys + 16 * wv;
+      const uint32_t bytes = pg < 0 ? 0u : static_cast<uint32_t>(rows_at(sg, k) * rowb);
+      const int64_t at = max(pg, int64_t(0)), r = row_at(a, hk, k) * rowb;
+      const i32x4_t rk = rsrc4(cc.k.codes + (at * cc.k.page_b + r), bytes), rv = rsrc4(cc.v.codes + (at * cc.v.page_b + r), bytes);
+      const uint32_t to = lds_addr + buf * (2 * kTileB) + 1024 * NL * wv;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int d = 16 * ks + 8 * hf;
-          qf[ks] = u32x4_t{0u, 0u, 0u, 0u};
-          if (!PAD || d < D) qf[ks] = *reinterpret_cast<const u32x4_t*>(qp + d);
-          qf[ks] ^= u32x4_t{sign, sign, sign, sign};
+      for (int i = 0; i < NL; ++i) dma16(to + 1024 * i, koff[i], rk);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) dma16(to + kTileB + 1024 * i, voff[i], rv);
+    };
+    RW x;
+    auto load = [&](int u) __attribute__((always_inline)) {
+      pages.need(a, sg, wk, u);
+      const int k = wk.tile(u) * kKeys + 16 * wv;
+      load_rows(x, cc, lane, 0, pages.of(u, wv), row_at(a, hk, k), rows_at(sg, k), rowb, sb, D);
+    };
+    auto store = [&](int buf) __attribute__((always_inline)) {
+      const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv);
+      if (lane == 0) s_top[buf][wv] = big;
+    };
+    for (bool careful = false;;) {
+      bk.clear();
+      if (sh.u0 < sh.u1) {
+        if constexpr (kLow) {
+          load(sh.u0);
+          store(step & 1);
+        } else {
+          dma(sh.u0, step & 1);
         }
-        if constexpr (kLow && DT == kBF16) {
-          uint32_t top = 0;  // the largest exponent, in place
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(qf[ks][i] & 0x7F800000u, (qf[ks][i] << 16) & 0x7F800000u));
-          const int e = min(static_cast<int>(__float_as_uint(half_max(__uint_as_float(top))) >> 23), 254) - 127;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              qf[ks][i] = round16x2<kF16>(__builtin_amdgcn_ldexpf(__uint_as_float(qf[ks][i] << 16), 14 - e),
-                                          __builtin_amdgcn_ldexpf(__uint_as_float(qf[ks][i] & 0xFFFF0000u), 14 - e));
-          c = __builtin_amdgcn_ldexpf(c, e - 14);
-        }
-        c = fminf(fmaxf(c * kUnitK<MODE>, 0x1p-126f), 0x1.fffffep127f);  // (a hidden score is -infinity times it)
       }
-
-      // ---- the pages of 16 tiles at a time: lane 4 i + w has that of the w-th 16 keys of the i-th of them
-      int pages = -1, pages_u = -(1 << 30);
-      uint64_t there = 0;
-      auto fetch_pages = [&](int u) __attribute__((always_inline)) {
-        const int i = u + (lane >> 2);
-        const int t = i < wk.n ? wk.tile(i) * kKeys + 16 * (lane & 3) : a.reach;
-        pages = t < lk ? kv_page(a.bt, sg.b, t, cc.page_log, cc.pages) : -1;
-        there = __ballot(pages >= 0 || t >= lk);
-        pages_u = u;
-      };
-      auto rows_of = [&](int u) __attribute__((always_inline)) {
-        return __builtin_amdgcn_readfirstlane(max(0, min(16, lk - (wk.tile(u) * kKeys + 16 * wv))));
-      };
-      auto row_of = [&](int u) __attribute__((always_inline)) {
-        return (static_cast<int64_t>(hk) << cc.page_log) + ((wk.tile(u) * kKeys + 16 * wv) & ((1 << cc.page_log) - 1));
-      };
-      auto dma = [&](int u, int buf) __attribute__((always_inline)) {
-        if (u >= pages_u + 16 || u < pages_u) fetch_pages(u);
-        const int64_t pg = __builtin_amdgcn_readlane(pages, 4 * (u - pages_u) + wv);
-        const uint32_t bytes = pg < 0 ? 0u : static_cast<uint32_t>(rows_of(u) * rowb);
-        const int64_t at = max(pg, int64_t(0)), r = row_of(u) * rowb;
-        const i32x4_t rk = rsrc4(cc.k.codes + (at * cc.k.page_b + r), bytes), rv = rsrc4(cc.v.codes + (at * cc.v.page_b + r), bytes);
-        const uint32_t to = lds_addr + buf * (2 * kTileB) + 1024 * NL * wv;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) dma16(to + 1024 * i, koff[i], rk);
-#pragma unroll
-        for (int i = 0; i < NL; ++i) dma16(to + kTileB + 1024 * i, voff[i], rv);
-      };
-      auto load_low = [&](int u, L& x) __attribute__((always_inline)) {
-        if (u >= pages_u + 16 || u < pages_u) fetch_pages(u);
-        const int pg = __builtin_amdgcn_readlane(pages, 4 * (u - pages_u) + wv), rows = rows_of(u);
-        const int64_t at = max(pg, 0), r = row_of(u);
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const KvSide& sd = side ? cc.v : cc.k;
-          const auto rc = __builtin_amdgcn_make_buffer_rsrc(sd.codes + (at * sd.page_b + r * rowb), static_cast<int16_t>(0),
-                                                            pg < 0 ? 0 : rows * rowb, kBufferWord3);
-          const auto rs = __builtin_amdgcn_make_buffer_rsrc(sd.scale + (at * sd.scale_page_b + r * sb), static_cast<int16_t>(0),
-                                                            pg < 0 ? 0 : rows * sb, kBufferWord3);
-#pragma unroll
-          for (int i = 0; i < L::N; ++i) {
-            const int rr = (64 * i + lane) / L::LPR, p = (64 * i + lane) % L::LPR;
-            const bool in = !PAD || L::CE * p < D;
-            load_piece<L::W>(rc, in ? static_cast<uint32_t>(rr * rowb + p * (L::CE * L::bits / 8)) : kOut, x.w[side][i]);
-            if constexpr (MODE == kKvFp4)
-              x.e8[side][i] = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? static_cast<uint32_t>(rr * sb + L::CE * p / 32) : kOut, 0, 0);
-          }
-          if constexpr (MODE != kKvFp4) x.scale[side] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (lane & 15), 0, 0));
+      for (int u = sh.u0; u < sh.u1; ++u, ++step) {
+        const int buf = step & 1, k0 = wk.tile(u) * kKeys;
+        const uint32_t in = pages.bits(u);  // which 16 keys have a page
+        tile_barrier();
+        if (u + 1 < sh.u1) {
+          if constexpr (kLow)
+            load(u + 1);
+          else
+            dma(u + 1, buf ^ 1);
         }
-      };
-      // the wave's rows, widened, and their factors to buffer `buf`
-      auto store_low = [&](const L& x, int buf) __attribute__((always_inline)) {
-        float big = 0.0f;  // of this lane's value scales
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-#pragma unroll
-          for (int i = 0; i < L::N; ++i) {
-            const int rr = (64 * i + lane) / L::LPR, p = (64 * i + lane) % L::LPR, r = 16 * wv + rr;
-            float s = 1.0f;
-            bool nan = false;
-            if constexpr (MODE == kKvFp4) {
-              const int e = static_cast<int>(x.e8[side][i]);
-              nan = e == 255;
-              const int top = max(kLeastE, lanes_max<L::LPR>(nan ? 0 : e));
-              s = pow2(max(e - top + kUpE, -126));
-              float f = pow2(top - 127 - (side == 0 ? kUpE : 0));
-              if (side == 0) {
-                if (lanes_max<L::LPR>(nan ? 1 : 0)) f = __builtin_nanf("");
-              } else {
-                big = fmaxf(big, f);
-              }
-              if (p == 0) s_scale[buf][side][r] = f;
-            }
-            uint8_t* const to = lds + (buf * 2 + side) * kTileB + r * kRowB;
-            const int sw = side == 0 ? (DP == 64 ? (r >> 1) & 7 : r & 15) : 4 * (DP == 64 ? (r >> 1) & 1 : r & 3);
-#pragma unroll
-            for (int e = 0; e < L::CE / 8; ++e) {
-              u32x4_t o = widened<MODE>(x.w[side][i], e, s);
-              if (MODE == kKvFp4 && side == 1 && nan) o = u32x4_t{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
-              *reinterpret_cast<u32x4_t*>(to + 16 * (((L::CE / 8) * p + e) ^ sw)) = o;
-            }
-          }
-          if constexpr (MODE != kKvFp4) {
-            if (lane < 16) s_scale[buf][side][16 * wv + lane] = x.scale[side];
-            if (side == 1) big = __builtin_fabsf(x.scale[1]) < kInf ? __builtin_fabsf(x.scale[1]) : 0.0f;  // (neither infinity nor NaN)
-          }
+        lds_u8* const kt = lds_l + buf * (2 * kTileB);
+        lds_u8* const vt = kt + kTileB;
+        if (careful) {
+          for (int b = RB == 2 ? wv / 2 : 0; b < (RB == 2 ? wv / 2 + 1 : 2); ++b) bk.add_odd(pl, a.sinks, k0 + 32 * b, (in >> (2 * b)) & 3u, vt + 32 * b * kRowB);
+          __syncthreads();
+          BK::drop_odd(vt + 16 * wv * kRowB, 16);
+          __syncthreads();
         }
-        big = fmaxf(big, dpp_f<kDppQuadXor1>(big));
-        big = fmaxf(big, dpp_f<kDppQuadXor2>(big));
-        big = fmaxf(big, dpp_f<kDppRowHalfMirror>(big));
-        big = fmaxf(big, dpp_f<kDppRowMirror>(big));
-        if constexpr (MODE == kKvFp4) big = fmaxf(half_max(big), __shfl_xor(half_max(big), 16));
-        if (lane == 0) s_top[buf][wv] = big;
-      };
-
-      const uint32_t krd = col * kRowB, kx = hf ^ (DP == 64 ? (col >> 1) & 7 : col & 15);
-      const int rj = (lane & 15) >> 2;
-      const uint32_t vrd = (4 * hf + rj) * kRowB + 32 * ((lane >> 4) & 1) + 8 * (lane & 3), vx = DP == 64 ? rj >> 1 : rj;
-
-      f32x16_t acc[DB];
-      float m, l;
-      int ref;  // R
-      auto walk = [&](auto careful) __attribute__((always_inline)) {
-        constexpr bool CAREFUL = decltype(careful)::value;
+        // 64 keys at a time in 16 bits, 32 where the widening of codes needs registers too
+        constexpr int NB = kLow || RB == 2 ? 1 : 2;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-        m = -kInf;
-        l = 0.0f;
-        ref = kLow ? kLeastRef : 0;
-        L x;
-        if (u0 < u1) {
-          if constexpr (kLow) {
-            load_low(u0, x);
-            store_low(x, step & 1);
-          } else {
-            dma(u0, step & 1);
-          }
+        for (int i = 0; i < (RB == 2 ? 1 : 2 / NB); ++i) {
+          const int b = RB == 2 ? wv / 2 : i;
+          if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) continue;
+          const float big = kLow ? fmaxf(s_top[buf][2 * b], s_top[buf][2 * b + 1]) : 0.0f;
+          bk.template step<NB>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big, careful ? 0x1p-126f : 0.0f,
+                               kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [] {});
         }
-        for (int u = u0; u < u1; ++u, ++step) {
-          const int buf = step & 1, t = wk.tile(u);
-          const uint32_t in = static_cast<uint32_t>(there >> (4 * (u - pages_u))) & 15u;  // which 16 keys have a page
-          tile_barrier();
-          if (u + 1 < u1) {
-            if constexpr (kLow)
-              load_low(u + 1, x);
-            else
-              dma(u + 1, buf ^ 1);
-          }
-          const int k0 = t * kKeys;
-          // (waves none of whose rows sees the tile go on)
-          if (k0 <= lim_last && (k0 + kKeys > lo_first || k0 < a.sinks)) {
-            const lds_u8* const kt = lds_l + buf * (2 * kTileB);
-            const lds_u8* const vt = kt + kTileB;
-            auto key = [&](int ks, int b) __attribute__((always_inline)) {
-              return *(const __attribute__((address_space(3))) u32x4_t*)(kt + krd + 16 * (kx ^ (2 * ks)) + b * 32 * kRowB);
-            };
-            auto value = [&](int d, int g) __attribute__((always_inline)) {
-              const lds_u8* const p = vt + vrd + 64 * (d ^ vx) + 16 * g * kRowB;
-              const u32x2_t lo2 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p));
-              const u32x2_t hi2 = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 8 * kRowB)));
-              return u32x4_t{lo2[0], lo2[1], hi2[0], hi2[1]};
-            };
-            // a row factor of the keys of accumulator registers 4 j .. 4 j + 3 of block b
-            auto factors = [&](int side, int b, int j) __attribute__((always_inline)) {
-              return *reinterpret_cast<const f32x4_t*>(&s_scale[buf][side][32 * b + 8 * j + 4 * hf]);
-            };
-            f32x16_t s[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
-            {
-              u32x4_t kf[2 * KS];
-#pragma unroll
-              for (int i = 0; i < kAhead; ++i) kf[i] = key(i / 2, i % 2);
-              static_for<0, 2 * KS>([&](auto ic) __attribute__((always_inline)) {
-                constexpr int i = decltype(ic)::value;
-                if constexpr (i + kAhead < 2 * KS) kf[i + kAhead] = key((i + kAhead) / 2, (i + kAhead) % 2);
-                __builtin_amdgcn_sched_barrier(0);
-                s[i % 2] = mfma32x32x16<ODT>(kf[i], qf[i / 2], s[i % 2]);
-                __builtin_amdgcn_sched_barrier(0);
-              });
-            }
-            f32x4_t vs[kLow ? 8 : 1];
-            if constexpr (kLow) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const f32x4_t f = factors(0, j / 4, j % 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[j / 4][4 * (j % 4) + i] *= f[i];
-                vs[j] = factors(1, j / 4, j % 4);
-              }
-            }
-            u32x4_t vf[4 * DB];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) vf[i] = value(i % DB, i / DB);
-            __builtin_amdgcn_sched_barrier(0);
-            const bool masked = k0 + kKeys - 1 > lim_first || (k0 < lo_last && k0 + kKeys > a.sinks) || in != 15u;
-            if (masked) {
-              // this lane's places (4 hf less than the key in the tile): seen up to `left`, and from `from` on or below `sk`
-              const int left = lim - k0 - 4 * hf, from = lo - k0 - 4 * hf, sk = a.sinks - k0 - 4 * hf;
-#pragma unroll
-              for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int place = 32 * b + 8 * (i / 4) + i % 4;
-                  const bool seen = place <= left && (place >= from || place < sk) && ((in >> (2 * b + i / 8)) & 1u);
-                  if (!seen) {
-                    s[b][i] = -kInf;
-                    if constexpr (kLow) vs[4 * b + i / 4][i % 4] = 0.0f;
-                  }
-                }
-            }
-            uint64_t seen = 0;  // CAREFUL: keys of the tile with a score above -infinity for this lane's row
-            if constexpr (CAREFUL) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                uint32_t w = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w |= (s[b][i] > -kInf ? 1u : 0u) << (8 * (i / 4) + i % 4);
-                w <<= 4 * hf;
-                w |= __shfl_xor(w, 32);
-                seen |= static_cast<uint64_t>(w) << (32 * b);
-              }
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-            int ev = kLeastRef;  // exponent of the largest value scale that is seen
-            if constexpr (kLow) {
-              float big;
-              if (masked) {
-                big = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) big = fmaxf(big, __builtin_fabsf(vs[j / 4][j % 4]) < kInf ? __builtin_fabsf(vs[j / 4][j % 4]) : 0.0f);
-              } else {
-                const f32x4_t q = *reinterpret_cast<const f32x4_t*>(s_top[buf]);
-                big = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
-              }
-              ev = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-            }
-            if (__any(top * c > m + kLazy || (kLow && ev > ref + 1))) {
-              const float mn = fmaxf(m, half_max(top) * c);
-              int rn = ref;
-              if constexpr (kLow) {
-                const auto r = __builtin_amdgcn_permlane32_swap(ev, ev, false, false);
-                rn = max(ref, min(kMostRef, max(static_cast<int>(r[0]), static_cast<int>(r[1]))));
-              }
-              const float to = mn + static_cast<float>(rn), from = m + static_cast<float>(ref);
-              const float f = mn == -kInf ? 1.0f : CAREFUL ? rescale(from, to) : __builtin_amdgcn_exp2f(from - to);
-              m = mn;
-              ref = rn;
-              l *= f;
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[d][i] *= f;
-            }
-            const float ms = m == -kInf ? 0.0f : m + static_cast<float>(ref) - kW;
-            u32x4_t pf[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int e = 8 * (g % 2) + 2 * i;
-                float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][e], c, -ms));
-                float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][e + 1], c, -ms));
-                l += x0 + x1;
-                if constexpr (kLow) {
-                  x0 *= vs[4 * (g / 2) + e / 4][e % 4];
-                  x1 *= vs[4 * (g / 2) + e / 4][e % 4 + 1];
-                }
-                pf[g][i] = round16x2<ODT>(x0, x1);
-              }
-            __builtin_amdgcn_sched_barrier(0);
-            uint32_t odd = 0;
-            static_for<0, 4 * DB>([&](auto ic) __attribute__((always_inline)) {
-              constexpr int i = decltype(ic)::value;
-              if constexpr (i + kAhead < 4 * DB) vf[i + kAhead] = value((i + kAhead) % DB, (i + kAhead) / DB);
-              if constexpr (CAREFUL) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  odd |= not_finite16<ODT>(vf[i][j]);
-                  vf[i][j] &= ~not_finite16_mask<ODT>(vf[i][j]);
-                }
-              }
-              __builtin_amdgcn_sched_barrier(0);
-              acc[i % DB] = mfma32x32x16<ODT>(vf[i], pf[i / DB], acc[i % DB]);
-              __builtin_amdgcn_sched_barrier(0);
-            });
-            if constexpr (CAREFUL) {
-              const bool any = __any(odd != 0);
-              for (int j = 0; any && j < kKeys; ++j) {
-                if (!((seen >> j) & 1)) continue;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const int e = 32 * d + 8 * (i / 4) + 4 * hf + i % 4;
-                    const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(
-                        vt + j * kRowB + 16 * ((e / 8) ^ (4 * (DP == 64 ? (j >> 1) & 1 : j & 3))) + 2 * (e % 8));
-                    if (not_finite16<ODT>(v)) acc[d][i] += load16<ODT>(v);
-                  }
-              }
-            }
-          }
-          if constexpr (kLow) {
-            if (u + 1 < u1) store_low(x, buf ^ 1);
-          }
+        if constexpr (kLow) {
+          if (u + 1 < sh.u1) store(buf ^ 1);
         }
-      };
-      walk(std::false_type{});
-      if constexpr (kOdd) {
-        float odd = 0.0f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) odd = __builtin_fmaf(acc[d][i], 0.0f, odd);
-        if (__syncthreads_or(odd != odd)) walk(std::true_type{});
       }
-      // (no barrier here: the next segment's first tile takes the buffer that was last read a step before the last one)
+      if (careful || !__syncthreads_or(bk.odd())) break;
+      careful = true;
+    }
+    // (no barrier needed here: the next segment's first tile takes the buffer that was last read a step before the last one)
 
-      l = half_sum(l);
-      if (!whole) {  // the part's sums as they are, [element][row], with m + R and l
-        float* const o = ws + static_cast<int64_t>(2 * run + (u0 == 0 ? 1 : 0)) * ((DP + 2) * kRows) + row;
+    const int end = lane_here(), col = end & 31, hf = end >> 5;
+    float l = half_sum(bk.l), m = bk.m + static_cast<float>(bk.ref);
+    if constexpr (RB == 2) {  // waves 2 and 3 hand their sums over in the other buffer
+      float* const at = reinterpret_cast<float*>(lds + ((step & 1) ^ 1) * (2 * kTileB)) + (wv & 1) * (32 * DP) + col;
+      __syncthreads();
+      if (wv >= 2) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kRows] = acc[d][i];
+          for (int i = 0; i < 16; ++i) at[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32] = bk.acc[d][i];
         if (hf == 0) {
-          o[DP * kRows] = m + static_cast<float>(ref);
-          o[(DP + 1) * kRows] = l;
+          s_m[0][32 * (wv & 1) + col] = m;
+          s_m[1][32 * (wv & 1) + col] = l;
         }
-      } else if (mine) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t to = sg.s.q0 + token;
-        uint16_t* const out = a.out.p + to * a.out.row + head * a.out.head;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 32 * d + 8 * i + 4 * hf;
-            if (PAD && e >= D) continue;
-            float o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = acc[d][4 * i + j] * inv * kUnitV<MODE>;
-            *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(o[0], o[1]), round16x2<DT>(o[2], o[3])};
-          }
-        if (a.lse && hf == 0)
-          a.lse[to * a.Hq + head] = l == 0.0f ? -kInf : (m + static_cast<float>(ref) - kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
       }
+      __syncthreads();
+      if (wv >= 2) continue;
+      const float mo = s_m[0][32 * wv + col], lo = s_m[1][32 * wv + col], mn = fmaxf(m, mo);
+      const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mo == -kInf ? 0.0f : rescale(mo, mn);
+      m = mn;
+      l = lo == 0.0f ? l * f0 : __builtin_fmaf(l, f0, lo * f1);  // (nothing seen, or NaN)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bk.acc[d][i] = __builtin_fmaf(bk.acc[d][i], f0, at[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32] * f1);
+    }
+    if (!sh.whole) {
+      float* const o = ws + static_cast<int64_t>(2 * run.i + (sh.u0 == 0 ? 1 : 0)) * kPart<DP, kTR> + 32 * (wv % RB) + col;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kTR] = bk.acc[d][i];
+      if (hf == 0) {
+        o[DP * kTR] = m;
+        o[(DP + 1) * kTR] = l;
+      }
+    } else if (pl.mine) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t to = sg.s.q0 + pl.token;
+      uint16_t* const out = a.out.p + to * a.out.row + pl.head * a.out.head;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 32 * d + 8 * i + 4 * hf;
+          if (PAD && e >= D) continue;
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = bk.acc[d][4 * i + j] * inv * kUnitV<MODE>;
+          *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(o[0], o[1]), round16x2<DT>(o[2], o[3])};
+        }
+      if (a.lse && hf == 0) a.lse[to * a.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
+    }
+  } while (next_segment(a, run, sg));
+}
+
+// ---- row tiles of 32: every wave has all of them, and keys of its own --------------------------------------
+
+// A wave takes every fourth 32 keys of the walk into an LDS region of its own: no barrier before the segment's end, where the
+// waves' sums are joined.  Low-bit rows go through registers, the next 32 on their way during the products of these; 16-bit ones by
+// LDS-DMA, the next keys as soon as the scores are done with these, the next values behind the second products.
+template <int MODE, int DT, int DP, bool PAD>
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kernel(ChunkArgs a, float* __restrict__ ws) {
+  using BK = Block<MODE, DT, DP, PAD>;
+  constexpr bool kLow = BK::kLow;
+  using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 32>;
+  constexpr int DB = BK::DB, kRowB = BK::kRowB, kTR = 32;
+  constexpr int kSideB = 32 * kRowB;  // bytes of a wave's keys (or values); both: 32 rows of DP sums in fp32
+  constexpr int kPieces = DP / 8;     // 16-byte pieces of a row
+  constexpr int NL = kSideB / 1024;   // LDS-DMA loads of a side
+  __shared__ __align__(16) uint8_t lds[kWaves][2 * kSideB];
+  __shared__ __align__(16) float s_scale[kLow ? kWaves : 1][2][32];
+  __shared__ float s_m[kWaves][32], s_l[kWaves][32];
+
+  const KvCache& cc = a.c;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = PAD ? cc.D : DP;
+  const int rowb = static_cast<int>(kv_row_bytes(MODE, D)), sb = static_cast<int>(kv_scale_bytes(MODE, D));
+  const Run run = run_of(a);
+  if (run.last <= run.first) return;
+  Segment sg = segment_at(a, run.first);
+  lds_u8* const kt = (lds_u8*)lds[wv];
+  lds_u8* const vt = kt + kSideB;
+  const uint32_t k_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt));
+
+  do {
+    const Walk wk = walk_of(a, sg.s, sg.tile);
+    const Share sh = share_of(a, run, sg, wk);
+    if (!sh.whole && sh.u0 >= sh.u1) continue;
+    const int hk = sg.head / a.head_tiles, lane = lane_here();
+    Pages pages{-1, -(1 << 30), 0};
+    // The v-th 32 keys of the walk: which 16 of them have a page, with the pages looked up.
+    auto bits = [&](int v) __attribute__((always_inline)) {
+      pages.need(a, sg, wk, v >> 1);
+      return (pages.bits(v >> 1) >> (2 * (v & 1))) & 3u;
+    };
+    auto key_of = [&](int v) __attribute__((always_inline)) { return wk.tile(v >> 1) * kKeys + 32 * (v & 1); };
+    RW x;
+    auto load = [&](int v) __attribute__((always_inline)) {
+      const int k = key_of(v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        load_rows(x, cc, lane, h, pages.of(v >> 1, 2 * (v & 1) + h), row_at(a, hk, k + 16 * h), rows_at(sg, k + 16 * h), rowb, sb, D);
+    };
+    // load i of a side fills the 16-byte places 64 i + lane; the first half of them is the first page's
+    auto dma = [&](int v, int side) __attribute__((always_inline)) {
+      const int k = key_of(v);
+      const KvSide& sd = side ? cc.v : cc.k;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t pg = pages.of(v >> 1, 2 * (v & 1) + h);
+        const i32x4_t rs = rsrc4(sd.codes + (max(pg, int64_t(0)) * sd.page_b + row_at(a, hk, k + 16 * h) * rowb),
+                                 pg < 0 ? 0u : static_cast<uint32_t>(rows_at(sg, k + 16 * h) * rowb));
+#pragma unroll
+        for (int i = 0; i < NL / 2; ++i) {
+          const int at = 64 * (NL / 2 * h + i) + lane, r = at / kPieces, p = (at % kPieces) ^ (side ? value_swz<DP>(r) : key_swz<DP>(r));
+          dma16(k_addr + side * kSideB + 1024 * (NL / 2 * h + i), !PAD || 8 * p < D ? static_cast<uint32_t>((r & 15) * rowb + 16 * p) : kOut, rs);
+        }
+      }
+    };
+    // everything but the last `NL` loads has landed (more: the other side's are on their way)
+    auto landed = [&](bool more) __attribute__((always_inline)) {
+      if (more)
+        asm volatile("s_waitcnt vmcnt(%0)" : : "i"(NL) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    };
+    auto lds_done = [] __attribute__((always_inline)) { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); };
+    const int v0 = 2 * sh.u0 + wv, v1 = 2 * sh.u1;
+    const Place pl = place_of_rows(a, sg, wk, lane, 0);
+    BK bk;
+    bk.load_q(a, sg, pl, lane);
+    for (bool careful = false;;) {
+      bk.clear();
+      uint32_t in = 0;
+      if (v0 < v1) {
+        in = bits(v0);
+        if constexpr (kLow) {
+          load(v0);
+        } else {
+          dma(v0, 0);
+          dma(v0, 1);
+        }
+      }
+      for (int v = v0; v < v1; v += kWaves) {
+        const int k0 = key_of(v);
+        const uint32_t now = in;
+        const bool more = v + kWaves < v1;
+        float big = 0.0f;
+        if constexpr (kLow) {
+          big = store_rows(x, lane, lds[wv], lds[wv] + kSideB, s_scale[wv][0], s_scale[wv][1], 0);
+          lds_done();  // (other lanes' rows are read below)
+        }
+        if (more) {
+          in = bits(v + kWaves);
+          if constexpr (kLow) load(v + kWaves);
+        }
+        if (careful) {
+          if constexpr (!kLow) landed(false);
+          bk.add_odd(pl, a.sinks, k0, now, vt);
+          lds_done();
+          BK::drop_odd(vt, 32);
+          lds_done();
+        }
+        const float least = careful ? 0x1p-126f : 0.0f;
+        const bool sees = BK::sees(pl, a.sinks, k0, 32);
+        if constexpr (kLow) {
+          if (sees) bk.template step<1>(pl, lane, a.sinks, k0, now, big, least, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
+          lds_done();  // (before the next rows take their places)
+        } else {
+          landed(true);  // (the keys)
+          bk.template step<1>(pl, lane, a.sinks, k0, now, big, least, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
+            lds_done();
+            if (more) dma(v + kWaves, 0);
+            landed(more);  // (the values)
+          });
+          lds_done();
+          if (more) dma(v + kWaves, 1);
+        }
+      }
+      if (careful || !__syncthreads_or(bk.odd())) break;
+      careful = true;
     }
 
-    // ---- the next segment
-    sg.at += places_before(a, sg.s.off, sg.s.lk, sg.tile + 1) - places_before(a, sg.s.off, sg.s.lk, sg.tile);
-    if (sg.at >= last) return;
-    if (++sg.tile == sg.s.tiles) {
-      sg.tile = 0;
-      if (++sg.head == a.heads) {
-        sg.head = 0;
-        do sg.s = seq_of(a, ++sg.b); while (sg.s.tiles == 0 && sg.b < a.B);
-        sg.s = lane_seq(sg.s, 0);
+    // ---- the waves' sums: [element][row] of each wave, then a wave joins a quarter of the elements
+    const int end = lane_here(), col = end & 31, hf = end >> 5;
+    float* const mine = reinterpret_cast<float*>(lds[wv]);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mine[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32 + col] = bk.acc[d][i];
+    const float lw = half_sum(bk.l);
+    if (hf == 0) {
+      s_m[wv][col] = bk.m + static_cast<float>(bk.ref);
+      s_l[wv][col] = lw;
+    }
+    __syncthreads();
+    float m = -kInf, l = 0.0f, f[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w][col]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = s_m[w][col] == -kInf ? 0.0f : rescale(s_m[w][col], m);
+      const float li = s_l[w][col];
+      l = li == 0.0f ? l : __builtin_fmaf(li, f[w], l);  // (nothing seen, or NaN)
+    }
+    // this lane's elements: DP / 8 from e0 on
+    constexpr int NE = DP / 8;
+    const int e0 = (2 * wv + hf) * NE;
+    float o[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      o[j] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float v = reinterpret_cast<const float*>(lds[w])[(e0 + j) * 32 + col];
+        o[j] = f[w] == 0.0f ? o[j] : __builtin_fmaf(v, f[w], o[j]);
       }
     }
-  }
+    __syncthreads();  // (before these places are written again)
+    if (!sh.whole) {
+      float* const to = ws + static_cast<int64_t>(2 * run.i + (sh.u0 == 0 ? 1 : 0)) * kPart<DP, kTR> + col;
+#pragma unroll
+      for (int j = 0; j < NE; ++j) to[(e0 + j) * kTR] = o[j];
+      if (wv == 0 && hf == 0) {
+        to[DP * kTR] = m;
+        to[(DP + 1) * kTR] = l;
+      }
+    } else if (pl.mine) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t to = sg.s.q0 + pl.token;
+      uint16_t* const out = a.out.p + to * a.out.row + pl.head * a.out.head + e0;
+#pragma unroll
+      for (int j = 0; j < NE; j += 8) {
+        if (PAD && e0 + j >= D) break;
+        u32x4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = round16x2<DT>(o[j + 2 * i] * inv * kUnitV<MODE>, o[j + 2 * i + 1] * inv * kUnitV<MODE>);
+        *reinterpret_cast<u32x4_t*>(out + j) = w;
+      }
+      if (a.lse && wv == 0 && hf == 0) a.lse[to * a.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
+    }
+  } while (next_segment(a, run, sg));
 }
 
 // Joins the parts of a segment that several runs share: the workgroups of run i do the one that begins in run i and
-// goes on behind it; a workgroup 32 elements, a thread a row and 16 of them.
-template <int MODE, int DT, int DP>
+// goes on behind it; a thread a row and four elements, a workgroup 1024 / TR elements.
+template <int MODE, int DT, int DP, int TR>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const float* __restrict__ ws) {
   const Deal deal(all_places(a), a.runs);
   const int run = blockIdx.x;
@@ -712,58 +1061,70 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
   const int base = sg.at + kStart;
   if (deal.start(run) > base || end <= base || end - base >= wk.n) return;  // its first tile is not here, or its last one is
   const int hk = sg.head / a.head_tiles, ht = sg.head - hk * a.head_tiles, hn = min(a.tile_heads, a.g - ht * a.tile_heads);
-  const int r = threadIdx.x % kRows, e = 32 * blockIdx.y + 16 * (threadIdx.x / kRows);
+  const int r = threadIdx.x % TR, e = (1024 / TR) * blockIdx.y + 4 * (threadIdx.x / TR);
   const int token = wk.row0 + r / a.tile_heads, hr = r % a.tile_heads, head = hk * a.g + ht * a.tile_heads + hr;
   if (token > wk.row1 || r >= a.tokens * a.tile_heads || hr >= hn || e >= a.c.D) return;
-  float m = -kInf, l = 0.0f, o[16];
+  int parts = 1;  // behind the first
+  while (deal.start(run + parts + 1) - base < wk.n) ++parts;
+  float m = -kInf, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i <= parts; i += 4) {  // (four parts' loads at a time)
+    float mi[4], li[4], x[4][4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) o[j] = 0.0f;
-  for (int i = run;; ++i) {
-    const float* const p = ws + static_cast<int64_t>(2 * i + (i == run ? 1 : 0)) * ((DP + 2) * kRows) + r;
-    const float mi = p[DP * kRows], li = p[(DP + 1) * kRows];
-    float x[16];
+    for (int k = 0; k < 4; ++k) {
+      const int part = min(i + k, parts);
+      const float* const p = ws + static_cast<int64_t>(2 * (run + part) + (part == 0 ? 1 : 0)) * kPart<DP, TR> + r;
+      mi[k] = p[DP * TR];
+      li[k] = p[(DP + 1) * TR];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = p[(e + j) * kRows];
-    const float mn = fmaxf(m, mi);
-    const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mi == -kInf ? 0.0f : rescale(mi, mn);
-    m = mn;
-    l = li == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li * f1);  // (nothing seen, or NaN)
+      for (int j = 0; j < 4; ++j) x[k][j] = p[(e + j) * TR];
+    }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = __builtin_fmaf(o[j], f0, x[j] * f1);
-    if (deal.start(i + 1) - base >= wk.n) break;
+    for (int k = 0; k < 4; ++k) {
+      if (i + k > parts) break;
+      const float mn = fmaxf(m, mi[k]);
+      const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mi[k] == -kInf ? 0.0f : rescale(mi[k], mn);
+      m = mn;
+      l = li[k] == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li[k] * f1);  // (nothing seen, or NaN)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(o[j], f0, x[k][j] * f1);
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t to = sg.s.q0 + token;
-  uint16_t* const out = a.out.p + to * a.out.row + head * a.out.head + e;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (e + 8 * h >= a.c.D) break;
-    u32x4_t w;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = round16x2<DT>(o[8 * h + 2 * j] * inv * kUnitV<MODE>, o[8 * h + 2 * j + 1] * inv * kUnitV<MODE>);
-    *reinterpret_cast<u32x4_t*>(out + 8 * h) = w;
-  }
+  *reinterpret_cast<u32x2_t*>(a.out.p + to * a.out.row + head * a.out.head + e) =
+      u32x2_t{round16x2<DT>(o[0] * inv * kUnitV<MODE>, o[1] * inv * kUnitV<MODE>), round16x2<DT>(o[2] * inv * kUnitV<MODE>, o[3] * inv * kUnitV<MODE>)};
   if (a.lse && e == 0)
     a.lse[to * a.Hq + head] = l == 0.0f ? -kInf : (m - kUpW<MODE, DT> + __builtin_amdgcn_logf(l)) * 0.693147181f;
 }
 
-template <int MODE, int DT, int DP, bool PAD>
+template <int MODE, int DT, int DP, bool PAD, int TR>
 hipError_t chunk_go(const ChunkArgs& a, float* ws, hipStream_t s) {
-  chunk_kernel<MODE, DT, DP, PAD><<<static_cast<uint32_t>(8 * ceil_div(a.runs, 8)), kThreads, 0, s>>>(a, ws);
+  const dim3 grid(static_cast<uint32_t>(8 * ceil_div(a.runs, 8)));
+  if constexpr (TR == 32)
+    chunk_narrow_kernel<MODE, DT, DP, PAD><<<grid, kThreads, 0, s>>>(a, ws);
+  else
+    chunk_wide_kernel<MODE, DT, DP, PAD, TR / 32><<<grid, kThreads, 0, s>>>(a, ws);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.runs == 1 || a.single) return err;
-  chunk_join_kernel<MODE, DT, DP><<<dim3(static_cast<uint32_t>(a.runs - 1), static_cast<uint32_t>(ceil_div(a.c.D, 32))), kThreads, 0, s>>>(a, ws);
+  chunk_join_kernel<MODE, DT, DP, TR><<<dim3(static_cast<uint32_t>(a.runs - 1), static_cast<uint32_t>(ceil_div(a.c.D, 1024 / TR))), kThreads, 0, s>>>(a, ws);
   return hipGetLastError();
+}
+
+template <int MODE, int DT, int DP, bool PAD>
+hipError_t chunk_by_rows(const ChunkArgs& a, float* ws, hipStream_t s) {
+  return a.tile_rows == 128  ? chunk_go<MODE, DT, DP, PAD, 128>(a, ws, s)
+         : a.tile_rows == 64 ? chunk_go<MODE, DT, DP, PAD, 64>(a, ws, s)
+                             : chunk_go<MODE, DT, DP, PAD, 32>(a, ws, s);
 }
 
 template <int MODE, int DT>
 hipError_t chunk_by_size(const ChunkArgs& a, float* ws, hipStream_t s) {
   const int D = a.c.D;
-  if (D == 64) return chunk_go<MODE, DT, 64, false>(a, ws, s);
-  if (D == 128) return chunk_go<MODE, DT, 128, false>(a, ws, s);
-  if (D == 256) return chunk_go<MODE, DT, 256, false>(a, ws, s);
-  if (D < 64) return chunk_go<MODE, DT, 64, true>(a, ws, s);
-  return D < 128 ? chunk_go<MODE, DT, 128, true>(a, ws, s) : chunk_go<MODE, DT, 256, true>(a, ws, s);
+  if (D == 64) return chunk_by_rows<MODE, DT, 64, false>(a, ws, s);
+  if (D == 128) return chunk_by_rows<MODE, DT, 128, false>(a, ws, s);
+  if (D == 256) return chunk_by_rows<MODE, DT, 256, false>(a, ws, s);
+  if (D < 64) return chunk_by_rows<MODE, DT, 64, true>(a, ws, s);
+  return D < 128 ? chunk_by_rows<MODE, DT, 128, true>(a, ws, s) : chunk_by_rows<MODE, DT, 256, true>(a, ws, s);
 }
 
 template <int MODE>

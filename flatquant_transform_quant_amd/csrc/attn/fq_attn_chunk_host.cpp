@@ -7,7 +7,7 @@ using namespace fq;
 
 namespace {
 
-constexpr int64_t kRows = 128, kKeys = 64;  // of a row tile, of a key tile
+constexpr int64_t kKeys = 64;               // of a key tile
 constexpr int64_t kPlaces = 5;              // key tiles that a segment's places may have above those of its span
 // Workgroups of a launch: two a CU, one of heads above 128 (their LDS and registers).  A run of fewer than kLeast tiles
 // costs more in parts to join than it gains.
@@ -30,9 +30,11 @@ bool chunk_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* 
   a->Tq = static_cast<int32_t>(Tq);
   a->Hq = static_cast<int32_t>(Hq);
   a->g = static_cast<int32_t>(g);
-  a->head_tiles = static_cast<int32_t>(ceil_div(g, kRows));
+  const int64_t rows = ceil_div(Tq, B) * g;  // of a sequence and cache head, the mean
+  a->tile_rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  a->head_tiles = static_cast<int32_t>(ceil_div(g, a->tile_rows));
   a->tile_heads = static_cast<int32_t>(ceil_div(g, a->head_tiles));
-  a->tokens = static_cast<int32_t>(kRows / a->tile_heads);
+  a->tokens = a->tile_rows / a->tile_heads;
   a->heads = static_cast<int32_t>(Hkv * a->head_tiles);
   a->window = window >= reach ? 0 : window;  // (one of the whole reach hides nothing)
   a->sinks = a->window > 0 ? static_cast<int32_t>(std::min<int64_t>(sinks, reach)) : 0;
@@ -51,7 +53,7 @@ bool chunk_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* 
 
 uint64_t chunk_workspace(const ChunkArgs& a, int64_t D) {
   const uint64_t padded = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  return a.runs == 1 || a.single ? 0 : static_cast<uint64_t>(2 * a.runs) * (padded + 2) * kRows * sizeof(float);
+  return a.runs == 1 || a.single ? 0 : static_cast<uint64_t>(2 * a.runs) * (padded + 2) * a.tile_rows * sizeof(float);
 }
 
 }  // namespace

@@ -81,10 +81,10 @@ def test_no_rows():
 
 
 def test_the_workspace():
-    """None for a call that one run does; two parts a run, of 128 rows with two more values, otherwise."""
+    """None where every row tile is one workgroup's; two parts a run otherwise, of a row tile with two more values a row."""
     assert need(args()) == (OK, 0)
     st, big = need(args(t=64, width=4096))
-    assert st == OK and big == 2 * 512 * 128 * (D + 2) * 4
+    assert st == OK and big == 2 * 512 * 64 * (D + 2) * 4  # (22 tokens of 2 heads a sequence: row tiles of 64)
     a = args(t=64, width=4096)
     assert call(a) == NULLP
     assert call(with_(a, ws=DUMMY, size=big - 1)) == INVAL and call(with_(a, ws=DUMMY + 4, size=big)) == INVAL
@@ -93,7 +93,7 @@ def test_the_workspace():
     assert few == (OK, 0)
     assert need(args(t=3, b=1, width=4096))[1] > 0
     # heads above 128 run one workgroup a CU
-    assert need(args(t=64, width=4096, d=256))[1] == 2 * 256 * 128 * 258 * 4
+    assert need(args(t=64, width=4096, d=256))[1] == 2 * 256 * 64 * 258 * 4
 
 
 @no_gpu

@@ -80,6 +80,17 @@ def test_chunk(mode, dt, Hq, H, D, P):
 
 
 @pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("D,P", [(64, 16), (96, 32), (128, 16), (256, 16)])
+@pytest.mark.parametrize("rows", [1, 3, 6])
+def test_row_tiles(mode, D, P, rows):
+    """Row tiles of 32, 64 and 128 (by the mean number of rows of a cache head: 16, 48 and 96), sequences of other numbers among them,
+    some long enough that their walks are split."""
+    for window, sinks in ((0, 0), (300, 20)):
+        say(f"[gpu] tiles {mode} D={D} rows={rows} window={window}")
+        _run([(rows, 2100), (2 * rows, 70), (rows, 15), (0, 33), (1, 901)], 16, 1, D, P, mode, "bf16", window, sinks, seed=20)
+
+
+@pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 300), (37, 4), (64, 64), (65, 0), (128, 65), (100000, 7)])
 def test_window(mode, window, sinks):
     for Hq, H, D, P, dt in ((8, 2, 64, 16, "bf16"), (7, 1, 128, 32, "f16")):
