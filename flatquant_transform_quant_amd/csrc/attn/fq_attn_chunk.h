@@ -63,6 +63,13 @@ __device__ __forceinline__ int lane_here() {
   return lane & 63;  // (so that its range stays known)
 }
 
+// A kernel's arguments (its first ones), read anew from here on, for the same reason: scalar registers.
+__device__ __forceinline__ const ChunkArgs& args_here() {
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ChunkArgs*)(const __attribute__((address_space(4))) ChunkArgs*)p;
+}
+
 // ---- the plan ------------------------------------------------------------------------------
 
 struct Seq {
@@ -410,6 +417,42 @@ __device__ __forceinline__ int64_t row_at(const ChunkArgs& a, int hk, int k) {
   return (static_cast<int64_t>(hk) << a.c.page_log) + (k & ((1 << a.c.page_log) - 1));
 }
 
+// a = acc[D] times f where `need` (the wave's) is not 0.  The compiler copies the 16-register blocks to other registers and back around such a
+// branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 300); so each block has a place
+// that the statements ask for, and the branch is inside: nothing is left to copy.  With it the wait states between the products that wrote the block and
+// this read (at most 18), and between this write and the products that read it.
+template <int D>
+__device__ __forceinline__ void scale_block(f32x16_t& a, float f, int need) {
+  need = __builtin_amdgcn_readfirstlane(need);
+#define FQ_SCALE(N, R0, R1, R2, R3, R4, R5, R6, R7, R8, R9, R10, R11, R12, R13, R14, R15) \
+  if constexpr (D == N) \
+    asm("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lfq_scaled%=\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\t" \
+        "v_mul_f32 v" #R0 ", %1, v" #R0 "\n\t" "v_mul_f32 v" #R1 ", %1, v" #R1 "\n\t" "v_mul_f32 v" #R2 ", %1, v" #R2 "\n\t" "v_mul_f32 v" #R3 ", %1, v" #R3 "\n\t" "v_mul_f32 v" #R4 ", %1, v" #R4 "\n\t" "v_mul_f32 v" #R5 ", %1, v" #R5 "\n\t" "v_mul_f32 v" #R6 ", %1, v" #R6 "\n\t" "v_mul_f32 v" #R7 ", %1, v" #R7 "\n\t" "v_mul_f32 v" #R8 ", %1, v" #R8 "\n\t" "v_mul_f32 v" #R9 ", %1, v" #R9 "\n\t" "v_mul_f32 v" #R10 ", %1, v" #R10 "\n\t" "v_mul_f32 v" #R11 ", %1, v" #R11 "\n\t" "v_mul_f32 v" #R12 ", %1, v" #R12 "\n\t" "v_mul_f32 v" #R13 ", %1, v" #R13 "\n\t" "v_mul_f32 v" #R14 ", %1, v" #R14 "\n\t" "v_mul_f32 v" #R15 ", %1, v" #R15 "\n\t" \
+        "s_nop 3\n.Lfq_scaled%=:" : "={v[" #R0 ":" #R15 "]}"(a) : "v"(f), "s"(need), "0"(a) : "scc")
+  FQ_SCALE(0, 16, 17, 18, 19, 20, 21, 22, 23, 24, 25, 26, 27, 28, 29, 30, 31);
+  FQ_SCALE(1, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 42, 43, 44, 45, 46, 47);
+  FQ_SCALE(2, 48, 49, 50, 51, 52, 53, 54, 55, 56, 57, 58, 59, 60, 61, 62, 63);
+  FQ_SCALE(3, 64, 65, 66, 67, 68, 69, 70, 71, 72, 73, 74, 75, 76, 77, 78, 79);
+  FQ_SCALE(4, 80, 81, 82, 83, 84, 85, 86, 87, 88, 89, 90, 91, 92, 93, 94, 95);
+  FQ_SCALE(5, 96, 97, 98, 99, 100, 101, 102, 103, 104, 105, 106, 107, 108, 109, 110, 111);
+  FQ_SCALE(6, 112, 113, 114, 115, 116, 117, 118, 119, 120, 121, 122, 123, 124, 125, 126, 127);
+  FQ_SCALE(7, 128, 129, 130, 131, 132, 133, 134, 135, 136, 137, 138, 139, 140, 141, 142, 143);
+#undef FQ_SCALE
+}
+
+// Holds a[d] at the registers that scale_block has for it.
+template <int D>
+__device__ __forceinline__ void pin_block(f32x16_t& a) {
+  if constexpr (D == 0) asm("" : "={v[16:31]}"(a) : "0"(a));
+  if constexpr (D == 1) asm("" : "={v[32:47]}"(a) : "0"(a));
+  if constexpr (D == 2) asm("" : "={v[48:63]}"(a) : "0"(a));
+  if constexpr (D == 3) asm("" : "={v[64:79]}"(a) : "0"(a));
+  if constexpr (D == 4) asm("" : "={v[80:95]}"(a) : "0"(a));
+  if constexpr (D == 5) asm("" : "={v[96:111]}"(a) : "0"(a));
+  if constexpr (D == 6) asm("" : "={v[112:127]}"(a) : "0"(a));
+  if constexpr (D == 7) asm("" : "={v[128:143]}"(a) : "0"(a));
+}
+
 // ---- the products of 32 keys with 32 query rows ------------------------------------------------------
 
 template <int MODE, int DT, int DP, bool PAD>
@@ -473,10 +516,10 @@ struct Block {
   }
 
   // Keys k0 .. k0 + 32 NB - 1, their rows at kt and vt in LDS (from a multiple of 32 on), their factors at ks and vs.  in: which 16
-  // of them have a page; big: the largest value scale; least: what a rescaling factor is at least.  `scored` is called when
-  // the scores have been formed, before a value is read.
+  // of them have a page; big: the largest value scale.  `scored` is called when
+  // the score products are under way, before a value is read.
   template <int NB, typename F>
-  __device__ __forceinline__ void step(const Place& p, int lane, int sinks, int k0, uint32_t in, float big, float least, const lds_u8* kt, const lds_u8* vt,
+  __device__ __forceinline__ void step(const Place& p, int lane, int sinks, int k0, uint32_t in, float big, const lds_u8* kt, const lds_u8* vt,
                                        const float* ks_, const float* vs_, F&& scored) {
     const int col = lane & 31, hf = lane >> 5;
     const uint32_t krd = col * kRowB, kx = hf ^ key_swz<DP>(col);
@@ -511,6 +554,7 @@ struct Block {
         __builtin_amdgcn_sched_barrier(0);
       });
     }
+    scored();
     if constexpr (kLow) {
 #pragma unroll
       for (int j = 0; j < 4 * NB; ++j) {
@@ -519,13 +563,13 @@ struct Block {
         for (int i = 0; i < 4; ++i) s[j / 4][4 * (j % 4) + i] *= f[i];
       }
     }
-    scored();
     u32x4_t vf[2 * NB * DB];
 #pragma unroll
     for (int i = 0; i < kAhead && i < 2 * NB * DB; ++i) vf[i] = value(i % DB, i / DB);
     __builtin_amdgcn_sched_barrier(0);
     const bool masked = k0 + 32 * NB - 1 > p.lim_first || (k0 < p.lo_last && k0 + 32 * NB > sinks) || in != (1u << (2 * NB)) - 1u;
     if (masked) {
+      asm volatile("");  // (a branch: as selects, this is done for every tile)
       // this lane's places (4 hf less than the key among these): seen up to `left`, and from `from` on or below `sk`
       const int left = p.lim - k0 - 4 * hf, from = p.lo - k0 - 4 * hf, sk = sinks - k0 - 4 * hf;
 #pragma unroll
@@ -551,22 +595,21 @@ struct Block {
       }
       ev = static_cast<int>(__float_as_uint(big) >> 23) - 127;
     }
-    if (__any(top * c > m + kLazy || (kLow && ev > ref + 1))) {
+    float f = 1.0f;
+    const int need = __any(top * c > m + kLazy || (kLow && ev > ref + 1));
+    if (need) {
       const float mn = fmaxf(m, half_max(top) * c);
       int rn = ref;
       if constexpr (kLow) {
         const auto r = __builtin_amdgcn_permlane32_swap(ev, ev, false, false);
         rn = max(ref, min(kMostRef, max(static_cast<int>(r[0]), static_cast<int>(r[1]))));
       }
-      const float f = mn == -kInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((m + static_cast<float>(ref)) - (mn + static_cast<float>(rn))), least);
+      f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f((m + static_cast<float>(ref)) - (mn + static_cast<float>(rn)));
       m = mn;
       ref = rn;
       l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] *= f;
     }
+    static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { scale_block<decltype(dc)::value>(acc[decltype(dc)::value], f, need); });
     const float ms = m == -kInf ? 0.0f : m + static_cast<float>(ref) - kW;
     u32x4_t pf[2 * NB];
 #pragma unroll
@@ -599,35 +642,65 @@ struct Block {
     });
   }
 
-  // The walk again, with values that are infinite or NaN in it: they are added to the rows that see them (a seen infinity
-  // stays one, however small its weight) ...
-  __device__ __forceinline__ void add_odd(const Place& p, int sinks, int k0, uint32_t in, const lds_u8* vt) {
+  // Where a sum is not finite, the walk is done again with the values that are infinite or NaN taken out of the products: they
+  // are noted for the rows that see them, a bit an element of a lane's sums for infinity, for minus infinity or both (NaN), in
+  // LDS (words 2 w and 2 w + 1 of each lane), and added at the end, so that a seen infinity stays one, however small its weight ...
+  static constexpr int kWords = DB / 2;
+  typedef uint32_t Odd[2 * kWords][64];
+  static __device__ __forceinline__ void no_odd(Odd& o) {
+#pragma unroll
+    for (int w = 0; w < 2 * kWords; ++w) o[w][threadIdx.x & 63] = 0u;
+  }
+  static __device__ __forceinline__ void note_odd(Odd& o, const Place& p, int sinks, int k0, uint32_t in, const lds_u8* vt) {
     const int lane = lane_here(), hf = lane >> 5;
+#pragma clang loop unroll(disable)
     for (int j = 0; j < 32; ++j) {
       bool odd = false;
       for (int e = 2 * lane; e < DP; e += 128)
         odd |= not_finite16<ODT>(*(const __attribute__((address_space(3))) uint32_t*)(vt + j * kRowB + 2 * e)) != 0;
       if (!__any(odd) || !((in >> (j / 16)) & 1u)) continue;
       const int k = k0 + j;
-      const bool seen = k <= p.lim && (k >= p.lo || k < sinks);
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 32 * d + 8 * (i / 4) + 4 * hf + i % 4;
+      if (!(k <= p.lim && (k >= p.lo || k < sinks))) continue;
+#pragma clang loop unroll(disable)
+      for (int w = 0; w < kWords; ++w) {
+        uint32_t up = 0, down = 0;
+#pragma clang loop unroll(disable)
+        for (int i = 0; i < 32; ++i) {
+          const int e = 64 * w + 8 * (i / 4) + 4 * hf + i % 4;
           const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(vt + j * kRowB + 16 * ((e / 8) ^ value_swz<DP>(j)) + 2 * (e % 8));
-          if (seen && not_finite16<ODT>(v)) acc[d][i] += load16<ODT>(v);
-          if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (registers: few of these reads at a time)
+          const float x = load16<ODT>(v);
+          const uint32_t bit = not_finite16<ODT>(v) ? 1u << i : 0u;
+          up |= x < 0.0f ? 0u : bit;
+          down |= x > 0.0f ? 0u : bit;
         }
+        o[2 * w][lane] |= up;
+        o[2 * w + 1][lane] |= down;
+      }
+    }
+  }
+  __device__ __forceinline__ void add_odd(const Odd& o) {
+    const int lane = lane_here();
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      const uint32_t up = o[2 * (d / 2)][lane], down = o[2 * (d / 2) + 1][lane];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int bit = 16 * (d % 2) + i;
+        acc[d][i] += ((up >> bit) & 1u ? kInf : 0.0f) + ((down >> bit) & 1u ? -kInf : 0.0f);
+      }
     }
   }
   // ... and taken out of the products, `rows` rows at vt.
   static __device__ __forceinline__ void drop_odd(lds_u8* vt, int rows) {
+#pragma clang loop unroll(disable)
     for (int i = lane_here(); i < rows * (DP / 2); i += 64) {
       __attribute__((address_space(3))) uint32_t* const at = (__attribute__((address_space(3))) uint32_t*)(vt + 4 * i);
       const uint32_t v = *at;
       *at = v & ~not_finite16_mask<ODT>(v);
     }
+  }
+  __device__ __forceinline__ void pin() {
+    static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { pin_block<decltype(dc)::value>(acc[decltype(dc)::value]); });
   }
   // whether a sum is infinite or NaN
   __device__ __forceinline__ bool odd() const {
@@ -688,7 +761,7 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& a, const Run& r, S
 // RB blocks of 32 rows: 4, a wave each; or 2, where waves 2 and 3 have the same rows as 0 and 1 and the tile's other 32 keys, and
 // their sums are joined at the segment's end.
 template <int MODE, int DT, int DP, bool PAD, int RB>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel(ChunkArgs a, float* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
   using RW = Rows<MODE, DP, PAD, 16>;
   constexpr bool kLow = BK::kLow;
@@ -700,16 +773,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
   __shared__ __align__(16) float s_scale[kLow ? 2 : 1][2][kLow ? kKeys : 1];  // [buffer][keys, values]
   __shared__ __align__(16) float s_top[kLow ? 2 : 1][kWaves];                 // largest value scale of 16 keys
   __shared__ float s_m[2][RB == 2 ? 64 : 1];                                   // of waves 2 and 3: m + R, l
+  __shared__ typename BK::Odd s_odd[kWaves];
   lds_u8* const lds_l = (lds_u8*)lds;
   const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
 
-  const KvCache& cc = a.c;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int D = PAD ? cc.D : DP;
+  const int D = PAD ? args_here().c.D : DP;
   const int rowb = static_cast<int>(kv_row_bytes(MODE, D)), sb = static_cast<int>(kv_scale_bytes(MODE, D));
-  const Run run = run_of(a);
+  const Run run = run_of(args_here());
   if (run.last <= run.first) return;
-  Segment sg = segment_at(a, run.first);
+  Segment sg = segment_at(args_here(), run.first);
 
   // LDS-DMA of 16-bit rows: load i of a wave fills the 16-byte places 64 (NL w + i) + lane of a tile, its 16 rows in all
   uint32_t koff[NL], voff[NL];
@@ -725,6 +798,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
   int step = 0;  // of this workgroup; the tile of step s is in buffer s % 2
 
   do {
+    const ChunkArgs& a = args_here();
+    const KvCache& cc = a.c;
     const Walk wk = walk_of(a, sg.s, sg.tile);
     const Share sh = share_of(a, run, sg, wk);
     if (!sh.whole && sh.u0 >= sh.u1) continue;
@@ -770,16 +845,19 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
         const int buf = step & 1, k0 = wk.tile(u) * kKeys;
         const uint32_t in = pages.bits(u);  // which 16 keys have a page
         tile_barrier();
-        if (u + 1 < sh.u1) {
-          if constexpr (kLow)
-            load(u + 1);
-          else
-            dma(u + 1, buf ^ 1);
-        }
+        // the next tile's loads: their addresses are formed while the first score products run
+        auto ahead = [&]() __attribute__((always_inline)) {
+          if (u + 1 < sh.u1) {
+            if constexpr (kLow)
+              load(u + 1);
+            else
+              dma(u + 1, buf ^ 1);
+          }
+        };
         lds_u8* const kt = lds_l + buf * (2 * kTileB);
         lds_u8* const vt = kt + kTileB;
         if (careful) {
-          for (int b = RB == 2 ? wv / 2 : 0; b < (RB == 2 ? wv / 2 + 1 : 2); ++b) bk.add_odd(pl, a.sinks, k0 + 32 * b, (in >> (2 * b)) & 3u, vt + 32 * b * kRowB);
+          for (int b = RB == 2 ? wv / 2 : 0; b < (RB == 2 ? wv / 2 + 1 : 2); ++b) BK::note_odd(s_odd[wv], pl, a.sinks, k0 + 32 * b, (in >> (2 * b)) & 3u, vt + 32 * b * kRowB);
           __syncthreads();
           BK::drop_odd(vt + 16 * wv * kRowB, 16);
           __syncthreads();
@@ -789,21 +867,30 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 #pragma unroll
         for (int i = 0; i < (RB == 2 ? 1 : 2 / NB); ++i) {
           const int b = RB == 2 ? wv / 2 : i;
-          if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) continue;
+          if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) {
+            if (i == 0) ahead();
+            continue;
+          }
           const float big = kLow ? fmaxf(s_top[buf][2 * b], s_top[buf][2 * b + 1]) : 0.0f;
-          bk.template step<NB>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big, careful ? 0x1p-126f : 0.0f,
-                               kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [] {});
+          bk.template step<NB>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big,
+                               kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [&]() __attribute__((always_inline)) { if (i == 0) ahead(); });
         }
         if constexpr (kLow) {
           if (u + 1 < sh.u1) store(buf ^ 1);
         }
       }
-      if (careful || !__syncthreads_or(bk.odd())) break;
+      bk.pin();
+      if (careful || !__syncthreads_or(bk.odd())) {
+        if (careful) bk.add_odd(s_odd[wv]);
+        break;
+      }
       careful = true;
+      BK::no_odd(s_odd[wv]);
     }
     // (no barrier needed here: the next segment's first tile takes the buffer that was last read a step before the last one)
 
     const int end = lane_here(), col = end & 31, hf = end >> 5;
+    const ChunkArgs& z = args_here();
     float l = half_sum(bk.l), m = bk.m + static_cast<float>(bk.ref);
     if constexpr (RB == 2) {  // waves 2 and 3 hand their sums over in the other buffer
       float* const at = reinterpret_cast<float*>(lds + ((step & 1) ^ 1) * (2 * kTileB)) + (wv & 1) * (32 * DP) + col;
@@ -842,7 +929,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
     } else if (pl.mine) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t to = sg.s.q0 + pl.token;
-      uint16_t* const out = a.out.p + to * a.out.row + pl.head * a.out.head;
+      uint16_t* const out = z.out.p + to * z.out.row + pl.head * z.out.head;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -854,9 +941,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
           for (int j = 0; j < 4; ++j) o[j] = bk.acc[d][4 * i + j] * inv * kUnitV<MODE>;
           *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(o[0], o[1]), round16x2<DT>(o[2], o[3])};
         }
-      if (a.lse && hf == 0) a.lse[to * a.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
+      if (z.lse && hf == 0) z.lse[to * z.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
     }
-  } while (next_segment(a, run, sg));
+  } while (next_segment(args_here(), run, sg));
 }
 
 // ---- row tiles of 32: every wave has all of them, and keys of its own --------------------------------------
@@ -865,7 +952,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 // waves' sums are joined.  Low-bit rows go through registers, the next 32 on their way during the products of these; 16-bit ones by
 // LDS-DMA, the next keys as soon as the scores are done with these, the next values behind the second products.
 template <int MODE, int DT, int DP, bool PAD>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kernel(ChunkArgs a, float* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
   constexpr bool kLow = BK::kLow;
   using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 32>;
@@ -876,19 +963,21 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
   __shared__ __align__(16) uint8_t lds[kWaves][2 * kSideB];
   __shared__ __align__(16) float s_scale[kLow ? kWaves : 1][2][32];
   __shared__ float s_m[kWaves][32], s_l[kWaves][32];
+  __shared__ typename BK::Odd s_odd[kWaves];
 
-  const KvCache& cc = a.c;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int D = PAD ? cc.D : DP;
+  const int D = PAD ? args_here().c.D : DP;
   const int rowb = static_cast<int>(kv_row_bytes(MODE, D)), sb = static_cast<int>(kv_scale_bytes(MODE, D));
-  const Run run = run_of(a);
+  const Run run = run_of(args_here());
   if (run.last <= run.first) return;
-  Segment sg = segment_at(a, run.first);
+  Segment sg = segment_at(args_here(), run.first);
   lds_u8* const kt = (lds_u8*)lds[wv];
   lds_u8* const vt = kt + kSideB;
   const uint32_t k_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt));
 
   do {
+    const ChunkArgs& a = args_here();
+    const KvCache& cc = a.c;
     const Walk wk = walk_of(a, sg.s, sg.tile);
     const Share sh = share_of(a, run, sg, wk);
     if (!sh.whole && sh.u0 >= sh.u1) continue;
@@ -956,26 +1045,30 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
           big = store_rows(x, lane, lds[wv], lds[wv] + kSideB, s_scale[wv][0], s_scale[wv][1], 0);
           lds_done();  // (other lanes' rows are read below)
         }
-        if (more) {
+        auto ahead = [&]() __attribute__((always_inline)) {
+          if (!more) return;
           in = bits(v + kWaves);
           if constexpr (kLow) load(v + kWaves);
-        }
+        };
         if (careful) {
           if constexpr (!kLow) landed(false);
-          bk.add_odd(pl, a.sinks, k0, now, vt);
+          BK::note_odd(s_odd[wv], pl, a.sinks, k0, now, vt);
           lds_done();
           BK::drop_odd(vt, 32);
           lds_done();
         }
-        const float least = careful ? 0x1p-126f : 0.0f;
         const bool sees = BK::sees(pl, a.sinks, k0, 32);
         if constexpr (kLow) {
-          if (sees) bk.template step<1>(pl, lane, a.sinks, k0, now, big, least, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
+          if (sees)
+            bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], ahead);
+          else
+            ahead();
           lds_done();  // (before the next rows take their places)
         } else {
           landed(true);  // (the keys)
-          bk.template step<1>(pl, lane, a.sinks, k0, now, big, least, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
+          bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
             lds_done();
+            ahead();
             if (more) dma(v + kWaves, 0);
             landed(more);  // (the values)
           });
@@ -983,12 +1076,18 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
           if (more) dma(v + kWaves, 1);
         }
       }
-      if (careful || !__syncthreads_or(bk.odd())) break;
+      bk.pin();
+      if (careful || !__syncthreads_or(bk.odd())) {
+        if (careful) bk.add_odd(s_odd[wv]);
+        break;
+      }
       careful = true;
+      BK::no_odd(s_odd[wv]);
     }
 
     // ---- the waves' sums: [element][row] of each wave, then a wave joins a quarter of the elements
     const int end = lane_here(), col = end & 31, hf = end >> 5;
+    const ChunkArgs& z = args_here();
     float* const mine = reinterpret_cast<float*>(lds[wv]);
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -1034,7 +1133,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
     } else if (pl.mine) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t to = sg.s.q0 + pl.token;
-      uint16_t* const out = a.out.p + to * a.out.row + pl.head * a.out.head + e0;
+      uint16_t* const out = z.out.p + to * z.out.row + pl.head * z.out.head + e0;
 #pragma unroll
       for (int j = 0; j < NE; j += 8) {
         if (PAD && e0 + j >= D) break;
@@ -1043,15 +1142,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         for (int i = 0; i < 4; ++i) w[i] = round16x2<DT>(o[j + 2 * i] * inv * kUnitV<MODE>, o[j + 2 * i + 1] * inv * kUnitV<MODE>);
         *reinterpret_cast<u32x4_t*>(out + j) = w;
       }
-      if (a.lse && wv == 0 && hf == 0) a.lse[to * a.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
+      if (z.lse && wv == 0 && hf == 0) z.lse[to * z.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
     }
-  } while (next_segment(a, run, sg));
+  } while (next_segment(args_here(), run, sg));
 }
 
 // Joins the parts of a segment that several runs share: the workgroups of run i do the one that begins in run i and
-// goes on behind it; a thread a row and four elements, a workgroup 1024 / TR elements.
+// goes on behind it; a workgroup 32 elements, a thread a row and TR / 8 of them.
 template <int MODE, int DT, int DP, int TR>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const float* __restrict__ ws) {
+  constexpr int NE = TR / 8;
   const Deal deal(all_places(a), a.runs);
   const int run = blockIdx.x;
   if (run + 1 >= static_cast<int>(deal.runs)) return;
@@ -1061,14 +1161,16 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
   const int base = sg.at + kStart;
   if (deal.start(run) > base || end <= base || end - base >= wk.n) return;  // its first tile is not here, or its last one is
   const int hk = sg.head / a.head_tiles, ht = sg.head - hk * a.head_tiles, hn = min(a.tile_heads, a.g - ht * a.tile_heads);
-  const int r = threadIdx.x % TR, e = (1024 / TR) * blockIdx.y + 4 * (threadIdx.x / TR);
+  const int r = threadIdx.x % TR, e = 32 * blockIdx.y + NE * (threadIdx.x / TR);
   const int token = wk.row0 + r / a.tile_heads, hr = r % a.tile_heads, head = hk * a.g + ht * a.tile_heads + hr;
   if (token > wk.row1 || r >= a.tokens * a.tile_heads || hr >= hn || e >= a.c.D) return;
   int parts = 1;  // behind the first
   while (deal.start(run + parts + 1) - base < wk.n) ++parts;
-  float m = -kInf, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -kInf, l = 0.0f, o[NE];
+#pragma unroll
+  for (int j = 0; j < NE; ++j) o[j] = 0.0f;
   for (int i = 0; i <= parts; i += 4) {  // (four parts' loads at a time)
-    float mi[4], li[4], x[4][4];
+    float mi[4], li[4], x[4][NE];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int part = min(i + k, parts);
@@ -1076,7 +1178,7 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
       mi[k] = p[DP * TR];
       li[k] = p[(DP + 1) * TR];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[k][j] = p[(e + j) * TR];
+      for (int j = 0; j < NE; ++j) x[k][j] = p[(e + j) * TR];
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1086,13 +1188,18 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
       m = mn;
       l = li[k] == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li[k] * f1);  // (nothing seen, or NaN)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(o[j], f0, x[k][j] * f1);
+      for (int j = 0; j < NE; ++j) o[j] = __builtin_fmaf(o[j], f0, x[k][j] * f1);
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t to = sg.s.q0 + token;
-  *reinterpret_cast<u32x2_t*>(a.out.p + to * a.out.row + head * a.out.head + e) =
-      u32x2_t{round16x2<DT>(o[0] * inv * kUnitV<MODE>, o[1] * inv * kUnitV<MODE>), round16x2<DT>(o[2] * inv * kUnitV<MODE>, o[3] * inv * kUnitV<MODE>)};
+  uint16_t* const out = a.out.p + to * a.out.row + head * a.out.head + e;
+#pragma unroll
+  for (int j = 0; j < NE; j += 4) {
+    if (e + j >= a.c.D) break;
+    *reinterpret_cast<u32x2_t*>(out + j) = u32x2_t{round16x2<DT>(o[j] * inv * kUnitV<MODE>, o[j + 1] * inv * kUnitV<MODE>),
+                                                   round16x2<DT>(o[j + 2] * inv * kUnitV<MODE>, o[j + 3] * inv * kUnitV<MODE>)};
+  }
   if (a.lse && e == 0)
     a.lse[to * a.Hq + head] = l == 0.0f ? -kInf : (m - kUpW<MODE, DT> + __builtin_amdgcn_logf(l)) * 0.693147181f;
 }
@@ -1106,7 +1213,7 @@ hipError_t chunk_go(const ChunkArgs& a, float* ws, hipStream_t s) {
     chunk_wide_kernel<MODE, DT, DP, PAD, TR / 32><<<grid, kThreads, 0, s>>>(a, ws);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.runs == 1 || a.single) return err;
-  chunk_join_kernel<MODE, DT, DP, TR><<<dim3(static_cast<uint32_t>(a.runs - 1), static_cast<uint32_t>(ceil_div(a.c.D, 1024 / TR))), kThreads, 0, s>>>(a, ws);
+  chunk_join_kernel<MODE, DT, DP, TR><<<dim3(static_cast<uint32_t>(a.runs - 1), static_cast<uint32_t>(ceil_div(a.c.D, 32))), kThreads, 0, s>>>(a, ws);
   return hipGetLastError();
 }
 
