@@ -110,9 +110,10 @@ def _load():
     L.fq_attn_prefill.argtypes = [vp] * 5 + [ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
     L.fq_qk_rope.argtypes = [vp] * 4 + [dbl, vp, vp, vp, ctypes.c_int32, vp, vp, vp]
     L.fq_kv_append.argtypes = [vp] * 6 + [dbl, vp, vp, vp, ctypes.c_int32, dbl, dbl] + [vp] * 6
+    L.fq_int8_gemm.argtypes = [vp] * 6
     L.fq_attn_chunk_get_workspace_size.argtypes = [vp] * 4 + [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(u64)]
     L.fq_attn_chunk.argtypes = [vp] * 8 + [ctypes.c_int32, ctypes.c_int32, dbl, vp, vp, vp, u64, vp]
-    for f in (L.fq_attn_chunk_get_workspace_size, L.fq_attn_chunk, L.fq_qk_rope, L.fq_kv_append, L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
+    for f in (L.fq_int8_gemm, L.fq_attn_chunk_get_workspace_size, L.fq_attn_chunk, L.fq_qk_rope, L.fq_kv_append, L.fq_kv_write, L.fq_kv_read, L.fq_attn_decode_get_workspace_size, L.fq_attn_decode,
               L.fq_attn_prefill_get_workspace_size, L.fq_attn_prefill):
         f.restype = ctypes.c_int32
     return L
@@ -123,7 +124,8 @@ EXPORTS = ("fq_get_workspace_size", "fq_run", "fq_executor_destroy", "fq_executo
            "fq_executor_set_kernel", "fq_executor_kernel", "fq_status_string", "fq_last_error", "fq_dequant",
            "fq_v1_get_workspace_size", "fq_mx_gemm", "fq_int4_gemm", "fq_run_no_alloc", "fq_kv_write", "fq_kv_read",
            "fq_attn_decode_get_workspace_size", "fq_attn_decode", "fq_attn_prefill_get_workspace_size",
-           "fq_attn_prefill", "fq_qk_rope", "fq_kv_append", "fq_attn_chunk_get_workspace_size", "fq_attn_chunk")
+           "fq_attn_prefill", "fq_qk_rope", "fq_kv_append", "fq_attn_chunk_get_workspace_size", "fq_attn_chunk",
+           "fq_int8_gemm")
 NO_ALLOC_SCRATCH_BYTES = 64 << 20  # FQ_NO_ALLOC_SCRATCH_BYTES of include/fq.h
 
 
@@ -415,6 +417,21 @@ def int4_gemm(a_codes, a_scale, w_codes, w_scale, H: int, out_dtype=None, out=No
                       (stream if stream is not None else torch.cuda.current_stream(a_codes.device)).cuda_stream)
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_int4_gemm")
+    return out
+
+
+def int8_gemm(a_codes, a_scale, w_codes, w_scale, out_dtype=None, out=None, stream=None):
+    """C [T, O] = a_scale[t] w_scale[o] (A . W^T) for int8 codes: torch.int8 [rows, H] (the int8 out of ``empty_outputs``
+    viewed as [K, M*N], say), scales float32 [rows].  C is torch.bfloat16 (default), torch.float16 or torch.float32."""
+    torch = _torch()
+    _same_gpu(stream, a_codes, a_scale, w_codes, w_scale, out)
+    if out is None:
+        make = lambda: torch.empty((a_codes.shape[0], w_codes.shape[0]), dtype=out_dtype or torch.bfloat16, device=a_codes.device)  # noqa: E731
+        out = make() if stream is None else _new(stream, make)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out is of another type than out_dtype")
+    d = _Descs(a_codes, a_scale, w_codes, w_scale, out)
+    _call(lib.fq_int8_gemm, "fq_int8_gemm", a_codes.device, *d.ptrs, _stream(stream, a_codes.device))
     return out
 
 

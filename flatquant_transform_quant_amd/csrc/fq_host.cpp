@@ -571,6 +571,36 @@ fq_status fq_int4_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_te
   return FQ_SUCCESS;
 }
 
+fq_status fq_int8_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
+                       const fq_tensor* c, hipStream_t stream) {
+  clear_last_error();
+  auto empty = [](const fq_tensor* t) { return t->ndim >= 1 && t->ndim <= 2 && (t->shape[0] == 0 || (t->ndim == 2 && t->shape[1] == 0)); };
+  for (const fq_tensor* t : {a, a_scale, w, w_scale, c})
+    if (!t || (!t->data && !empty(t))) return FQ_ERR_PARAM_NULLPTR;
+  for (const fq_tensor* t : {a, a_scale, w, w_scale, c})  // (an empty tensor's strides say nothing)
+    if (!strides_ok(*t) || (!empty(t) && !is_contiguous(*t))) return FQ_ERR_PARAM_INVALID;
+  if (a->dtype != FQ_DT_INT8 || w->dtype != FQ_DT_INT8 || a->ndim != 2 || w->ndim != 2) return FQ_ERR_PARAM_INVALID;
+  const int64_t T = a->shape[0], H = a->shape[1], O = w->shape[0];
+  if (H < 16 || H % 16 != 0 || H >= (int64_t(1) << 17) || w->shape[1] != H) return FQ_ERR_PARAM_INVALID;
+  if (a_scale->dtype != FQ_DT_FLOAT32 || !shape_is(*a_scale, 1, T)) return FQ_ERR_PARAM_INVALID;
+  if (w_scale->dtype != FQ_DT_FLOAT32 || !shape_is(*w_scale, 1, O)) return FQ_ERR_PARAM_INVALID;
+  const int32_t out = c->dtype == FQ_DT_FLOAT32 ? 0 : c->dtype == FQ_DT_FLOAT16 ? fq::kF16 : c->dtype == FQ_DT_BFLOAT16 ? fq::kBF16 : -1;
+  if (out < 0 || !shape_is(*c, 2, T, O)) return FQ_ERR_PARAM_INVALID;
+  const int64_t lim = int64_t(1) << 26;  // (and a launch's workgroups below 2^23, of up to 512 threads)
+  if (T >= lim || O >= lim || ceil_div(T, 128) * ceil_div(O, 128) >= (int64_t(1) << 23)) return FQ_ERR_PARAM_INVALID;
+  auto al = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  if (!al(a->data, 16) || !al(w->data, 16) || !al(a_scale->data, 4) || !al(w_scale->data, 4) ||
+      !al(c->data, c->dtype == FQ_DT_FLOAT32 ? 4 : 2))
+    return FQ_ERR_PARAM_INVALID;
+  if (T == 0 || O == 0) return FQ_SUCCESS;
+  if (!device_is_gfx950()) return fail_runtime("the current device is not gfx950", hipSuccess);
+  const hipError_t err = fq::launch_int8_gemm(T, O, H, static_cast<const uint8_t*>(a->data), static_cast<const float*>(a_scale->data),
+                                              static_cast<const uint8_t*>(w->data), static_cast<const float*>(w_scale->data), c->data,
+                                              out, stream);
+  if (err != hipSuccess) return fail_runtime("int8 GEMM kernel launch", err);
+  return FQ_SUCCESS;
+}
+
 fq_status fq_mx_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
                      const fq_tensor* c, hipStream_t stream) {
   clear_last_error();

@@ -1,0 +1,249 @@
+// int8 consumer GEMM: C[t, o] = fl32(sum_h qa[t, h] qw[o, h]) * fl32(sa[t] * sw[o]) with A the quantizer's per-token int8
+// codes (its INT8 [K, M, N] output viewed as [K, M N]) and their fp32 scales, W int8 weights with one fp32 scale per output
+// channel.  The integer sums are exact in int32 (|sum| <= 2^14 H, H < 2^17), so C is one defined value, rounded once more to a 16-bit C.
+//
+// Tiles (many rows): a workgroup computes a BT x BO tile on v_mfma_i32_16x16x64_i8, 128 bytes of the contraction a stage: the
+// stage's rows of A and W are copied by LDS-DMA into one of two buffers while the other feeds the products, one barrier a
+// stage; chunk c of row r sits at c ^ (r & 7); W is the first operand, so a lane's four results are four consecutive columns
+// of one row; tiles are numbered XCD by XCD in groups of four row bands.
+// Rows (few rows, as in single steps): bound by reading W once.  A workgroup of eight waves has 16 or 32 channels; the waves
+// take 128 bytes of the contraction in turn, straight from memory into operand registers (both operands relabel the contraction the
+// same way: lane group kb has bytes 32 kb .. 32 kb + 31 of the 128), and their sums are added up in LDS.
+#include <hip/hip_runtime.h>
+
+#include "attn/fq_attn_tile.h"
+
+namespace fq {
+namespace {
+
+constexpr int kStage = 128;  // bytes of the contraction a stage
+constexpr int kGroup = 4;    // row bands walked together
+enum Out : int { kOutF32 = 0, kOutF16 = kF16, kOutBF16 = kBF16 };
+
+struct Gemm {
+  const uint8_t *a, *w;
+  const float *sa, *sw;
+  void* c;
+  int32_t T, O, H;
+  int32_t vec;  // rows of C are a whole number of four elements, aligned
+};
+
+// Four columns o .. o + 3 of row t from their sums.
+template <int OUT>
+__device__ __forceinline__ void put4(const Gemm& g, int t, int o, i32x4_t acc, float sa, f32x4_t sw) {
+  f32x4_t v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[e]) * (sa * sw[e]);
+  const int64_t at = static_cast<int64_t>(t) * g.O + o;
+  if (g.vec && o + 4 <= g.O) {
+    if constexpr (OUT == kOutF32)
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.c) + at) = v;
+    else
+      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(g.c) + at) = u32x2_t{round16x2<OUT>(v[0], v[1]), round16x2<OUT>(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (o + e >= g.O) break;
+      if constexpr (OUT == kOutF32)
+        static_cast<float*>(g.c)[at + e] = v[e];
+      else
+        static_cast<uint16_t*>(g.c)[at + e] = round16<OUT>(v[e]);
+    }
+  }
+}
+
+// ---- tiles ------------------------------------------------------------------------------------
+
+// BT x BO a workgroup, WT x WO waves
+template <int BT, int BO, int WT, int WO, int OUT>
+__global__ __launch_bounds__(64 * WT * WO) void tile_kernel(Gemm g, int32_t nT, int32_t nO) {
+  constexpr int NW = WT * WO, NI = BT / WT / 16, NJ = BO / WO / 16;
+  constexpr int LA = BT / 8 / NW, LW = BO / 8 / NW;  // LDS-DMA loads of a wave and stage: 8 rows each
+  constexpr int kStageB = (BT + BO) * kStage;
+  __shared__ __align__(16) uint8_t lds[2][kStageB];
+  const lds_u8* const lds_l = (const lds_u8*)lds[0];
+  const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  int b = blockIdx.x;
+  const int n = nT * nO;
+  if ((n & 7) == 0) b = (b & 7) * (n >> 3) + (b >> 3);  // dispatch goes round-robin over the 8 XCDs
+  const int grp = b / (kGroup * nO), gfirst = grp * kGroup, gsz = min(nT - gfirst, kGroup);
+  const int rem = b - grp * kGroup * nO;
+  const int t0 = (gfirst + rem % gsz) * BT, o0 = (rem / gsz) * BO;
+
+  // operand rows past T or O read zeros through resources that end with the tile's last row
+  const int H = g.H, rows_a = min(BT, g.T - t0), rows_w = min(BO, g.O - o0);
+  const i32x4_t ra = rsrc4(g.a + static_cast<int64_t>(t0) * H, static_cast<uint32_t>(rows_a * H));
+  const i32x4_t rw = rsrc4(g.w + static_cast<int64_t>(o0) * H, static_cast<uint32_t>(rows_w * H));
+  // load j of wave wv fills rows 8 (NW j + wv) .. + 7; lane l has chunk (l % 8) ^ (row & 7) of row l / 8
+  const int crow = 8 * wv + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3);
+  uint32_t off[LA > LW ? LA : LW];
+#pragma unroll
+  for (int j = 0; j < (LA > LW ? LA : LW); ++j) off[j] = static_cast<uint32_t>((8 * NW * j + crow) * H + 16 * chunk);
+  auto dma = [&](int buf, int kt) __attribute__((always_inline)) {
+    const uint32_t to = lds_addr + buf * kStageB + 1024 * wv;
+    const uint32_t past = kStage * kt + 16 * chunk < H ? 0u : kOut;  // (the last stage may be short)
+#pragma unroll
+    for (int j = 0; j < LA; ++j) dma16(to + 1024 * NW * j, (off[j] + kStage * kt) | past, ra);
+#pragma unroll
+    for (int j = 0; j < LW; ++j) dma16(to + BT * kStage + 1024 * NW * j, (off[j] + kStage * kt) | past, rw);
+  };
+
+  const int wm = wv / WO, wn = wv % WO;
+  const int r16 = lane & 15, kb = lane >> 4;
+  i32x4_t acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+
+  // 64 bytes of the contraction: W's fragments, then A's, each read while the products of the one before run
+  auto half = [&](int buf, int h) __attribute__((always_inline)) {
+    const lds_u8* const st = lds_l + buf * kStageB + 16 * ((4 * h + kb) ^ (r16 & 7));
+    const lds_u8* const ap = st + (16 * NI * wm + r16) * kStage;
+    const lds_u8* const wp = st + (BT + 16 * NJ * wn + r16) * kStage;
+    auto read = [](const lds_u8* p) __attribute__((always_inline)) { return *(const __attribute__((address_space(3))) i32x4_t*)p; };
+    i32x4_t wf[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) wf[j] = read(wp + 16 * j * kStage);
+    i32x4_t af = read(ap);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      i32x4_t next = af;
+      if (i + 1 < NI) next = read(ap + 16 * (i + 1) * kStage);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], af, acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      af = next;
+    }
+  };
+
+  const int nkt = (H + kStage - 1) / kStage;
+  dma(0, 0);
+  for (int kt = 0; kt < nkt; ++kt) {
+    tile_barrier();
+    if (kt + 1 < nkt) dma((kt + 1) & 1, kt + 1);
+    half(kt & 1, 0);
+    if (kStage * kt + 64 < H) half(kt & 1, 1);
+  }
+
+  // lane l holds C[t][o .. o + 3] with t = .. + 16 i + l % 16, o = .. + 16 j + 4 (l / 16)
+  const auto rsw = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(g.sw), static_cast<int16_t>(0), g.O * 4, kBufferWord3);
+  f32x4_t sw[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sw[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsw, 4 * (o0 + 16 * (NJ * wn + j) + 4 * kb + e), 0, 0));
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int t = t0 + 16 * (NI * wm + i) + r16;
+    if (t >= g.T) continue;
+    const float sa = g.sa[t];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) put4<OUT>(g, t, o0 + 16 * (NJ * wn + j) + 4 * kb, acc[i][j], sa, sw[j]);
+  }
+}
+
+// ---- rows ---------------------------------------------------------------------------------------
+
+constexpr int kRowWaves = 8;
+constexpr int kRowAhead = 4;  // 128-byte pieces of W on their way
+
+// 16 NT rows of A (blockIdx.y) by 16 NO channels
+template <int NT, int NO, int OUT>
+__global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(Gemm g) {
+  __shared__ __align__(16) i32x4_t s_acc[kRowWaves][NT * NO][64];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, kb = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H = g.H, o0 = 16 * NO * blockIdx.x, t0 = 16 * NT * blockIdx.y;
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.w) + static_cast<int64_t>(o0) * H, static_cast<int16_t>(0),
+                                                    min(16 * NO, g.O - o0) * H, kBufferWord3);
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a) + static_cast<int64_t>(t0) * H, static_cast<int16_t>(0),
+                                                    min(16 * NT, g.T - t0) * H, kBufferWord3);
+  i32x4_t acc[NT][NO];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NO; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  struct Piece {
+    u32x4_t w[NO][2], a[NT][2];
+  } p[kRowAhead];
+  auto load = [&](Piece& x, int k) __attribute__((always_inline)) {  // bytes k .. k + 127 of the rows
+    const int at = k + 32 * kb;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t past = at + 16 * h < H ? 0u : kOut;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) x.w[j][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, static_cast<uint32_t>((16 * j + r16) * H + at + 16 * h) | past, 0, 0);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) x.a[i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, static_cast<uint32_t>((16 * i + r16) * H + at + 16 * h) | past, 0, 0);
+    }
+  };
+  constexpr int kStep = kRowWaves * kStage;
+  const int k0 = kStage * wv;
+#pragma unroll
+  for (int q = 0; q < kRowAhead; ++q) load(p[q], k0 + q * kStep);  // (past the end: zeros, and no memory is touched)
+  for (int k = k0; k < H; k += kRowAhead * kStep) {
+#pragma unroll
+    for (int q = 0; q < kRowAhead; ++q) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, p[q].w[j][h]), __builtin_bit_cast(i32x4_t, p[q].a[i][h]),
+                                                              acc[i][j], 0, 0, 0);
+      load(p[q], k + (kRowAhead + q) * kStep);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NO; ++j) s_acc[wv][i * NO + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int x = threadIdx.x; x < NT * NO * 64; x += 64 * kRowWaves) {
+    const int ij = x >> 6, l = x & 63;
+    i32x4_t sum = s_acc[0][ij][l];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) sum += s_acc[w][ij][l];
+    const int t = t0 + 16 * (ij / NO) + (l & 15), o = o0 + 16 * (ij % NO) + 4 * (l >> 4);
+    if (t >= g.T || o >= g.O) continue;
+    f32x4_t sw;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sw[e] = g.sw[min(o + e, g.O - 1)];
+    put4<OUT>(g, t, o, sum, g.sa[t], sw);
+  }
+}
+
+template <int OUT>
+hipError_t go(const Gemm& g, hipStream_t s) {
+  auto tiles = [&](int bt, int bo) { return static_cast<int64_t>(ceil_div(g.T, bt)) * ceil_div(g.O, bo); };
+  if (g.T <= 64) {
+    const uint32_t one = static_cast<uint32_t>(ceil_div(g.O, 16)), two = static_cast<uint32_t>(ceil_div(g.O, 32));
+    if (g.T <= 16) rows_kernel<1, 1, OUT><<<one, 64 * kRowWaves, 0, s>>>(g);
+    else if (g.T <= 32) rows_kernel<2, 2, OUT><<<two, 64 * kRowWaves, 0, s>>>(g);
+    else rows_kernel<4, 2, OUT><<<two, 64 * kRowWaves, 0, s>>>(g);
+  } else if (tiles(256, 256) >= 256) {
+    tile_kernel<256, 256, 2, 4, OUT><<<static_cast<uint32_t>(tiles(256, 256)), 512, 0, s>>>(g, static_cast<int32_t>(ceil_div(g.T, 256)), static_cast<int32_t>(ceil_div(g.O, 256)));
+  } else {
+    tile_kernel<128, 128, 2, 2, OUT><<<static_cast<uint32_t>(tiles(128, 128)), 256, 0, s>>>(g, static_cast<int32_t>(ceil_div(g.T, 128)), static_cast<int32_t>(ceil_div(g.O, 128)));
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_gemm(int64_t T, int64_t O, int64_t H, const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, void* c,
+                            int32_t out, hipStream_t s) {
+  const uintptr_t al = out == kOutF32 ? 16 : 8;
+  const Gemm g{a, w, sa, sw, c, static_cast<int32_t>(T), static_cast<int32_t>(O), static_cast<int32_t>(H),
+               O % 4 == 0 && reinterpret_cast<uintptr_t>(c) % al == 0};
+  return out == kOutF32 ? go<kOutF32>(g, s) : out == kOutF16 ? go<kOutF16>(g, s) : go<kOutBF16>(g, s);
+}
+
+}  // namespace fq

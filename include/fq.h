@@ -211,6 +211,22 @@ fq_status fq_dequant(const fq_tensor* codes, const fq_tensor* scale, const fq_te
 fq_status fq_int4_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
                        const fq_tensor* c, hipStream_t stream);
 
+/* ---- int8 consumer GEMM ------------------------------------------------------------
+ * The same product of the per-token int8 codes (out INT8 [K, M, N] viewed as [K, M*N]: T = K, H = M*N) with their
+ * FLOAT32 [K] quantScale:
+ *     C[t, o] = fl32( fl32(acc[t, o]) * fl32(a_scale[t] * w_scale[o]) ),   acc[t, o] = sum_h qa[t, h] * qw[o, h]
+ * (exact: int32 accumulation, |acc| <= 2^14 H).
+ *   a        INT8    [T, H]     16 <= H < 2^17, H % 16 == 0
+ *   a_scale  FLOAT32 [T]
+ *   w        INT8    [O, H]
+ *   w_scale  FLOAT32 [O]
+ *   c        FLOAT32 | FLOAT16 | BFLOAT16 [T, O]   (a 16-bit C is the fp32 value rounded to nearest even)
+ * All tensors contiguous device memory owned by the caller; a and w 16-byte aligned, the scales 4-byte; T and O below
+ * 2^26 (either may be 0: nothing to do, and empty tensors may have NULL data), ceilDiv(T, 128) * ceilDiv(O, 128) < 2^23.
+ * Enqueued on `stream` without synchronizing; no workspace; the same inputs give the same bits.  Errors as for fq_int4_gemm. */
+fq_status fq_int8_gemm(const fq_tensor* a, const fq_tensor* a_scale, const fq_tensor* w, const fq_tensor* w_scale,
+                       const fq_tensor* c, hipStream_t stream);
+
 /* ---- MXFP4 consumer GEMM ----------------------------------------------------------------
  * The product that follows the quantizer in a FlatQuant linear layer:
  *     C[t, o] = sum_h value(a[t, h]) * value(w[o, h])
