@@ -2,11 +2,15 @@
 // codes (its INT8 [K, M, N] output viewed as [K, M N]) and their fp32 scales, W int8 weights with one fp32 scale per output
 // channel.  The integer sums are exact in int32 (|sum| <= 2^14 H, H < 2^17), so C is one defined value, rounded once more to a 16-bit C.
 //
-// Tiles (many rows): a workgroup computes a BT x BO tile on v_mfma_i32_16x16x64_i8, 128 bytes of the contraction a stage: the
-// stage's rows of A and W are copied by LDS-DMA into one of two buffers while the other feeds the products, one barrier a
-// stage; chunk c of row r sits at c ^ (r & 7); W is the first operand, so a lane's four results are four consecutive columns
-// of one row; tiles are numbered XCD by XCD in groups of four row bands.
-// Rows (few rows, as in single steps): bound by reading W once.  A workgroup of eight waves has 16 or 32 channels; the waves
+// Tiles: a workgroup computes a BT x BO tile on v_mfma_i32_16x16x64_i8, 128 bytes of the contraction a stage: the stage's rows of
+// A and W are copied by LDS-DMA into one of NB buffers while others feed the products, one barrier a stage; chunk c of row r
+// sits at c ^ (r & 7); W is the first operand, so a lane's four results are four consecutive columns of one row.  A half-stage's
+// fragments are read among the products of the one before (read in front of their own: 64 x 64 tiles 26 us where they now
+// take 19, 100 x 1024 x 8192).  Each XCD takes neighbouring tiles, in groups of four row bands.
+// Bound by the walk over the contraction while the device holds all tiles at once (100 x 1024 x 8192: 19 us, 300 ns a stage of barrier,
+// LDS reads and products); at 8192^3, 441 us (2.49 POP/s, half of the dense int8 peak), by LDS: the reads and copies of a
+// stage take as many cycles as its products.
+// Rows (up to 32, as in single steps): bound by reading W once, 4 x 10240 x 8192 (84 MB) 20.4 us, 4.1 TB/s.  A workgroup of eight waves has 16 or 32 channels; the waves
 // take 128 bytes of the contraction in turn, straight from memory into operand registers (both operands relabel the contraction the
 // same way: lane group kb has bytes 32 kb .. 32 kb + 31 of the 128), and their sums are added up in LDS.
 #include <hip/hip_runtime.h>
@@ -54,21 +58,21 @@ __device__ __forceinline__ void put4(const Gemm& g, int t, int o, i32x4_t acc, f
 
 // ---- tiles ------------------------------------------------------------------------------------
 
-// BT x BO a workgroup, WT x WO waves
-template <int BT, int BO, int WT, int WO, int OUT>
+// BT x BO a workgroup, WT x WO waves, NB buffers
+template <int BT, int BO, int WT, int WO, int NB, int OUT>
 __global__ __launch_bounds__(64 * WT * WO) void tile_kernel(Gemm g, int32_t nT, int32_t nO) {
   constexpr int NW = WT * WO, NI = BT / WT / 16, NJ = BO / WO / 16;
   constexpr int LA = BT / 8 / NW, LW = BO / 8 / NW;  // LDS-DMA loads of a wave and stage: 8 rows each
   constexpr int kStageB = (BT + BO) * kStage;
-  __shared__ __align__(16) uint8_t lds[2][kStageB];
+  __shared__ __align__(16) uint8_t lds[NB][kStageB];
   const lds_u8* const lds_l = (const lds_u8*)lds[0];
   const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int b = blockIdx.x;
-  const int n = nT * nO;
-  if ((n & 7) == 0) b = (b & 7) * (n >> 3) + (b >> 3);  // dispatch goes round-robin over the 8 XCDs
+  // dispatch goes round-robin over the 8 XCDs: each takes neighbouring tiles, which share rows of A and W in its L2
+  const int n = nT * nO, b = static_cast<int>(blockIdx.x & 7) * ((n + 7) / 8) + static_cast<int>(blockIdx.x >> 3);
+  if (b >= n) return;
   const int grp = b / (kGroup * nO), gfirst = grp * kGroup, gsz = min(nT - gfirst, kGroup);
   const int rem = b - grp * kGroup * nO;
   const int t0 = (gfirst + rem % gsz) * BT, o0 = (rem / gsz) * BO;
@@ -99,35 +103,57 @@ __global__ __launch_bounds__(64 * WT * WO) void tile_kernel(Gemm g, int32_t nT, 
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
 
-  // 64 bytes of the contraction: W's fragments, then A's, each read while the products of the one before run
-  auto half = [&](int buf, int h) __attribute__((always_inline)) {
-    const lds_u8* const st = lds_l + buf * kStageB + 16 * ((4 * h + kb) ^ (r16 & 7));
-    const lds_u8* const ap = st + (16 * NI * wm + r16) * kStage;
-    const lds_u8* const wp = st + (BT + 16 * NJ * wn + r16) * kStage;
-    auto read = [](const lds_u8* p) __attribute__((always_inline)) { return *(const __attribute__((address_space(3))) i32x4_t*)p; };
-    i32x4_t wf[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) wf[j] = read(wp + 16 * j * kStage);
-    i32x4_t af = read(ap);
+  // the fragments of 64 bytes of the contraction, and their products
+  struct Half {
+    i32x4_t w[NJ], a[NI];
+  } x, y;
+  auto place = [&](int buf, int h) __attribute__((always_inline)) { return lds_l + buf * kStageB + 16 * ((4 * h + kb) ^ (r16 & 7)); };
+  auto read_w = [&](Half& f, const lds_u8* st, int j) __attribute__((always_inline)) {
+    f.w[j] = *(const __attribute__((address_space(3))) i32x4_t*)(st + (BT + 16 * (NJ * wn + j) + r16) * kStage);
+  };
+  auto read_a = [&](Half& f, const lds_u8* st, int i) __attribute__((always_inline)) {
+    f.a[i] = *(const __attribute__((address_space(3))) i32x4_t*)(st + (16 * (NI * wm + i) + r16) * kStage);
+  };
+  // the products of f, and the reads of `next` (from `st`) spread among them
+  auto phase = [&](const Half& f, Half& next, const lds_u8* st) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      i32x4_t next = af;
-      if (i + 1 < NI) next = read(ap + 16 * (i + 1) * kStage);
+#pragma unroll
+      for (int j = i * NJ / NI; j < (i + 1) * NJ / NI; ++j) read_w(next, st, j);
+      read_a(next, st, i);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], af, acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[j], f.a[i], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      af = next;
     }
   };
-
+  // A stage's loads have landed when at most those of the `behind` stages after it are outstanding; its second half's
+  // fragments are read under the first one's products, the next stage's first ones under the second one's.  So a stage's
+  // buffer is free, all waves' reads of it done, at the barrier in its middle.
   const int nkt = (H + kStage - 1) / kStage;
-  dma(0, 0);
-  for (int kt = 0; kt < nkt; ++kt) {
+  auto landed = [&](auto behind) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "i"(decltype(behind)::value * (LA + LW)) : "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+    if (i < nkt) dma(i, i);
+  if (nkt >= NB)
+    landed(std::integral_constant<int, NB - 1>{});
+  else
     tile_barrier();
-    if (kt + 1 < nkt) dma((kt + 1) & 1, kt + 1);
-    half(kt & 1, 0);
-    if (kStage * kt + 64 < H) half(kt & 1, 1);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) read_w(x, place(0, 0), j);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) read_a(x, place(0, 0), i);
+  for (int kt = 0, buf = 0; kt < nkt; ++kt) {
+    phase(x, y, place(buf, 1));
+    if (kt + NB <= nkt)
+      landed(std::integral_constant<int, NB - 2>{});
+    else
+      tile_barrier();
+    if (kt + NB < nkt) dma(buf, kt + NB);
+    buf = buf + 1 == NB ? 0 : buf + 1;
+    phase(y, x, place(buf, 0));  // (behind the last stage: of no use)
   }
 
   // lane l holds C[t][o .. o + 3] with t = .. + 16 i + l % 16, o = .. + 16 j + 4 (l / 16)
@@ -151,7 +177,7 @@ __global__ __launch_bounds__(64 * WT * WO) void tile_kernel(Gemm g, int32_t nT, 
 // ---- rows ---------------------------------------------------------------------------------------
 
 constexpr int kRowWaves = 8;
-constexpr int kRowAhead = 4;  // 128-byte pieces of W on their way
+constexpr int kRowAhead = 4;  // 128-byte pieces of W on their way (6 and 8: 24.5 us where 4 takes 20.4; four waves with 8: 21.1)
 
 // 16 NT rows of A (blockIdx.y) by 16 NO channels
 template <int NT, int NO, int OUT>
@@ -220,18 +246,32 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(Gemm g) {
   }
 }
 
+// The smallest tile whose number the device still holds at once (two a CU) has the shortest walk; more of them than that
+// read A and W too often.  us of 64 x 64, 128 x 64, 128 x 128, 256 x 256:
+//   100 x 8192 x 8192   21.2  31.7  48.5  86.7      1024 x 8192 x 8192   119  97.9  86.7  96.2
+//   200 x 8192 x 8192   28.9  35.2  49.9  89.8      2048 x 4096 x 4096  60.7  51.6  44.8  53.3
+//   333 x 8200 x 4112   39.4  30.6  30.4  55.9      2048 x 8192 x 1024  43.4  36.3  31.0  25.1
+//   512 x 8192 x 8192   59.8  50.8  56.5  93.5      4096 x 4096 x 4096   122  99.1  88.3  62.6
+// Up to 32 rows without tiles: 20 x 8192 x 8192 20.2 us; 50 rows took 26.8 that way, in 64 x 64 tiles 19.9.
 template <int OUT>
 hipError_t go(const Gemm& g, hipStream_t s) {
   auto tiles = [&](int bt, int bo) { return static_cast<int64_t>(ceil_div(g.T, bt)) * ceil_div(g.O, bo); };
-  if (g.T <= 64) {
-    const uint32_t one = static_cast<uint32_t>(ceil_div(g.O, 16)), two = static_cast<uint32_t>(ceil_div(g.O, 32));
-    if (g.T <= 16) rows_kernel<1, 1, OUT><<<one, 64 * kRowWaves, 0, s>>>(g);
-    else if (g.T <= 32) rows_kernel<2, 2, OUT><<<two, 64 * kRowWaves, 0, s>>>(g);
-    else rows_kernel<4, 2, OUT><<<two, 64 * kRowWaves, 0, s>>>(g);
-  } else if (tiles(256, 256) >= 256) {
-    tile_kernel<256, 256, 2, 4, OUT><<<static_cast<uint32_t>(tiles(256, 256)), 512, 0, s>>>(g, static_cast<int32_t>(ceil_div(g.T, 256)), static_cast<int32_t>(ceil_div(g.O, 256)));
+  auto run = [&](auto bt, auto bo, auto wo, auto nb) {
+    constexpr int BT = decltype(bt)::value, BO = decltype(bo)::value, WO = decltype(wo)::value, NB = decltype(nb)::value;
+    tile_kernel<BT, BO, 2, WO, NB, OUT><<<static_cast<uint32_t>(8 * ceil_div(tiles(BT, BO), 8)), 128 * WO, 0, s>>>(
+        g, static_cast<int32_t>(ceil_div(g.T, BT)), static_cast<int32_t>(ceil_div(g.O, BO)));
+  };
+  if (g.T <= 32) {
+    if (g.T <= 16) rows_kernel<1, 1, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 16)), 64 * kRowWaves, 0, s>>>(g);
+    else rows_kernel<2, 2, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 32)), 64 * kRowWaves, 0, s>>>(g);
+  } else if (tiles(64, 64) <= 512) {
+    run(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+  } else if (tiles(128, 64) <= 512) {
+    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{});
+  } else if (tiles(128, 128) <= 512) {
+    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
   } else {
-    tile_kernel<128, 128, 2, 2, OUT><<<static_cast<uint32_t>(tiles(128, 128)), 256, 0, s>>>(g, static_cast<int32_t>(ceil_div(g.T, 128)), static_cast<int32_t>(ceil_div(g.O, 128)));
+    run(std::integral_constant<int, 256>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   }
   return hipGetLastError();
 }
