@@ -12,7 +12,10 @@ constexpr int64_t kPlaces = 5;              // key tiles that a segment's places
 // Workgroups of a launch: two a CU, one of heads above 128 (their LDS and registers).  A run of fewer than kLeast tiles
 // costs more in parts to join than it gains.
 constexpr int64_t kLeast = 8;
-constexpr int64_t kShort = 12;  // key tiles of the longest walk up to which every row tile is one workgroup's
+// Key tiles of the longest walk up to which every row tile is one workgroup's, without parts and a second launch.  us with 12, 24 and
+// 48: 32 single tokens with a window of 1024 46.9, 31.6, 31.6; four 23.8, 21.5, 21.8; 32 of 300 to 1500 42.3, 36.5, 36.4; 128 of
+// them in int4, 64 heads 92.8, 76.4, 77.0.
+constexpr int64_t kShort = 24;
 
 // The parts of a call that its workspace depends on, into a's sizes.
 bool chunk_sizes(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table, const fq_tensor* cu_q, int32_t window,
