@@ -116,6 +116,15 @@ def test_many_sequences(mode):
         _run(sizes, 4, 2, 64, 16, mode, "f16", window, sinks, seed=4)
 
 
+@pytest.mark.parametrize("mode", ["same", "int8", "fp4"])
+def test_many_sequences_dealt(mode):
+    """The same with long ones among them, so that the work is dealt in runs over many short segments and parts of long ones."""
+    sizes = [((i * i) % 4, (37 * i) % 400) for i in range(70)] + [(2, 3000)] + [((i * i) % 7, (41 * i) % 300) for i in range(70)] + [(30, 1800)]
+    for window, sinks in ((0, 0), (1700, 5)):
+        say(f"[gpu] many dealt {mode} window={window}")
+        _run(sizes, 4, 2, 64, 16, mode, "f16", window, sinks, seed=21)
+
+
 @pytest.mark.parametrize("Hq,H", [(128, 1), (130, 1), (300, 1), (258, 2)])
 def test_many_heads_on_one(Hq, H):
     """Up to 128 heads of a cache head are rows of one tile; more take several."""
