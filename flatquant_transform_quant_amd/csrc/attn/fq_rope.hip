@@ -10,6 +10,11 @@
 // So the angles, the only expensive part, are formed once a token and lane: the product with the position in fp64 (exact
 // below 2^29), its fraction of a turn in fp64, sine and cosine of that in fp32.  The other element of a pair is R/2 away
 // in another lane; its lane reads it too (a second request to lines that the row's own loads bring into the cache).
+//
+// Bound by HBM: 16384 tokens of 72 heads of 128 in f16 (604 MB there and back) take 130 us, 4.6 TB/s (of 5.2 that a copy reaches);
+// pairs side by side, which need no second request, 122.  A token's weights times its cosines and sines are formed once, not once a head (146 us,
+// so 141).  Rows go out past the caches, which they only fill: 141 us, so 130; 2048 tokens of 40 heads 18.6, so 15.7.  More
+// heads of a token side by side in a wave (its rows lie one behind the other) cost as many more angles: 142 to 174 us.
 #include <hip/hip_runtime.h>
 
 #include "fq_kv_store.h"
@@ -19,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kEnough = 512;  // workgroups of a launch that need no more spreading
-constexpr int kInFlight = 2;  // heads whose rows are loaded before the first is used
+constexpr int kInFlight = 4;  // heads whose rows are loaded before the first is used
 constexpr int kRows = -1;     // the place of a cache mode: keys go to rows, and there are no values
 
 // Sum over aligned groups of SPAN lanes, in an order that does not depend on the lane.
@@ -49,7 +54,7 @@ __device__ __forceinline__ void weights8(const RopeNorm& n, int e0, int e1, floa
 
 // What a lane's elements have in common over the heads of a token.
 struct Turn {
-  float c[8], s[8];  // y = x c + other s, the sign of the sine included
+  float c[8], s[8];  // y = x c + other s, the sign of the sine included (weights come to these)
   int o0, o1;        // the others' places in the row, of the lower and the upper four; -1: none (not turned)
 };
 
@@ -105,8 +110,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int32_t toke
     }
   }
 
-  // One row: normed where there are weights, and turned.  `other`: the row's elements at o0 and o1, four each.  (An
-  // element that is not turned is left as it is: a zero's sign, and whatever the other one holds.)
+  // One row: normed where there are weights, and turned.  `other`: the row's elements at o0 and o1, four each; w, wo: weights times cosines
+  // and sines.  (An element that is not turned is left as it is: a zero's sign, and whatever the other one holds.)
   auto turned = [&](const RopeNorm& n, const float (&w)[8], const float (&wo)[8], const u32x4_t raw, const u32x4_t other, float (&y)[8])
                     __attribute__((always_inline)) {
     float x[8], o[8];
@@ -124,12 +129,12 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int32_t toke
       const float inv = 1.0f / __builtin_sqrtf(group_sum<LPR>(q) / static_cast<float>(a.D) + a.eps);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] *= inv * w[i];
-        o[i] *= inv * (a.interleaved ? w[i ^ 1] : wo[i]);
+        x[i] *= inv;
+        o[i] *= inv;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = tn.s[i] != 0.0f ? __builtin_fmaf(x[i], tn.c[i], o[i] * tn.s[i]) : x[i] * tn.c[i];
+    for (int i = 0; i < 8; ++i) y[i] = tn.s[i] != 0.0f ? __builtin_fmaf(x[i], w[i], o[i] * wo[i]) : x[i] * w[i];
   };
 
   // The heads of one side, kInFlight rows at a time; sink(head, values, there).
@@ -139,7 +144,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int32_t toke
     for (int i = 0; i < 8; ++i) w[i] = wo[i] = 1.0f;
     if (n.w && mine) {
       weights8(n, 8 * ch, 8 * ch + 4, w);
-      weights8(n, max(tn.o0, 0), max(tn.o1, 0), wo);
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wo[i] = w[i ^ 1];
+      } else {
+        weights8(n, max(tn.o0, 0), max(tn.o1, 0), wo);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] *= tn.c[i];
+      wo[i] *= tn.s[i];
     }
     const uint16_t* src = in.p + (t * in.row + h0 * in.head);
     const int64_t step = dh * in.head;
@@ -176,8 +191,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int32_t toke
   auto to_rows = [&](const Rows16& out) __attribute__((always_inline)) {
     return [&, out](int h, const float (&y)[8], bool there) __attribute__((always_inline)) {
       if (there)
-        *reinterpret_cast<u32x4_t*>(out.p + (t * out.row + h * out.head + 8 * ch)) =
-            u32x4_t{round16x2<DT>(y[0], y[1]), round16x2<DT>(y[2], y[3]), round16x2<DT>(y[4], y[5]), round16x2<DT>(y[6], y[7])};
+        __builtin_nontemporal_store(u32x4_t{round16x2<DT>(y[0], y[1]), round16x2<DT>(y[2], y[3]), round16x2<DT>(y[4], y[5]), round16x2<DT>(y[6], y[7])},
+                                    reinterpret_cast<u32x4_t*>(out.p + (t * out.row + h * out.head + 8 * ch)));
     };
   };
 
