@@ -5,11 +5,11 @@
 // Tiles: a workgroup computes a BT x BO tile on v_mfma_i32_16x16x64_i8, 128 bytes of the contraction a stage: the stage's rows of
 // A and W are copied by LDS-DMA into one of NB buffers while others feed the products, one barrier a stage; chunk c of row r
 // sits at c ^ (r & 7); W is the first operand, so a lane's four results are four consecutive columns of one row.  A half-stage's
-// fragments are read among the products of the one before (read in front of their own: 64 x 64 tiles 26 us where they now
-// take 19, 100 x 1024 x 8192).  Each XCD takes neighbouring tiles, in groups of four row bands.
-// Bound by the walk over the contraction while the device holds all tiles at once (100 x 1024 x 8192: 19 us, 300 ns a stage of barrier,
-// LDS reads and products); at 8192^3, 441 us (2.49 POP/s, half of the dense int8 peak), by LDS: the reads and copies of a
-// stage take as many cycles as its products.
+// fragments are read among the products of the one before (read in front of their own: 64 x 64 tiles 26 us where they then
+// took 19, 100 x 1024 x 8192).  Each XCD takes neighbouring tiles, in groups of four row bands.
+// Bound by the walk over the contraction while the device holds all tiles at once (100 x 1024 x 8192: 17.5 us, 270 ns a stage of barrier,
+// LDS reads and products); at 8192^3, 442 us (2.49 POP/s, half of the dense int8 peak, matrix cores 58% busy), by LDS: the reads and
+// copies of a stage take as many cycles as its products.
 // Rows (up to 32, as in single steps): bound by reading W once, 4 x 10240 x 8192 (84 MB) 20.4 us, 4.1 TB/s.  A workgroup of eight waves has 16 or 32 channels; the waves
 // take 128 bytes of the contraction in turn, straight from memory into operand registers (both operands relabel the contraction the
 // same way: lane group kb has bytes 32 kb .. 32 kb + 31 of the 128), and their sums are added up in LDS.
@@ -246,32 +246,33 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(Gemm g) {
   }
 }
 
-// The smallest tile whose number the device still holds at once (two a CU) has the shortest walk; more of them than that
-// read A and W too often.  us of 64 x 64, 128 x 64, 128 x 128, 256 x 256:
-//   100 x 8192 x 8192   21.2  31.7  48.5  86.7      1024 x 8192 x 8192   119  97.9  86.7  96.2
-//   200 x 8192 x 8192   28.9  35.2  49.9  89.8      2048 x 4096 x 4096  60.7  51.6  44.8  53.3
-//   333 x 8200 x 4112   39.4  30.6  30.4  55.9      2048 x 8192 x 1024  43.4  36.3  31.0  25.1
-//   512 x 8192 x 8192   59.8  50.8  56.5  93.5      4096 x 4096 x 4096   122  99.1  88.3  62.6
-// Up to 32 rows without tiles: 20 x 8192 x 8192 20.2 us; 50 rows took 26.8 that way, in 64 x 64 tiles 19.9.
+// The smallest tile whose number the device still holds at once has the shortest walk (64 x 64: two a CU, the others one); more of
+// them than that read A and W too often.  us of 64 x 64, 128 x 128, 256 x 256, with eight waves:
+//   200 x 8192 x 8192   29.2  40.8  89.8      1024 x 8192 x 8192    119  72.7  96.2
+//   333 x 8200 x 4112   39.4  24.5  55.9      2048 x 4096 x 4096   60.7  39.3  53.3
+//   320 x 8192 x 4096   27.2  21.8            4096 x 4096 x 4096    122  88.3  62.6
+// and 128 x 256, where it fits: 1024 x 8192 x 8192 70.4, 2048 x 4096 x 4096 38.5.  Four waves a workgroup hide less of a stage's
+// waits: 100 x 1024 x 8192 19.3 (eight: 17.5), 128 x 4096 x 4096 11.6 (10.8), 512 x 8192 x 8192 53.6 (42.5).
+// Up to 32 rows without tiles: 20 x 8192 x 8192 20.2 us; 50 rows took 26.8 that way, in 64 x 64 tiles 18.6.
 template <int OUT>
 hipError_t go(const Gemm& g, hipStream_t s) {
   auto tiles = [&](int bt, int bo) { return static_cast<int64_t>(ceil_div(g.T, bt)) * ceil_div(g.O, bo); };
-  auto run = [&](auto bt, auto bo, auto wo, auto nb) {
-    constexpr int BT = decltype(bt)::value, BO = decltype(bo)::value, WO = decltype(wo)::value, NB = decltype(nb)::value;
-    tile_kernel<BT, BO, 2, WO, NB, OUT><<<static_cast<uint32_t>(8 * ceil_div(tiles(BT, BO), 8)), 128 * WO, 0, s>>>(
+  auto run = [&](auto bt, auto bo, auto nb) {
+    constexpr int BT = decltype(bt)::value, BO = decltype(bo)::value, NB = decltype(nb)::value;
+    tile_kernel<BT, BO, 2, 4, NB, OUT><<<static_cast<uint32_t>(8 * ceil_div(tiles(BT, BO), 8)), 512, 0, s>>>(
         g, static_cast<int32_t>(ceil_div(g.T, BT)), static_cast<int32_t>(ceil_div(g.O, BO)));
   };
   if (g.T <= 32) {
     if (g.T <= 16) rows_kernel<1, 1, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 16)), 64 * kRowWaves, 0, s>>>(g);
     else rows_kernel<2, 2, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 32)), 64 * kRowWaves, 0, s>>>(g);
   } else if (tiles(64, 64) <= 512) {
-    run(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
-  } else if (tiles(128, 64) <= 512) {
-    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{});
-  } else if (tiles(128, 128) <= 512) {
-    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+    run(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  } else if (tiles(128, 128) <= 256) {
+    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 3>{});
+  } else if (tiles(128, 256) <= 256) {
+    run(std::integral_constant<int, 128>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
   } else {
-    run(std::integral_constant<int, 256>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    run(std::integral_constant<int, 256>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
   }
   return hipGetLastError();
 }

@@ -47,6 +47,12 @@ def test_large(T, O, H):
     check(T, O, H, torch.bfloat16, 1)
 
 
+@pytest.mark.parametrize("T,O,H", [(300, 9001, 80), (300, 9000, 400), (257, 10900, 1040), (1000, 5000, 144), (1001, 4999, 1168), (200, 60000, 272)])
+def test_middle_tiles(T, O, H):
+    """Tiles of 128 by 128 and by 256, walks shorter and longer than their buffers."""
+    check(T, O, H, torch.bfloat16, 2)
+
+
 @pytest.mark.parametrize("T", [1, 20, 50, 100, 2000])
 def test_rows_do_not_depend_on_their_number(T):
     """The same row gives the same bits whatever kernel the number of rows chooses."""
