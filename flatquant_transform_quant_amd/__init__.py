@@ -784,10 +784,16 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float = 0
     return out
 
 
+def _int32(n) -> int:
+    """n, held to what an int32 can say of a length (ctypes keeps the low bits of any other)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 def attn_chunk_workspace_size(q, cache: KVCache, block_table, cu_q, window: int = 0, sinks: int = 0) -> int:
     size = ctypes.c_uint64(0)
     d = _Descs(q, block_table, cu_q)
-    st = lib.fq_attn_chunk_get_workspace_size(d.ptrs[0], cache._args()[0], d.ptrs[1], d.ptrs[2], window, sinks, ctypes.byref(size))
+    st = lib.fq_attn_chunk_get_workspace_size(d.ptrs[0], cache._args()[0], d.ptrs[1], d.ptrs[2], _int32(window), _int32(sinks),
+                                                ctypes.byref(size))
     if st != FQ_SUCCESS:
         raise FqError(st, "fq_attn_chunk_get_workspace_size")
     return size.value
@@ -800,6 +806,7 @@ def attn_chunk(q, cache: KVCache, block_table, cu_q, lengths, window: int = 0, s
     own position; with ``window`` only the last ``window`` of them and the first ``sinks`` tokens.  scale 0 means 1/sqrt(D).
     ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least attn_chunk_workspace_size) may be passed to reuse one."""
     torch = _torch()
+    window, sinks = _int32(window), _int32(sinks)
     _same_gpu(stream, cache.k, q, block_table, cu_q, lengths, out, lse, workspace)
     if out is None:
         make = lambda: torch.empty_like(q, memory_format=torch.contiguous_format)  # noqa: E731

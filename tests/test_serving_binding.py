@@ -73,3 +73,19 @@ def test_a_workspace_is_contiguous(streams, launches):  # noqa: F811
     assert not launches
     fq.attn_chunk(q, cache, table, cu, lens, workspace=torch.zeros(size, dtype=torch.uint8))
     assert launches == ["fq_attn_chunk"]
+
+
+@pytest.mark.parametrize("window,sinks,same", [(2 ** 32 + 5, 0, (0, 0)), (2 ** 40, 2 ** 32, (0, 0)), (100, 2 ** 32 + 1, (100, 2 ** 31 - 1))])
+def test_windows_past_32_bits(window, sinks, same):
+    """A window beyond every length is none; its low bits are not taken for a short one."""
+    cache = fq.empty_kv_cache(4, 2, 16, 64, "int8", "cpu")
+    at = _b16(3, 4, 64), cache, _i32(1, 4096), torch.tensor([0, 3], dtype=torch.int32)
+    want = fq.attn_chunk_workspace_size(*at, *same)
+    assert want > 0 and fq.attn_chunk_workspace_size(*at, window, sinks) == want
+
+
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (-2 ** 32 + 5, 0), (100, -2 ** 32 + 5)])
+def test_lengths_below_zero_are_refused(window, sinks):
+    cache = fq.empty_kv_cache(4, 2, 16, 64, "int8", "cpu")
+    with pytest.raises(fq.FqError):
+        fq.attn_chunk_workspace_size(_b16(3, 4, 64), cache, _i32(1, 4096), torch.tensor([0, 3], dtype=torch.int32), window, sinks)
