@@ -18,7 +18,10 @@ Output storage in torch:
     quantScale ``torch.float32`` [K].
 
 A paged key-value cache in the same formats is a :class:`KVCache` (``empty_kv_cache`` allocates
-one); ``kv_write``, ``kv_read``, ``attn_decode`` and ``attn_prefill`` are the calls on it.
+one); ``kv_write``, ``kv_read``, ``attn_decode`` (one new token per sequence), ``attn_prefill`` (packed prompts) and
+``attn_chunk`` (any number of new tokens per sequence, with a window) are the calls on it.  ``qk_rope`` normalizes and
+rotates queries and keys, ``kv_append`` does that and writes keys and values to the cache.  ``int4_gemm``, ``mx_gemm`` and
+``int8_gemm`` multiply codes.
 
 Streams: a call runs on the current stream, or on ``stream``.  Results and workspaces that a call allocates
 come from that stream's memory; another stream reads a result after waiting for it.  Tensors that the caller

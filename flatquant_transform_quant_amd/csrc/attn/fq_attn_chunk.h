@@ -4,14 +4,16 @@
 // among its lengths[b] tokens.  Row i sees the keys up to its own position, with a window only the last W of them and
 // the first S: o = sum_j p_j v_j, p = softmax over the visible keys of scale * <q, k_j>.
 //
-// A workgroup of four waves takes 128 query rows, 32 a wave: the g query heads of one cache head for 128 / g
-// neighbouring tokens (a cached byte is read once for all of them), and walks the keys in tiles of 64 as the prompt
-// kernel does: two LDS buffers, S^T = K Q^T and O^T = V^T P^T with 32 x 32 x 16 products, a lane owning one row's
-// statistics, the maximum moved only when a score passes m + 8 in base-2 units.  LDS layouts as there.
-// A tile's keys lie in pages of 16 tokens at least: each wave brings the 16 rows that are one page's (16 bits by LDS-DMA).
+// A workgroup of four waves takes a row tile: the g query heads of one cache head for neighbouring tokens (a cached byte is
+// read once for all of them), 128, 64 or 32 rows, the smallest that the mean rows of a sequence and cache head fit.  With 128 a wave has
+// 32 rows; with 64 waves 2 and 3 have the rows of 0 and 1 and the other half of the keys; with 32 each wave has all rows and keys of its
+// own, in LDS of its own without barriers (us in tiles of 128: 24 sequences of 5 drafts, 40 rows, over int8 265, now 122; see kShort for
+// single tokens).  It walks the keys in tiles of 64 as the prompt kernel does: two LDS buffers, S^T = K Q^T and O^T = V^T P^T with
+// 32 x 32 x 16 products, a lane owning one row's statistics, the maximum moved only when a score passes m + 8 in base-2 units.  LDS
+// layouts as there.  A tile's keys lie in pages of 16 tokens at least: each wave brings the 16 rows that are one page's (16 bits by LDS-DMA).
 //
 // Low-bit formats: the codes go through registers, are widened to f16 numbers there, exactly, and written to LDS;
-// a tile's bytes are widened once for all 128 rows.  Widened: int8 and int4 the code times 2^-9, E4M3 the code, E2M1 the code
+// a tile's bytes are widened once for all of its rows.  Widened: int8 and int4 the code times 2^-9, E4M3 the code, E2M1 the code
 // times its group's power of two over the row's largest, times 2^13 (a group more than 2^26 below the largest of its
 // row loses bits).  So every format has one factor a row: a key's multiplies its scores, a value's its weights, both in fp32 out of
 // LDS.  A bf16 q is brought to f16 by a power of two a row (28 binades below its largest element keep all bits).
@@ -23,7 +25,12 @@
 // the grid in equal runs.  A segment's place in that order has a closed form in its tile number (its walk's
 // length is linear in it, up to the window), so a run finds its first segment by a scan over the sequences and a
 // bisection.  A run that has a segment in part leaves its sums in the workspace, at most two such parts a run,
-// and a second launch joins them in order.
+// and a second launch joins them in order.  (Cuts moved to a segment's edge where that is near save few parts and cost as much: no gain.)
+//
+// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 322 us, 0.75 PFLOP/s, matrix cores 34% and
+// vector unit 42% busy, one after the other in a wave, two waves a SIMD (a tile's scalar instructions, 60 of them taken out for a trial,
+// do not count); 5 chunks of 1024 over int4, 582 us, 0.63 PFLOP/s: widening and softmax, vector unit 50%; 24 x 5 drafts over up to 16384
+// int8 tokens, 112 us, 2.9 TB/s: vector unit 57%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -418,7 +425,7 @@ __device__ __forceinline__ int64_t row_at(const ChunkArgs& a, int hk, int k) {
 }
 
 // a = acc[D] times f where `need` (the wave's) is not 0.  The compiler copies the 16-register blocks to other registers and back around such a
-// branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 300); so each block has a place
+// branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 315); so each block has a place
 // that the statements ask for, and the branch is inside: nothing is left to copy.  With it the wait states between the products that wrote the block and
 // this read (at most 18), and between this write and the products that read it.
 template <int D>

@@ -400,8 +400,9 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
  * q, out, the cache, block_table, scale, lse FLOAT32 [Tq, Hq] and the workspace as for fq_attn_decode (of the size that
  * fq_attn_chunk_get_workspace_size gives for the same q, cache, table, cu_q, window and sinks; its contents need not be initialised; calls
  * that overlap in time must not share it); 1 <= B <= 65536, Hq <= 65536; reach and Tq below 2^31 - 65536, and
- * (floor(Tq / t) + B) * Hkv * ceilDiv(g, 128) * (ceilDiv(seen, 64) + 5) < 2^31, with t = floor(128 / min(g, 128)) tokens of a row tile
- * and `seen` the keys that such a tile can see (reach + t, or window + t + 126 and the sinks).
+ * (floor(Tq / t) + min(B, Tq)) * Hkv * n * (ceilDiv(seen, 64) + 5) < 2^31, with row tiles of r rows (the first of 32, 64 and 128 that
+ * ceilDiv(Tq, B) * g rows fit, else 128), n = ceilDiv(g, r) of them for a token's heads, t = floor(r / ceilDiv(g, n)) tokens of one, and
+ * `seen` the keys that such a tile can see (reach + t, or window + t + 126 and the sinks).
  * A row that sees nothing (more rows than cached tokens, no page) gives zeros and lse = -infinity.  A token whose
  * table entry is outside the cache is left out.  What a row does not see never reaches it, infinities and NaN included; rows of out past
  * cu_q[B] are not written.  The same inputs give the same bits.
