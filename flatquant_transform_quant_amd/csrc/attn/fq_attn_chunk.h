@@ -27,10 +27,10 @@
 // bisection.  A run that has a segment in part leaves its sums in the workspace, at most two such parts a run,
 // and a second launch joins them in order.  (Cuts moved to a segment's edge where that is near save few parts and cost as much: no gain.)
 //
-// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 322 us, 0.75 PFLOP/s, matrix cores 34% and
-// vector unit 42% busy, one after the other in a wave, two waves a SIMD (a tile's scalar instructions, 60 of them taken out for a trial,
-// do not count); 5 chunks of 1024 over int4, 582 us, 0.63 PFLOP/s: widening and softmax, vector unit 50%; 24 x 5 drafts over up to 16384
-// int8 tokens, 112 us, 2.9 TB/s: vector unit 57%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
+// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 317 us, 0.76 PFLOP/s, matrix cores 35% and
+// vector unit 41% busy, one after the other in a wave, two waves a SIMD (a tile's scalar instructions, 60 of them taken out for a trial,
+// do not count); 5 chunks of 1024 over int4, 582 us, 0.63 PFLOP/s: widening and softmax, vector unit 52%; 24 x 5 drafts over up to 16384
+// int8 tokens, 112 us, 2.9 TB/s: vector unit 44%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
