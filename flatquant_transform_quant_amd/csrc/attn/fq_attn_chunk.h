@@ -27,15 +27,16 @@
 // bisection.  A run that has a segment in part leaves its sums in the workspace, at most two such parts a run,
 // and a second launch joins them in order.  (Cuts moved to a segment's edge where that is near save few parts and cost as much: no gain.)
 //
-// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 317 us, 0.76 PFLOP/s, matrix cores 35% and
-// vector unit 41% busy, one after the other in a wave, two waves a SIMD (a tile's scalar instructions, 60 of them taken out for a trial,
-// do not count); 5 chunks of 1024 over int4, 582 us, 0.63 PFLOP/s: widening and softmax, vector unit 52%; 24 x 5 drafts over up to 16384
-// int8 tokens, 112 us, 2.9 TB/s: vector unit 44%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
+// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 35% and
+// vector unit 41% busy, one after the other in a wave, two waves a SIMD;
+// 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and softmax, vector unit 52%; 24 x 5 drafts over up to 16384
+// int8 tokens, 111 us, 2.9 TB/s: vector unit 44%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fq_attn_tile.h"
 
@@ -423,6 +424,28 @@ __device__ __forceinline__ int rows_at(const Segment& sg, int k) { return __buil
 __device__ __forceinline__ int64_t row_at(const ChunkArgs& a, int hk, int k) {
   return (static_cast<int64_t>(hk) << a.c.page_log) + (k & ((1 << a.c.page_log) - 1));
 }
+
+// The same with the addresses of the 16 rows on both sides and their bytes, so that a tile's LDS-DMA needs no more than to pick a
+// lane's, and starts before the tile's products (formed a tile at a time from arguments read anew, under the first products: document of 16384
+// rows 317 us, so 309; the earlier start alone changes nothing).
+struct PageRows : Pages {
+  uint64_t at[2];
+  int bytes;
+  __device__ __forceinline__ void need(const ChunkArgs& a, const Segment& sg, const Walk& wk, int u, int hk, int rowb) {
+    if (u >= from && u < from + 16) return;
+    Pages::need(a, sg, wk, u);
+    const int lane = threadIdx.x & 63, i = u + (lane >> 2), k = i < wk.n ? wk.tile(i) * kKeys + 16 * (lane & 3) : a.reach;
+    const int64_t pg = max(page, 0), r = row_at(a, hk, k) * rowb;
+    bytes = page < 0 ? 0 : max(0, min(16, sg.s.lk - k)) * rowb;
+    at[0] = reinterpret_cast<uint64_t>(a.c.k.codes) + (pg * a.c.k.page_b + r);
+    at[1] = reinterpret_cast<uint64_t>(a.c.v.codes) + (pg * a.c.v.page_b + r);
+  }
+  __device__ __forceinline__ i32x4_t rows(int u, int sub, int side) const {
+    const int lane = 4 * (u - from) + sub;
+    const uint32_t high = __builtin_amdgcn_readlane(static_cast<int>(at[side] >> 32), lane), low = __builtin_amdgcn_readlane(static_cast<int>(at[side]), lane);
+    return rsrc4(reinterpret_cast<const void*>(static_cast<uint64_t>(high) << 32 | low), static_cast<uint32_t>(__builtin_amdgcn_readlane(bytes, lane)));
+  }
+};
 
 // a = acc[D] times f where `need` (the wave's) is not 0.  The compiler copies the 16-register blocks to other registers and back around such a
 // branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 315); so each block has a place
@@ -814,25 +837,26 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
     const Place pl = place_of_rows(a, sg, wk, lane, 32 * (wv % RB));
     BK bk;
     bk.load_q(a, sg, pl, lane);
-    Pages pages{-1, -(1 << 30), 0};
+    std::conditional_t<kLow, Pages, PageRows> pages{};
+    pages.from = -(1 << 30);
     auto dma = [&](int u, int buf) __attribute__((always_inline)) {
-      pages.need(a, sg, wk, u);
-      const int64_t pg = pages.of(u, wv);
-      const int k = wk.tile(u) * kKeys + 16 * wv;
-      const uint32_t bytes = pg < 0 ? 0u : static_cast<uint32_t>(rows_at(sg, k) * rowb);
-      const int64_t at = max(pg, int64_t(0)), r = row_at(a, hk, k) * rowb;
-      const i32x4_t rk = rsrc4(cc.k.codes + (at * cc.k.page_b + r), bytes), rv = rsrc4(cc.v.codes + (at * cc.v.page_b + r), bytes);
-      const uint32_t to = lds_addr + buf * (2 * kTileB) + 1024 * NL * wv;
+      if constexpr (!kLow) {
+        pages.need(a, sg, wk, u, hk, rowb);
+        const i32x4_t rk = pages.rows(u, wv, 0), rv = pages.rows(u, wv, 1);
+        const uint32_t to = lds_addr + buf * (2 * kTileB) + 1024 * NL * wv;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) dma16(to + 1024 * i, koff[i], rk);
+        for (int i = 0; i < NL; ++i) dma16(to + 1024 * i, koff[i], rk);
 #pragma unroll
-      for (int i = 0; i < NL; ++i) dma16(to + kTileB + 1024 * i, voff[i], rv);
+        for (int i = 0; i < NL; ++i) dma16(to + kTileB + 1024 * i, voff[i], rv);
+      }
     };
     RW x;
     auto load = [&](int u) __attribute__((always_inline)) {
-      pages.need(a, sg, wk, u);
-      const int k = wk.tile(u) * kKeys + 16 * wv;
-      load_rows(x, cc, lane, 0, pages.of(u, wv), row_at(a, hk, k), rows_at(sg, k), rowb, sb, D);
+      if constexpr (kLow) {
+        pages.need(a, sg, wk, u);
+        const int k = wk.tile(u) * kKeys + 16 * wv;
+        load_rows(x, cc, lane, 0, pages.of(u, wv), row_at(a, hk, k), rows_at(sg, k), rowb, sb, D);
+      }
     };
     auto store = [&](int buf) __attribute__((always_inline)) {
       const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv);
@@ -852,15 +876,14 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
         const int buf = step & 1, k0 = wk.tile(u) * kKeys;
         const uint32_t in = pages.bits(u);  // which 16 keys have a page
         tile_barrier();
-        // the next tile's loads: their addresses are formed while the first score products run
-        auto ahead = [&]() __attribute__((always_inline)) {
-          if (u + 1 < sh.u1) {
-            if constexpr (kLow)
-              load(u + 1);
-            else
-              dma(u + 1, buf ^ 1);
-          }
-        };
+        // the next tile's rows: to LDS, or to registers until this tile is done (loaded under its first products 24 x 5 drafts over int8
+        // take 113 us in place of 111, 5 chunks of 1024 over int4 582 in place of 574)
+        if (u + 1 < sh.u1) {
+          if constexpr (kLow)
+            load(u + 1);
+          else
+            dma(u + 1, buf ^ 1);
+        }
         lds_u8* const kt = lds_l + buf * (2 * kTileB);
         lds_u8* const vt = kt + kTileB;
         if (careful) {
@@ -874,13 +897,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 #pragma unroll
         for (int i = 0; i < (RB == 2 ? 1 : 2 / NB); ++i) {
           const int b = RB == 2 ? wv / 2 : i;
-          if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) {
-            if (i == 0) ahead();
-            continue;
-          }
+          if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) continue;
           const float big = kLow ? fmaxf(s_top[buf][2 * b], s_top[buf][2 * b + 1]) : 0.0f;
           bk.template step<NB>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big,
-                               kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [&]() __attribute__((always_inline)) { if (i == 0) ahead(); });
+                               kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [] {});
         }
         if constexpr (kLow) {
           if (u + 1 < sh.u1) store(buf ^ 1);
@@ -1052,11 +1072,12 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
           big = store_rows(x, lane, lds[wv], lds[wv] + kSideB, s_scale[wv][0], s_scale[wv][1], 0);
           lds_done();  // (other lanes' rows are read below)
         }
-        auto ahead = [&]() __attribute__((always_inline)) {
-          if (!more) return;
-          in = bits(v + kWaves);
-          if constexpr (kLow) load(v + kWaves);
-        };
+        if constexpr (kLow) {
+          if (more) {
+            in = bits(v + kWaves);
+            load(v + kWaves);
+          }
+        }
         if (careful) {
           if constexpr (!kLow) landed(false);
           BK::note_odd(s_odd[wv], pl, a.sinks, k0, now, vt);
@@ -1066,17 +1087,16 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         }
         const bool sees = BK::sees(pl, a.sinks, k0, 32);
         if constexpr (kLow) {
-          if (sees)
-            bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], ahead);
-          else
-            ahead();
+          if (sees) bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
           lds_done();  // (before the next rows take their places)
         } else {
           landed(true);  // (the keys)
           bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
             lds_done();
-            ahead();
-            if (more) dma(v + kWaves, 0);
+            if (more) {
+              in = bits(v + kWaves);
+              dma(v + kWaves, 0);
+            }
             landed(more);  // (the values)
           });
           lds_done();
