@@ -27,10 +27,9 @@
 // bisection.  A run that has a segment in part leaves its sums in the workspace, at most two such parts a run,
 // and a second launch joins them in order.  (Cuts moved to a segment's edge where that is near save few parts and cost as much: no gain.)
 //
-// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 35% and
-// vector unit 41% busy, one after the other in a wave, two waves a SIMD;
-// 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and softmax, vector unit 52%; 24 x 5 drafts over up to 16384
-// int8 tokens, 111 us, 2.9 TB/s: vector unit 44%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
+// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 37% and
+// vector unit 42% busy, one after the other in a wave, two waves a SIMD; 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and
+// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 111 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
