@@ -29,7 +29,8 @@
 //
 // Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 37% and
 // vector unit 42% busy, one after the other in a wave, two waves a SIMD; 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and
-// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 111 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
+// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 111 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's;
+// 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -141,7 +142,8 @@ struct Segment {
   int b, head, tile, at;
 };
 
-// The segment that holds place x (below all of them).
+// The segment that holds place x (below all of them; without row tiles if there is none, as sequences that lie over each other may
+// have more places than an int counts).
 __device__ __forceinline__ Segment segment_at(const ChunkArgs& a, int x) {
   const int lane = threadIdx.x & 63;
   Segment g;
@@ -161,7 +163,7 @@ __device__ __forceinline__ Segment segment_at(const ChunkArgs& a, int x) {
     break;
   }
   const int p = max(1, g.s.places);
-  g.head = min((x - g.at) / p, a.heads - 1);
+  g.head = max(0, min((x - g.at) / p, a.heads - 1));
   g.at += g.head * p;
   int lo = 0, hi = max(1, g.s.tiles);  // the tile's first place is at or before x, that of tile hi behind it
   while (hi - lo > 1) {
@@ -780,6 +782,7 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& a, const Run& r, S
       sg.head = 0;
       do sg.s = seq_of(a, ++sg.b); while (sg.s.tiles == 0 && sg.b < a.B);
       sg.s = lane_seq(sg.s, 0);
+      return sg.s.tiles != 0;
     }
   }
   return true;
@@ -812,6 +815,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
   const Run run = run_of(args_here());
   if (run.last <= run.first) return;
   Segment sg = segment_at(args_here(), run.first);
+  if (sg.s.tiles == 0) return;
 
   // LDS-DMA of 16-bit rows: load i of a wave fills the 16-byte places 64 (NL w + i) + lane of a tile, its 16 rows in all
   uint32_t koff[NL], voff[NL];
@@ -997,6 +1001,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
   const Run run = run_of(args_here());
   if (run.last <= run.first) return;
   Segment sg = segment_at(args_here(), run.first);
+  if (sg.s.tiles == 0) return;
   lds_u8* const kt = (lds_u8*)lds[wv];
   lds_u8* const vt = kt + kSideB;
   const uint32_t k_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt));
@@ -1183,6 +1188,7 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
   if (run + 1 >= static_cast<int>(deal.runs)) return;
   const int end = deal.start(run + 1);
   const Segment sg = segment_at(a, end - 1);
+  if (sg.s.tiles == 0) return;
   const Walk wk = walk_of(a, sg.s, sg.tile);
   const int base = sg.at + kStart;
   if (deal.start(run) > base || end <= base || end - base >= wk.n) return;  // its first tile is not here, or its last one is
@@ -1191,7 +1197,7 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
   const int token = wk.row0 + r / a.tile_heads, hr = r % a.tile_heads, head = hk * a.g + ht * a.tile_heads + hr;
   if (token > wk.row1 || r >= a.tokens * a.tile_heads || hr >= hn || e >= a.c.D) return;
   int parts = 1;  // behind the first
-  while (deal.start(run + parts + 1) - base < wk.n) ++parts;
+  while (run + parts + 1 < static_cast<int>(deal.runs) && deal.start(run + parts + 1) - base < wk.n) ++parts;
   float m = -kInf, l = 0.0f, o[NE];
 #pragma unroll
   for (int j = 0; j < NE; ++j) o[j] = 0.0f;
