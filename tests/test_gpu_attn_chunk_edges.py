@@ -1,0 +1,102 @@
+"""GPU: attention of new tokens over the paged cache where sums are not finite, in every row tile, in walks that one
+workgroup has and in walks that are dealt in parts, against fp64 with the derived elementwise bound of attn_ref.bound."""
+import math
+
+import pytest
+import torch
+
+import flatquant_transform_quant_amd as fq
+from attn_ref import TDT, bound, encode, pack, values
+from gpu_util import DEV, say
+from test_gpu_attn_chunk import _i32, attend, seen_by
+
+pytestmark = pytest.mark.gpu
+
+
+def _cache(k, v, mode, dt, P=16):
+    """A cache of one sequence with its pages in reverse, its table, and what it holds in fp64."""
+    n, H, D = k.shape
+    pages = -(-n // P)
+    slots = (pages - 1 - torch.arange(n) // P) * P + torch.arange(n) % P
+    m = dt if mode == "same" else mode
+    cache = fq.empty_kv_cache(pages, H, P, D, m, "cpu")
+    held = []
+    for x, codes, scales in ((k, cache.k, cache.k_scale), (v, cache.v, cache.v_scale)):
+        p, o = slots // P, slots % P
+        if mode == "same":
+            codes[p, :, o] = x
+            held.append(x.double())
+            continue
+        code, sc = encode(x, mode)
+        codes.view(torch.uint8)[p, :, o] = torch.from_numpy(pack(code, mode))
+        scales[p, :, o] = torch.from_numpy(sc.astype("uint8") if mode == "fp4" else sc)
+        held.append(torch.from_numpy(values(code, sc, mode)))
+    dev = [None if t is None else t.to(DEV) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    return fq.KVCache(m, *dev), torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=DEV)[None], *held
+
+
+# two query heads a cache head: row tiles of 32, 64 and 128
+ROWS = [1, 20, 120]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [200, 2600])
+@pytest.mark.parametrize("r", ROWS)
+def test_infinities_in_16_bits(dt, D, n, r):
+    """Infinities and NaN reach the rows that see them and no other, whatever part of a walk they lie in: one of a value stays an
+    infinity however small its weight, two of other signs are NaN, a NaN key is a row's NaN."""
+    say(f"[gpu] infinities {dt} D={D} keys={n} rows={r}")
+    g = torch.Generator().manual_seed(30)
+    H, G = 4, 2
+    q, k, v = (torch.randn(m, h, D, generator=g).to(TDT[dt]) for m, h in ((r, H * G), (n, H), (n, H)))
+    odd = []  # (key, cache head, element, value)
+    for j, h, d, x in ((n // 3, 0, 7, math.inf), (n - r, 0, D - 1, -math.inf), (n - 1 - r // 2, 1, 9, math.nan), (n // 2, 2, 11, -math.inf),
+                       (n // 5, 3, 33, math.inf), (n - 1 - r // 3, 3, 33, -math.inf)):
+        v[j, h, d] = x
+        odd.append((j, h, d))
+    k[n // 2, 2] = -30.0 * q[r // 2, 2 * G]  # its weight is 0 in 32 bits for that row
+    k[5, 0] = 2.0 * q[r // 2, 0]             # far from the infinities, a row's maximum
+    k[n - 1 - r // 4, 1, 3] = math.nan
+    for window, sinks in ((0, 0), (25, 3), (n - 30, 0)):
+        cache, table, _, _ = _cache(k, v, "same", dt)
+        got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n), window, sinks).cpu().double()
+        seen = seen_by(r, n, window, sinks)
+        clean = [torch.where(torch.isfinite(t), t, 0.0).double() for t in (k, v)]
+        out, _, absv, top, vmax = attend(q.double(), *clean, seen, 1 / math.sqrt(D))
+        extra = torch.zeros(r, H * G, D, dtype=torch.float64)
+        for j, h, d in odd:
+            extra[seen[:, j], G * h:G * h + G, d] += float(v[j, h, d])
+        extra[seen[:, n - 1 - r // 4], G:2 * G] = math.nan
+        fin = extra == 0
+        assert torch.equal(torch.isnan(got), torch.isnan(extra))
+        assert torch.equal(got[~fin & ~extra.isnan()], extra[~fin & ~extra.isnan()])
+        assert ((got - out).abs() <= bound(out, absv, top, vmax, n, D, dt, dt))[fin].all()
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3", "int4", "fp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [200, 2600])
+@pytest.mark.parametrize("r", ROWS)
+def test_rows_that_are_not_finite_in_low_bits(mode, D, n, r):
+    """A cached row (E2M1: a group) that reads back as NaN makes NaN of the rows that see it, and only of those."""
+    say(f"[gpu] not finite {mode} D={D} keys={n} rows={r}")
+    g = torch.Generator().manual_seed(31)
+    H, G = 4, 2
+    q, k, v = (torch.randn(m, h, D, generator=g).bfloat16() for m, h in ((r, H * G), (n, H), (n, H)))
+    k[n - 1 - r // 4, 1, 3], v[n // 3, 0, 40], v[n - 1 - r // 2, 2, 1] = math.nan, math.inf, math.nan
+    second, first = (slice(32, 64), slice(32)) if mode == "fp4" else (slice(D), slice(D))  # what the values' NaN and infinity reach of a row
+    cache, table, _, _ = _cache(k, v, mode, "bf16")
+    clean = _cache(torch.where(torch.isfinite(k), k, 0.0), torch.where(torch.isfinite(v), v, 0.0), mode, "bf16")
+    kk, vv = clean[2:]
+    vv[n // 3, 0, second], vv[n - 1 - r // 2, 2, first] = 0.0, 0.0
+    for window, sinks in ((0, 0), (25, 3), (n - 30, 0)):
+        got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n), window, sinks).cpu().double()
+        seen = seen_by(r, n, window, sinks)
+        bad = torch.zeros(r, H * G, D, dtype=torch.bool)
+        bad[seen[:, n - 1 - r // 4], G:2 * G] = True
+        bad[seen[:, n // 3], :G, second] = True
+        bad[seen[:, n - 1 - r // 2], 2 * G:3 * G, first] = True
+        assert torch.equal(torch.isnan(got), bad)
+        out, _, absv, top, vmax = attend(q.double(), kk, vv, seen, 1 / math.sqrt(D))
+        assert ((got - out).abs() <= bound(out, absv, top, vmax, n, D, "bf16", "f16"))[~bad].all()
