@@ -48,6 +48,8 @@ constexpr int kKeys = 64;           // keys of a tile
 constexpr int kStart = 2;           // tiles that a segment's beginning and end count as when the work is dealt
 constexpr int kAhead = 4;           // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
+// Scores up to this far from 0, in base-2 units, have their maximum taken off within the weights' exponent; its rounding is 2^-5 there.
+constexpr float kFar = 0x1p20f;
 
 template <int MODE>
 constexpr int kCodeBits = MODE == kKv16 ? 16 : (MODE == kKvInt8 || MODE == kKvE4M3) ? 8 : 4;
@@ -498,8 +500,9 @@ struct Block {
   u32x4_t qf[KS];  // the query rows as B operands
   float c;         // base-2 scores' factor
   f32x16_t acc[DB];
-  float m, l;
-  int ref;  // R
+  float m, l;  // m: the maximum as a score, before its factor
+  int ref;     // R
+  int far;     // whether some row's maximum of the wave is beyond kFar
 
   __device__ __forceinline__ void load_q(const ChunkArgs& a, const Segment& sg, const Place& p, int lane) {
     const int hf = lane >> 5, D = PAD ? a.c.D : DP;
@@ -539,6 +542,7 @@ struct Block {
     m = -kInf;
     l = 0.0f;
     ref = kLow ? kLeastRef : 0;
+    far = 0;
   }
 
   // Whether some of the wave's rows see a key of k0 .. k0 + n - 1.
@@ -627,21 +631,31 @@ struct Block {
       ev = static_cast<int>(__float_as_uint(big) >> 23) - 127;
     }
     float f = 1.0f;
-    const int need = __any(top * c > m + kLazy || (kLow && ev > ref + 1));
+    const int need = __any((top - m) * c > kLazy || (kLow && ev > ref + 1));
     if (need) {
-      const float mn = fmaxf(m, half_max(top) * c);
+      const float mn = fmaxf(m, half_max(top));
       int rn = ref;
       if constexpr (kLow) {
         const auto r = __builtin_amdgcn_permlane32_swap(ev, ev, false, false);
         rn = max(ref, min(kMostRef, max(static_cast<int>(r[0]), static_cast<int>(r[1]))));
       }
-      f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f((m + static_cast<float>(ref)) - (mn + static_cast<float>(rn)));
+      f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(m - mn, c, static_cast<float>(ref - rn)));
       m = mn;
       ref = rn;
       l *= f;
+      far = __any(m != -kInf && __builtin_fabsf(m) * c > kFar);
     }
     static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { scale_block<decltype(dc)::value>(acc[decltype(dc)::value], f, need); });
-    const float ms = m == -kInf ? 0.0f : m + static_cast<float>(ref) - kW;
+    const float m0 = m == -kInf ? 0.0f : m;
+    float ms = __builtin_fmaf(m0, c, static_cast<float>(ref) - kW);
+    if (far) {
+      // A maximum that large is off by units as an fp32 number in base 2 (its weight 2^8, infinite or 0 where it has to be 1): it is
+      // taken off as a score.
+      asm volatile("");
+#pragma unroll
+      for (int i = 0; i < 16 * NB; ++i) s[i / 16][i % 16] -= m0;
+      ms = static_cast<float>(ref) - kW;
+    }
     u32x4_t pf[2 * NB];
 #pragma unroll
     for (int g = 0; g < 2 * NB; ++g) {
@@ -730,6 +744,8 @@ struct Block {
       *at = v & ~not_finite16_mask<ODT>(v);
     }
   }
+  // What the parts of a walk are joined by: m + R in base-2 units.
+  __device__ __forceinline__ float scale2() const { return __builtin_fmaf(m, c, static_cast<float>(ref)); }
   __device__ __forceinline__ void pin() {
     static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { pin_block<decltype(dc)::value>(acc[decltype(dc)::value]); });
   }
@@ -921,7 +937,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 
     const int end = lane_here(), col = end & 31, hf = end >> 5;
     const ChunkArgs& z = args_here();
-    float l = half_sum(bk.l), m = bk.m + static_cast<float>(bk.ref);
+    float l = half_sum(bk.l), m = bk.scale2();
     if constexpr (RB == 2) {  // waves 2 and 3 hand their sums over in the other buffer
       float* const at = reinterpret_cast<float*>(lds + ((step & 1) ^ 1) * (2 * kTileB)) + (wv & 1) * (32 * DP) + col;
       __syncthreads();
@@ -1126,7 +1142,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
       for (int i = 0; i < 16; ++i) mine[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32 + col] = bk.acc[d][i];
     const float lw = half_sum(bk.l);
     if (hf == 0) {
-      s_m[wv][col] = bk.m + static_cast<float>(bk.ref);
+      s_m[wv][col] = bk.scale2();
       s_l[wv][col] = lw;
     }
     __syncthreads();

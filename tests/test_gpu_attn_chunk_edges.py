@@ -1,4 +1,4 @@
-"""GPU: attention of new tokens over the paged cache where sums are not finite, in every row tile, in walks that one
+"""GPU: attention of new tokens over the paged cache where sums are not finite or scores are large, in every row tile, in walks that one
 workgroup has and in walks that are dealt in parts, against fp64 with the derived elementwise bound of attn_ref.bound."""
 import math
 
@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import flatquant_transform_quant_amd as fq
-from attn_ref import TDT, bound, encode, pack, values
+from attn_ref import TDT, U, bound, encode, pack, values
 from gpu_util import DEV, say
+from test_gpu_attention import MODES
 from test_gpu_attn_chunk import _i32, attend, seen_by
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,30 @@ def test_rows_that_are_not_finite_in_low_bits(mode, D, n, r):
         assert torch.equal(torch.isnan(got), bad)
         out, _, absv, top, vmax = attend(q.double(), kk, vv, seen, 1 / math.sqrt(D))
         assert ((got - out).abs() <= bound(out, absv, top, vmax, n, D, "bf16", "f16"))[~bad].all()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [1e3, 1e7, -1e9, 1e15, 1e30])
+def test_scores_of_any_size(mode, dt, scale):
+    """Scores far past what fp32 tells apart by less than 1 still give means of the values that are seen, and the value of the
+    key that stands out where one does by more than the scores' own error, (D + 8) 2^-24 of their terms."""
+    n, D, G = 2100, 64, 4
+    for r in (1, 12, 40):
+        say(f"[gpu] scores {mode} {dt} scale={scale} rows={r}")
+        g = torch.Generator().manual_seed(33)
+        q, k, v = (torch.randn(m, h, D, generator=g).to(TDT[dt]) for m, h in ((r, G), (n, 1), (n, 1)))
+        cache, table, kk, vv = _cache(k, v, mode, dt)
+        got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n), scale=scale).cpu().double()
+        seen = seen_by(r, n, 0, 0)
+        s = (torch.einsum("ihd,jd->ihj", q.double(), kk[:, 0]) * scale).masked_fill(~seen[:, None], -math.inf)
+        off = torch.einsum("ihd,jd->ihj", q.double().abs(), kk[:, 0].abs()).amax(-1) * abs(scale) * (D + 8) * 2.0 ** -24
+        top = s.topk(2, -1)
+        u = U[dt]
+        least, most = vv[:, 0].amin(0), vv[:, 0].amax(0)
+        assert torch.isfinite(got).all()
+        assert (got >= least - 3 * u * least.abs()).all() and (got <= most + 3 * u * most.abs()).all()
+        clear = top.values[..., 0] - top.values[..., 1] > 2 * off + 60
+        assert clear.any()
+        one = vv[:, 0][top.indices[..., 0]]
+        assert ((got - one).abs() <= 3 * u * one.abs() + 2.0 ** -24)[clear].all()
