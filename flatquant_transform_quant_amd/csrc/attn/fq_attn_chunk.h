@@ -19,7 +19,7 @@
 // LDS.  A bf16 q is brought to f16 by a power of two a row (28 binades below its largest element keep all bits).
 // Weights times value scales go to f16 relative to a reference exponent R, a row's own: w = exp2(s - m - R + 5) scale, where
 // R is at least the exponent of the scales seen, less one (w stays below 2^15).  The sum l is of exp2(s - m - R + 5), so the
-// quotient needs neither; m + R is what the parts of a walk are joined by.
+// quotient needs neither, and parts of a walk are joined as means with their weights' sums, without R.
 //
 // Split: every (sequence, cache head, row tile) is a segment of key tiles; all segments one after the other are dealt to
 // the grid in equal runs.  A segment's place in that order has a closed form in its tile number (its walk's
@@ -59,8 +59,9 @@ constexpr float kUnitK = MODE == kKvInt8 || MODE == kKvInt4 ? 512.0f : 1.0f;
 template <int MODE>
 constexpr float kUnitV = MODE == kKvFp4 ? 0x1p-13f : kUnitK<MODE>;
 // The reference R lies between these.  From kLeastRef on a walk's 2^31 weights sum below 2^127; up to kMostRef a weight of 1 is
-// well within fp32's normal numbers.
-constexpr int kLeastRef = -82, kMostRef = 120;
+// well within fp32's normal numbers.  Above kFullRef those 2^-35 of the largest are not (exp2 gives 0 below 2^-126): the walk is done again with
+// value scales 2^-kDown of what they are, which are far below the largest where that is a subnormal number.
+constexpr int kLeastRef = -82, kMostRef = 120, kFullRef = 96, kDown = 64;
 // weights enter the second product 2^kUpW times above the row's reference
 template <int MODE, int DT>
 constexpr float kUpW = MODE == kKv16 ? kUp<DT> : 5.0f;
@@ -316,9 +317,9 @@ __device__ __forceinline__ void load_rows(Rows<MODE, DP, PAD, NR>& x, const KvCa
 
 // The rows, widened, to LDS: keys from row `row0` of the tile at kt on, values of that at vt, their factors to ks and vs.
 // Returns the largest value scale (neither infinity nor NaN) of them.  Values that are not finite become f16 NaN, with a factor of 0 or
-// of the row's other groups.
+// of the row's other groups.  Values' factors are `down` of what they are.
 template <int MODE, int DP, bool PAD, int NR>
-__device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, int lane, uint8_t* kt, uint8_t* vt, float* ks, float* vs, int row0) {
+__device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, int lane, uint8_t* kt, uint8_t* vt, float* ks, float* vs, int row0, float down) {
   using R = Rows<MODE, DP, PAD, NR>;
   float big = 0.0f;
 #pragma unroll
@@ -337,6 +338,7 @@ __device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, in
         if (side == 0) {
           if (lanes_max<R::LPR>(nan ? 1 : 0)) f = __builtin_nanf("");
         } else {
+          f *= down;
           big = fmaxf(big, f);
         }
         if (p == 0) (side == 0 ? ks : vs)[r] = f;
@@ -360,8 +362,9 @@ __device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, in
 #pragma unroll
       for (int h = 0; h < NR / 16; ++h) {
         const bool fine = side == 0 || __builtin_fabsf(x.scale[1][h]) < kInf;
-        if (lane < 16) (side == 0 ? ks : vs)[row0 + 16 * h + lane] = fine ? x.scale[side][h] : 0.0f;
-        if (side == 1) big = fmaxf(big, fine ? __builtin_fabsf(x.scale[1][h]) : 0.0f);
+        const float f = !fine ? 0.0f : side == 0 ? x.scale[0][h] : x.scale[1][h] * down;
+        if (lane < 16) (side == 0 ? ks : vs)[row0 + 16 * h + lane] = f;
+        if (side == 1) big = fmaxf(big, __builtin_fabsf(f));
       }
     }
   }
@@ -639,10 +642,14 @@ struct Block {
         const auto r = __builtin_amdgcn_permlane32_swap(ev, ev, false, false);
         rn = max(ref, min(kMostRef, max(static_cast<int>(r[0]), static_cast<int>(r[1]))));
       }
-      f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(m - mn, c, static_cast<float>(ref - rn)));
+      f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f((m - mn) * c);
       m = mn;
-      ref = rn;
       l *= f;
+      if constexpr (kLow) {  // (R may rise by more than exp2 can say)
+        f = __builtin_amdgcn_ldexpf(f, ref - rn);
+        l = __builtin_amdgcn_ldexpf(l, ref - rn);
+        ref = rn;
+      }
       far = __any(m != -kInf && __builtin_fabsf(m) * c > kFar);
     }
     static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { scale_block<decltype(dc)::value>(acc[decltype(dc)::value], f, need); });
@@ -744,12 +751,27 @@ struct Block {
       *at = v & ~not_finite16_mask<ODT>(v);
     }
   }
-  // What the parts of a walk are joined by: m + R in base-2 units.
-  __device__ __forceinline__ float scale2() const { return __builtin_fmaf(m, c, static_cast<float>(ref)); }
   __device__ __forceinline__ void pin() {
     static_for<0, DB>([&](auto dc) __attribute__((always_inline)) { pin_block<decltype(dc)::value>(acc[decltype(dc)::value]); });
   }
-  // whether a sum is infinite or NaN
+  // Whether the walk has to be done again: a sum is infinite or NaN, or the reference beyond kFullRef (`high`).
+  __device__ __forceinline__ bool again() const { return odd() || high(); }
+  __device__ __forceinline__ bool high() const { return kLow && ref > kFullRef; }
+  // The walk's end: the sums become means of the values (0 where nothing was seen), l the sum of the weights, 2^kW times what they are
+  // relative to m, without R, and m is in base-2 units.  Value scales were `down` of what they are.
+  __device__ __forceinline__ void finish(float down) {
+    l = half_sum(l);
+    float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    constexpr bool kFirst = kUnitV<MODE> < 1.0f;  // (E2M1's sums are up to 2^13 above the values: that goes first)
+    const float up = kLow ? kUnitV<MODE> / down : 1.0f;
+    if (kFirst) inv *= up;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = kFirst || !kLow ? acc[d][i] * inv : acc[d][i] * inv * up;
+    if constexpr (kLow) l = __builtin_amdgcn_ldexpf(l, ref);
+    m *= c;
+  }
   __device__ __forceinline__ bool odd() const {
     float o = 0.0f;
 #pragma unroll
@@ -760,7 +782,15 @@ struct Block {
   }
 };
 
-// A part's sums for the join: [element][row] of TR rows, then m + R and l.
+// Means of two or more parts are joined by their weights' sums l, brought to one maximum: a part's share of them.  (A mean may hold the infinity of
+// an element that was seen: a share is never 0 but where nothing was.)
+__device__ __forceinline__ float part_weight(float l, float m, float to) { return m == -kInf ? 0.0f : l * rescale(m, to); }
+__device__ __forceinline__ float part_share(float w, float all) {
+  const float s = w == 0.0f ? 0.0f : w / all;  // (NaN stays)
+  return s < 0x1p-126f && w != 0.0f ? 0x1p-126f : s;
+}
+
+// A part for the join: its means [element][row] of TR rows, then m and l.
 template <int DP, int TR>
 constexpr int kPart = (DP + 2) * TR;
 
@@ -820,7 +850,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
   __shared__ __align__(16) uint8_t lds[4 * kTileB];  // buffer b: keys at 2 b, values at 2 b + 1
   __shared__ __align__(16) float s_scale[kLow ? 2 : 1][2][kLow ? kKeys : 1];  // [buffer][keys, values]
   __shared__ __align__(16) float s_top[kLow ? 2 : 1][kWaves];                 // largest value scale of 16 keys
-  __shared__ float s_m[2][RB == 2 ? 64 : 1];                                   // of waves 2 and 3: m + R, l
+  __shared__ float s_m[2][RB == 2 ? 64 : 1];                                   // of waves 2 and 3: m, l
   __shared__ typename BK::Odd s_odd[kWaves];
   lds_u8* const lds_l = (lds_u8*)lds;
   const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds_l));
@@ -877,8 +907,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
         load_rows(x, cc, lane, 0, pages.of(u, wv), row_at(a, hk, k), rows_at(sg, k), rowb, sb, D);
       }
     };
+    float down = 1.0f;
     auto store = [&](int buf) __attribute__((always_inline)) {
-      const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv);
+      const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv, down);
       if (lane == 0) s_top[buf][wv] = big;
     };
     for (bool careful = false;;) {
@@ -926,10 +957,11 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
         }
       }
       bk.pin();
-      if (careful || !__syncthreads_or(bk.odd())) {
+      if (careful || !__syncthreads_or(bk.again())) {
         if (careful) bk.add_odd(s_odd[wv]);
         break;
       }
+      if (kLow && __syncthreads_or(bk.high())) down = pow2(-kDown);
       careful = true;
       BK::no_odd(s_odd[wv]);
     }
@@ -937,7 +969,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 
     const int end = lane_here(), col = end & 31, hf = end >> 5;
     const ChunkArgs& z = args_here();
-    float l = half_sum(bk.l), m = bk.scale2();
+    bk.finish(down);
     if constexpr (RB == 2) {  // waves 2 and 3 hand their sums over in the other buffer
       float* const at = reinterpret_cast<float*>(lds + ((step & 1) ^ 1) * (2 * kTileB)) + (wv & 1) * (32 * DP) + col;
       __syncthreads();
@@ -947,16 +979,17 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 #pragma unroll
           for (int i = 0; i < 16; ++i) at[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32] = bk.acc[d][i];
         if (hf == 0) {
-          s_m[0][32 * (wv & 1) + col] = m;
-          s_m[1][32 * (wv & 1) + col] = l;
+          s_m[0][32 * (wv & 1) + col] = bk.m;
+          s_m[1][32 * (wv & 1) + col] = bk.l;
         }
       }
       __syncthreads();
       if (wv >= 2) continue;
-      const float mo = s_m[0][32 * wv + col], lo = s_m[1][32 * wv + col], mn = fmaxf(m, mo);
-      const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mo == -kInf ? 0.0f : rescale(mo, mn);
-      m = mn;
-      l = lo == 0.0f ? l * f0 : __builtin_fmaf(l, f0, lo * f1);  // (nothing seen, or NaN)
+      const float mo = s_m[0][32 * wv + col], mn = fmaxf(bk.m, mo);
+      const float w0 = part_weight(bk.l, bk.m, mn), w1 = part_weight(s_m[1][32 * wv + col], mo, mn);
+      bk.m = mn;
+      bk.l = w0 + w1;
+      const float f0 = part_share(w0, bk.l), f1 = part_share(w1, bk.l);
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -969,11 +1002,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * kTR] = bk.acc[d][i];
       if (hf == 0) {
-        o[DP * kTR] = m;
-        o[(DP + 1) * kTR] = l;
+        o[DP * kTR] = bk.m;
+        o[(DP + 1) * kTR] = bk.l;
       }
     } else if (pl.mine) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t to = sg.s.q0 + pl.token;
       uint16_t* const out = z.out.p + to * z.out.row + pl.head * z.out.head;
 #pragma unroll
@@ -982,12 +1014,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
         for (int i = 0; i < 4; ++i) {
           const int e = 32 * d + 8 * i + 4 * hf;
           if (PAD && e >= D) continue;
-          float o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = bk.acc[d][4 * i + j] * inv * kUnitV<MODE>;
-          *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(o[0], o[1]), round16x2<DT>(o[2], o[3])};
+          *reinterpret_cast<u32x2_t*>(out + e) = u32x2_t{round16x2<DT>(bk.acc[d][4 * i], bk.acc[d][4 * i + 1]),
+                                                         round16x2<DT>(bk.acc[d][4 * i + 2], bk.acc[d][4 * i + 3])};
         }
-      if (z.lse && hf == 0) z.lse[to * z.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
+      if (z.lse && hf == 0) z.lse[to * z.Hq + pl.head] = bk.l == 0.0f ? -kInf : (bk.m - BK::kW + __builtin_amdgcn_logf(bk.l)) * 0.693147181f;
     }
   } while (next_segment(args_here(), run, sg));
 }
@@ -1071,6 +1101,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
     const Place pl = place_of_rows(a, sg, wk, lane, 0);
     BK bk;
     bk.load_q(a, sg, pl, lane);
+    float down = 1.0f;
     for (bool careful = false;;) {
       bk.clear();
       uint32_t in = 0;
@@ -1089,7 +1120,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         const bool more = v + kWaves < v1;
         float big = 0.0f;
         if constexpr (kLow) {
-          big = store_rows(x, lane, lds[wv], lds[wv] + kSideB, s_scale[wv][0], s_scale[wv][1], 0);
+          big = store_rows(x, lane, lds[wv], lds[wv] + kSideB, s_scale[wv][0], s_scale[wv][1], 0, down);
           lds_done();  // (other lanes' rows are read below)
         }
         if constexpr (kLow) {
@@ -1124,15 +1155,17 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         }
       }
       bk.pin();
-      if (careful || !__syncthreads_or(bk.odd())) {
+      if (careful || !__syncthreads_or(bk.again())) {
         if (careful) bk.add_odd(s_odd[wv]);
         break;
       }
+      if (kLow && __syncthreads_or(bk.high())) down = pow2(-kDown);
       careful = true;
       BK::no_odd(s_odd[wv]);
     }
 
-    // ---- the waves' sums: [element][row] of each wave, then a wave joins a quarter of the elements
+    // ---- the waves' means: [element][row] of each wave, then a wave joins a quarter of the elements
+    bk.finish(down);
     const int end = lane_here(), col = end & 31, hf = end >> 5;
     const ChunkArgs& z = args_here();
     float* const mine = reinterpret_cast<float*>(lds[wv]);
@@ -1140,10 +1173,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mine[(32 * d + 8 * (i / 4) + 4 * hf + i % 4) * 32 + col] = bk.acc[d][i];
-    const float lw = half_sum(bk.l);
     if (hf == 0) {
-      s_m[wv][col] = bk.scale2();
-      s_l[wv][col] = lw;
+      s_m[wv][col] = bk.m;
+      s_l[wv][col] = bk.l;
     }
     __syncthreads();
     float m = -kInf, l = 0.0f, f[kWaves];
@@ -1151,10 +1183,11 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
     for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w][col]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      f[w] = s_m[w][col] == -kInf ? 0.0f : rescale(s_m[w][col], m);
-      const float li = s_l[w][col];
-      l = li == 0.0f ? l : __builtin_fmaf(li, f[w], l);  // (nothing seen, or NaN)
+      f[w] = part_weight(s_l[w][col], s_m[w][col], m);
+      l += f[w];
     }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) f[w] = part_share(f[w], l);
     // this lane's elements: DP / 8 from e0 on
     constexpr int NE = DP / 8;
     const int e0 = (2 * wv + hf) * NE;
@@ -1178,7 +1211,6 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         to[(DP + 1) * kTR] = l;
       }
     } else if (pl.mine) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t to = sg.s.q0 + pl.token;
       uint16_t* const out = z.out.p + to * z.out.row + pl.head * z.out.head + e0;
 #pragma unroll
@@ -1186,7 +1218,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         if (PAD && e0 + j >= D) break;
         u32x4_t w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = round16x2<DT>(o[j + 2 * i] * inv * kUnitV<MODE>, o[j + 2 * i + 1] * inv * kUnitV<MODE>);
+        for (int i = 0; i < 4; ++i) w[i] = round16x2<DT>(o[j + 2 * i], o[j + 2 * i + 1]);
         *reinterpret_cast<u32x4_t*>(out + j) = w;
       }
       if (z.lse && wv == 0 && hf == 0) z.lse[to * z.Hq + pl.head] = l == 0.0f ? -kInf : (m - BK::kW + __builtin_amdgcn_logf(l)) * 0.693147181f;
@@ -1232,21 +1264,20 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
     for (int k = 0; k < 4; ++k) {
       if (i + k > parts) break;
       const float mn = fmaxf(m, mi[k]);
-      const float f0 = m == -kInf ? 0.0f : rescale(m, mn), f1 = mi[k] == -kInf ? 0.0f : rescale(mi[k], mn);
+      const float w0 = part_weight(l, m, mn), w1 = part_weight(li[k], mi[k], mn);
       m = mn;
-      l = li[k] == 0.0f ? l * f0 : __builtin_fmaf(l, f0, li[k] * f1);  // (nothing seen, or NaN)
+      l = w0 + w1;
+      const float f0 = part_share(w0, l), f1 = part_share(w1, l);
 #pragma unroll
       for (int j = 0; j < NE; ++j) o[j] = __builtin_fmaf(o[j], f0, x[k][j] * f1);
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t to = sg.s.q0 + token;
   uint16_t* const out = a.out.p + to * a.out.row + head * a.out.head + e;
 #pragma unroll
   for (int j = 0; j < NE; j += 4) {
     if (e + j >= a.c.D) break;
-    *reinterpret_cast<u32x2_t*>(out + j) = u32x2_t{round16x2<DT>(o[j] * inv * kUnitV<MODE>, o[j + 1] * inv * kUnitV<MODE>),
-                                                   round16x2<DT>(o[j + 2] * inv * kUnitV<MODE>, o[j + 3] * inv * kUnitV<MODE>)};
+    *reinterpret_cast<u32x2_t*>(out + j) = u32x2_t{round16x2<DT>(o[j], o[j + 1]), round16x2<DT>(o[j + 2], o[j + 3])};
   }
   if (a.lse && e == 0)
     a.lse[to * a.Hq + head] = l == 0.0f ? -kInf : (m - kUpW<MODE, DT> + __builtin_amdgcn_logf(l)) * 0.693147181f;

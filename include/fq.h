@@ -410,7 +410,7 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
  * row lose bits, and a bf16 query's elements more than 2^28 below the largest of its row).  The weights are rounded once for
  * the second product: to 11 bits and 2^-32 of the row's largest at the least over an f16 cache, 8 bits over a bf16 one; over the low-bit
  * formats a weight, off by up to 2^-17 of itself where value scales are far from 1, times its value's scale to 11 bits, and to 2^-30 of the largest of these.  Value scales below 2^-80 lose bits (E2M1:
- * values below 2^-80), above 2^96 the weights below 2^-21 do not count. */
+ * values below 2^-80), and below 2^-16 where some of 128 neighbouring rows of a cache head see ones above 2^96. */
 fq_status fq_attn_chunk_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table, const fq_tensor* cu_q,
                                            int32_t window, int32_t sinks, uint64_t* workspaceSize);
 fq_status fq_attn_chunk(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* k_scale, const fq_tensor* v_cache,

@@ -1,4 +1,4 @@
-"""GPU: attention of new tokens over the paged cache where sums are not finite or scores are large, in every row tile, in walks that one
+"""GPU: attention of new tokens over the paged cache where sums are not finite, scores large or values far from 1, in every row tile, in walks that one
 workgroup has and in walks that are dealt in parts, against fp64 with the derived elementwise bound of attn_ref.bound."""
 import math
 
@@ -8,7 +8,7 @@ import torch
 import flatquant_transform_quant_amd as fq
 from attn_ref import TDT, U, bound, encode, pack, values
 from gpu_util import DEV, say
-from test_gpu_attention import MODES
+from test_gpu_attention import MODES, _check_rows
 from test_gpu_attn_chunk import _i32, attend, seen_by
 
 pytestmark = pytest.mark.gpu
@@ -101,6 +101,52 @@ def test_rows_that_are_not_finite_in_low_bits(mode, D, n, r):
         assert torch.equal(torch.isnan(got), bad)
         out, _, absv, top, vmax = attend(q.double(), kk, vv, seen, 1 / math.sqrt(D))
         assert ((got - out).abs() <= bound(out, absv, top, vmax, n, D, "bf16", "f16"))[~bad].all()
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3", "int4", "fp4"])
+@pytest.mark.parametrize("e", [90, 104, 112, 118, 125])
+def test_many_small_weights_beside_large_values(mode, e):
+    """4000 keys 9 to 12 nats below the one that stands out hold a third of the weight: with values of any size (2^e and its neighbours)
+    they count, in the result and in lse."""
+    n, D, G = 4000, 64, 8
+    g = torch.Generator().manual_seed(32)
+    for r in (1, 6, 16):
+        say(f"[gpu] small weights {mode} e={e} rows={r}")
+        q = torch.zeros(r, G, D, dtype=torch.bfloat16)
+        q[..., 0] = 8.0
+        k = torch.zeros(n, 1, D)
+        k[:, 0, 0] = -(torch.rand(n, generator=g) * 3 + 9)
+        k[7] = 0.0
+        k[n - r:, 0, 0] = -30.0
+        v = ((0.5 + torch.rand(n, 1, D, generator=g)) * 2.0 ** e).bfloat16()
+        cache, table, kk, vv = _cache(k.bfloat16(), v, mode, "bf16")
+        lse = torch.empty(r, G, device=DEV)
+        got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n), lse=lse).cpu()
+        want = attend(q.double(), kk, vv, seen_by(r, n, 0, 0), 1 / math.sqrt(D))
+        assert want[1].min() > 0.1
+        _check_rows(got, lse.cpu(), want, "bf16", D, n, "f16", f"{mode} 2^{e}")
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3", "int4", "fp4"])
+@pytest.mark.parametrize("e", [60, 100, 125])
+def test_rows_before_large_values(mode, e):
+    """Rows that see a token's values of 2^e and, in the same tile, rows that do not and whose own are ordinary: all within the bound."""
+    n, D, G, H = 1900, 64, 2, 2
+    for r in (6, 20, 120):
+        say(f"[gpu] before large values {mode} e={e} rows={r}")
+        g = torch.Generator().manual_seed(34)
+        q, k, v = (torch.randn(m, h, D, generator=g).bfloat16() for m, h in ((r, H * G), (n, H), (n, H)))
+        v[n - 1 - r // 3] *= 2.0 ** e
+        cache, table, kk, vv = _cache(k, v, mode, "bf16")
+        lse = torch.empty(r, H * G, device=DEV)
+        got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n), lse=lse).cpu()
+        # (rows in two groups: the bound's largest value is one that a row sees)
+        before = r - 1 - r // 3
+        for rows, m in ((slice(before), n - r + before), (slice(before, r), n)):
+            *want, top = attend(q[rows].double(), kk[:m], vv[:m], seen_by(r, n, 0, 0)[rows, :m], 1 / math.sqrt(D))
+            # A weight times its value's scale is held to 2^-30 of the row's largest of these, for all elements alike: that times a code is
+            # up to 2^-30 of the largest value of any element (127, 448, 7 or 6 times its scale), also where the large token's own code is 0.
+            _check_rows(got[rows], lse.cpu()[rows], (*want, top.amax(-1, keepdim=True).expand_as(top)), "bf16", D, m, "f16", f"{mode} rows {rows}")
 
 
 @pytest.mark.parametrize("mode", MODES)
