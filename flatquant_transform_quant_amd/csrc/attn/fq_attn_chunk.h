@@ -62,6 +62,14 @@ constexpr float kUnitV = MODE == kKvFp4 ? 0x1p-13f : kUnitK<MODE>;
 // well within fp32's normal numbers.  Above kFullRef those 2^-35 of the largest are not (exp2 gives 0 below 2^-126): the walk is done again with
 // value scales 2^-kDown of what they are, which are far below the largest where that is a subnormal number.
 constexpr int kLeastRef = -82, kMostRef = 120, kFullRef = 96, kDown = 64;
+// Whether the weights of row tiles of 32 RB rows enter the second product in two parts, the rounded weight and what the rounding left, and
+// so with 16 bits (bf16) or 22.  Rounded once they add as much to an output's error as its own rounding where that has as many bits: 1.4 times the
+// error in all (single tokens over a bf16 cache 2.2e-3 of the output, so 1.6e-3).  us without and with: 32 single tokens of 1028 keys in
+// bf16 35.0, 35.8, like all tiles of 32, which wait for memory; 24 x 5 drafts over int8 in tiles of 64 113.8, 122.5, so not for
+// bf16 rows, whose output has 8 bits to these weights' 11; tiles of 128 keep one part, a document of 16384 rows in f16 314, 405, 5 chunks of
+// 1024 over int4 575, 656: matrix and vector unit are what bounds them.
+template <int MODE, int DT, int RB>
+constexpr bool kRest = RB == 1 || (RB == 2 && (MODE == kKv16 || DT == kF16));
 // weights enter the second product 2^kUpW times above the row's reference
 template <int MODE, int DT>
 constexpr float kUpW = MODE == kKv16 ? kUp<DT> : 5.0f;
@@ -556,7 +564,7 @@ struct Block {
   // Keys k0 .. k0 + 32 NB - 1, their rows at kt and vt in LDS (from a multiple of 32 on), their factors at ks and vs.  in: which 16
   // of them have a page; big: the largest value scale.  `scored` is called when
   // the score products are under way, before a value is read.
-  template <int NB, typename F>
+  template <int NB, bool REST, typename F>
   __device__ __forceinline__ void step(const Place& p, int lane, int sinks, int k0, uint32_t in, float big, const lds_u8* kt, const lds_u8* vt,
                                        const float* ks_, const float* vs_, F&& scored) {
     const int col = lane & 31, hf = lane >> 5;
@@ -663,7 +671,7 @@ struct Block {
       for (int i = 0; i < 16 * NB; ++i) s[i / 16][i % 16] -= m0;
       ms = static_cast<float>(ref) - kW;
     }
-    u32x4_t pf[2 * NB];
+    u32x4_t pf[2 * NB], rest[REST ? 2 * NB : 1];
 #pragma unroll
     for (int g = 0; g < 2 * NB; ++g) {
       f32x4_t vs[2];
@@ -682,6 +690,8 @@ struct Block {
           x1 *= vs[i / 2][2 * (i % 2) + 1];
         }
         pf[g][i] = round16x2<ODT>(x0, x1);
+        if constexpr (REST)
+          rest[g][i] = round16x2<ODT>(x0 - load16<ODT>(static_cast<uint16_t>(pf[g][i])), x1 - load16<ODT>(static_cast<uint16_t>(pf[g][i] >> 16)));
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -690,6 +700,7 @@ struct Block {
       if constexpr (i + kAhead < 2 * NB * DB) vf[i + kAhead] = value((i + kAhead) % DB, (i + kAhead) / DB);
       __builtin_amdgcn_sched_barrier(0);
       acc[i % DB] = mfma32x32x16<ODT>(vf[i], pf[i / DB], acc[i % DB]);
+      if constexpr (REST) acc[i % DB] = mfma32x32x16<ODT>(vf[i], rest[i / DB], acc[i % DB]);
       __builtin_amdgcn_sched_barrier(0);
     });
   }
@@ -949,7 +960,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
           const int b = RB == 2 ? wv / 2 : i;
           if (!BK::sees(pl, a.sinks, k0 + 32 * b, 32 * NB)) continue;
           const float big = kLow ? fmaxf(s_top[buf][2 * b], s_top[buf][2 * b + 1]) : 0.0f;
-          bk.template step<NB>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big,
+          bk.template step<NB, kRest<MODE, DT, RB>>(pl, lane, a.sinks, k0 + 32 * b, (in >> (2 * b)) & ((1u << (2 * NB)) - 1u), big,
                                kt + 32 * b * kRowB, vt + 32 * b * kRowB, &s_scale[buf][0][32 * b], &s_scale[buf][1][32 * b], [] {});
         }
         if constexpr (kLow) {
@@ -1138,11 +1149,11 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
         }
         const bool sees = BK::sees(pl, a.sinks, k0, 32);
         if constexpr (kLow) {
-          if (sees) bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
+          if (sees) bk.template step<1, kRest<MODE, DT, 1>>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
           lds_done();  // (before the next rows take their places)
         } else {
           landed(true);  // (the keys)
-          bk.template step<1>(pl, lane, a.sinks, k0, now, big, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
+          bk.template step<1, kRest<MODE, DT, 1>>(pl, lane, a.sinks, k0, now, big, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
             lds_done();
             if (more) {
               in = bits(v + kWaves);

@@ -407,9 +407,10 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
  * table entry is outside the cache is left out.  What a row does not see never reaches it, infinities and NaN included; rows of out past
  * cu_q[B] are not written.  The same inputs give the same bits.
  * Scores, statistics and sums are fp32, codes enter the products exactly (E2M1 groups more than 2^26 below the largest of their
- * row lose bits, and a bf16 query's elements more than 2^28 below the largest of its row).  The weights are rounded once for
+ * row lose bits, and a bf16 query's elements more than 2^28 below the largest of its row).  The weights are rounded for
  * the second product: to 11 bits and 2^-32 of the row's largest at the least over an f16 cache, 8 bits over a bf16 one; over the low-bit
- * formats a weight, off by up to 2^-17 of itself where value scales are far from 1, times its value's scale to 11 bits, and to 2^-30 of the largest of these.  Value scales below 2^-80 lose bits (E2M1:
+ * formats a weight, off by up to 2^-17 of itself where value scales are far from 1, times its value's scale to 11 bits, and to 2^-30 of the largest of these.
+ * Twice as many bits (as fq_attn_decode's) where r is 32, so for single tokens and few drafts, and, over 16-bit caches or with f16 rows, where r is 64.  Value scales below 2^-80 lose bits (E2M1:
  * values below 2^-80), and below 2^-16 where some of 128 neighbouring rows of a cache head see ones above 2^96. */
 fq_status fq_attn_chunk_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table, const fq_tensor* cu_q,
                                            int32_t window, int32_t sinks, uint64_t* workspaceSize);

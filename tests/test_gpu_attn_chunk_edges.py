@@ -174,3 +174,33 @@ def test_scores_of_any_size(mode, dt, scale):
         assert clear.any()
         one = vv[:, 0][top.indices[..., 0]]
         assert ((got - one).abs() <= 3 * u * one.abs() + 2.0 ** -24)[clear].all()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("r", [1, 4, 8])
+def test_weights_of_few_rows_keep_their_bits(mode, dt, r):
+    """Two kinds of keys whose values cancel, so that what a weight's rounding adds shows in the output: with weights in two parts it is 2^-16 of
+    sum p |v| for bf16 operands and 2^-22 for f16 ones, as fq_attn_decode's.  Tiles of 32 rows, and of 64 where the rows' type has
+    the weights' bits."""
+    n, D, G, H = 1000, 64, 8, 1
+    if r * G > 32 and mode != "same" and dt == "bf16":
+        return
+    say(f"[gpu] weights {mode} {dt} rows={r}")
+    g = torch.Generator().manual_seed(35)
+    q = torch.zeros(r, G, D)
+    q[..., 0] = 0.25 * torch.arange(1, G + 1)  # (other weights for each head)
+    k, v = torch.zeros(n, H, D), torch.ones(n, H, D)
+    k[::2, :, 0], v[::2] = -2.0, -1.3
+    q, k, v = q.to(TDT[dt]), k.to(TDT[dt]), (v * (1 + 0.2 * torch.rand(1, 1, D, generator=g))).to(TDT[dt])
+    cache, table, kk, vv = _cache(k, v, mode, dt)
+    got = fq.attn_chunk(q.to(DEV), cache, table, _i32(0, r), _i32(n)).cpu().double()
+    out, _, absv, top, _ = attend(q.double(), kk, vv, seen_by(r, n, 0, 0), 1 / math.sqrt(D))
+    # attn_ref.bound with these weights: scores, exp and sums as there
+    rel = (2.0 ** -16 if mode == "same" and dt == "bf16" else 2.0 ** -22) + (2.0 ** -17 if mode != "same" else 0.0)
+    rel = rel + 2.0 * (D + 8) * 2.0 ** -24 * top[..., None] + (16 + math.sqrt(n)) * 2.0 ** -23
+    assert (out.abs() < 0.1 * absv).any()
+    tol = U[dt] * out.abs() + rel * absv * (1 + U[dt]) + n * 2.0 ** -40 * vv.abs().max() + (2.0 ** -25 if dt == "f16" else 0.0)
+    worst = ((got - out).abs() / tol).max().item()
+    say(f"[gpu]   worst error {worst:.3f} of its bound")
+    assert worst <= 1
