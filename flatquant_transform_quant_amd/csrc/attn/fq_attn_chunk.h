@@ -7,7 +7,7 @@
 // A workgroup of four waves takes a row tile: the g query heads of one cache head for neighbouring tokens (a cached byte is
 // read once for all of them), 128, 64 or 32 rows, the smallest that the mean rows of a sequence and cache head fit.  With 128 a wave has
 // 32 rows; with 64 waves 2 and 3 have the rows of 0 and 1 and the other half of the keys; with 32 each wave has all rows and keys of its
-// own, in LDS of its own without barriers (us in tiles of 128: 24 sequences of 5 drafts, 40 rows, over int8 265, now 122; see kShort for
+// own, in LDS of its own without barriers (24 sequences of 5 drafts, 40 rows, over int8, in tiles of 128 265 us, of 64 122; see kShort for
 // single tokens).  It walks the keys in tiles of 64 as the prompt kernel does: two LDS buffers, S^T = K Q^T and O^T = V^T P^T with
 // 32 x 32 x 16 products, a lane owning one row's statistics, the maximum moved only when a score passes m + 8 in base-2 units.  LDS
 // layouts as there.  A tile's keys lie in pages of 16 tokens at least: each wave brings the 16 rows that are one page's (16 bits by LDS-DMA).
@@ -29,7 +29,7 @@
 //
 // Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 37% and
 // vector unit 42% busy, one after the other in a wave, two waves a SIMD; 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and
-// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 111 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's;
+// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 114 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's;
 // 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
 #pragma once
 
@@ -52,7 +52,7 @@ constexpr float kLazy = 8.0f;
 constexpr float kFar = 0x1p20f;
 
 template <int MODE>
-constexpr int kCodeBits = MODE == kKv16 ? 16 : (MODE == kKvInt8 || MODE == kKvE4M3) ? 8 : 4;
+constexpr int kCodeBits = MODE == kKvInt8 || MODE == kKvE4M3 ? 8 : 4;
 // a key's and a value's operand for 1 (E2M1: the keys' is in their factors)
 template <int MODE>
 constexpr float kUnitK = MODE == kKvInt8 || MODE == kKvInt4 ? 512.0f : 1.0f;
@@ -274,6 +274,7 @@ __device__ __forceinline__ int lanes_max(int v) {
 // Rows of a tile that one wave brings through registers, NR of them (16 a page): their pieces and scales, of both sides.
 template <int MODE, int DP, bool PAD, int NR>
 struct Rows {
+  static_assert(MODE != kKv16, "16-bit rows go to LDS by LDS-DMA");
   static constexpr int bits = kCodeBits<MODE>;
   static constexpr int CE = PAD ? 8 : (128 / bits < DP / 4 ? 128 / bits : DP / 4);  // elements of a piece
   static constexpr int LPR = DP / CE;        // lanes of a row
@@ -306,19 +307,17 @@ __device__ __forceinline__ void load_rows(Rows<MODE, DP, PAD, NR>& x, const KvCa
       const int rr = (64 * i + lane) / R::LPR, p = (64 * i + lane) % R::LPR;
       load_piece<R::W>(rc, !PAD || R::CE * p < D ? static_cast<uint32_t>(rr * rowb + p * (R::CE * R::bits / 8)) : kOut, x.w[side][half * R::NH + i]);
     }
-    if constexpr (MODE != kKv16) {
-      const auto rs = __builtin_amdgcn_make_buffer_rsrc(sd.scale + (at * sd.scale_page_b + r * sb), static_cast<int16_t>(0), pg < 0 ? 0 : rows * sb,
-                                                        kBufferWord3);
-      if constexpr (MODE == kKvFp4) {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(sd.scale + (at * sd.scale_page_b + r * sb), static_cast<int16_t>(0), pg < 0 ? 0 : rows * sb,
+                                                      kBufferWord3);
+    if constexpr (MODE == kKvFp4) {
 #pragma unroll
-        for (int i = 0; i < R::NH; ++i) {
-          const int rr = (64 * i + lane) / R::LPR, p = (64 * i + lane) % R::LPR;
-          x.e8[side][half * R::NH + i] =
-              __builtin_amdgcn_raw_buffer_load_b8(rs, !PAD || R::CE * p < D ? static_cast<uint32_t>(rr * sb + R::CE * p / 32) : kOut, 0, 0);
-        }
-      } else {
-        x.scale[side][half] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (lane & 15), 0, 0));
+      for (int i = 0; i < R::NH; ++i) {
+        const int rr = (64 * i + lane) / R::LPR, p = (64 * i + lane) % R::LPR;
+        x.e8[side][half * R::NH + i] =
+            __builtin_amdgcn_raw_buffer_load_b8(rs, !PAD || R::CE * p < D ? static_cast<uint32_t>(rr * sb + R::CE * p / 32) : kOut, 0, 0);
       }
+    } else {
+      x.scale[side][half] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (lane & 15), 0, 0));
     }
   }
 }
@@ -350,23 +349,19 @@ __device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, in
           big = fmaxf(big, f);
         }
         if (p == 0) (side == 0 ? ks : vs)[r] = f;
-      } else if (MODE != kKv16 && side == 1) {
+      } else if (side == 1) {
         nan = !(__shfl(__builtin_fabsf(x.scale[1][half]), rr) < kInf);
       }
       uint8_t* const to = (side == 0 ? kt : vt) + r * (2 * DP);
       const int sw = side == 0 ? key_swz<DP>(r) : value_swz<DP>(r);
-      if constexpr (MODE == kKv16) {
-        *reinterpret_cast<u32x4_t*>(to + 16 * (p ^ sw)) = u32x4_t{x.w[side][i][0], x.w[side][i][1], x.w[side][i][2], x.w[side][i][3]};
-      } else {
 #pragma unroll
-        for (int e = 0; e < R::CE / 8; ++e) {
-          u32x4_t o = widened<MODE>(x.w[side][i], e, s);
-          if (side == 1 && nan) o = u32x4_t{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
-          *reinterpret_cast<u32x4_t*>(to + 16 * (((R::CE / 8) * p + e) ^ sw)) = o;
-        }
+      for (int e = 0; e < R::CE / 8; ++e) {
+        u32x4_t o = widened<MODE>(x.w[side][i], e, s);
+        if (side == 1 && nan) o = u32x4_t{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
+        *reinterpret_cast<u32x4_t*>(to + 16 * (((R::CE / 8) * p + e) ^ sw)) = o;
       }
     }
-    if constexpr (MODE != kKv16 && MODE != kKvFp4) {
+    if constexpr (MODE != kKvFp4) {
 #pragma unroll
       for (int h = 0; h < NR / 16; ++h) {
         const bool fine = side == 0 || __builtin_fabsf(x.scale[1][h]) < kInf;
@@ -376,15 +371,13 @@ __device__ __forceinline__ float store_rows(const Rows<MODE, DP, PAD, NR>& x, in
       }
     }
   }
-  if constexpr (MODE != kKv16) {
-    big = fmaxf(big, dpp_f<kDppQuadXor1>(big));
-    big = fmaxf(big, dpp_f<kDppQuadXor2>(big));
-    big = fmaxf(big, dpp_f<kDppRowHalfMirror>(big));
-    big = fmaxf(big, dpp_f<kDppRowMirror>(big));
-    if constexpr (MODE == kKvFp4) {  // (the others have the same 16 scales in every row of 16 lanes)
-      big = half_max(big);
-      big = fmaxf(big, __shfl_xor(big, 16));
-    }
+  big = fmaxf(big, dpp_f<kDppQuadXor1>(big));
+  big = fmaxf(big, dpp_f<kDppQuadXor2>(big));
+  big = fmaxf(big, dpp_f<kDppRowHalfMirror>(big));
+  big = fmaxf(big, dpp_f<kDppRowMirror>(big));
+  if constexpr (MODE == kKvFp4) {  // (the others have the same 16 scales in every row of 16 lanes)
+    big = half_max(big);
+    big = fmaxf(big, __shfl_xor(big, 16));
   }
   return big;
 }
@@ -852,8 +845,8 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& a, const Run& r, S
 template <int MODE, int DT, int DP, bool PAD, int RB>
 __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
-  using RW = Rows<MODE, DP, PAD, 16>;
   constexpr bool kLow = BK::kLow;
+  using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 16>;  // (16 bits: not used)
   constexpr int DB = BK::DB, kRowB = BK::kRowB, kTR = 32 * RB;
   constexpr int kTileB = kKeys * kRowB;  // bytes of a tile (keys or values)
   constexpr int kPieces = DP / 8;        // 16-byte pieces of a row
@@ -920,8 +913,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
     };
     float down = 1.0f;
     auto store = [&](int buf) __attribute__((always_inline)) {
-      const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv, down);
-      if (lane == 0) s_top[buf][wv] = big;
+      if constexpr (kLow) {
+        const float big = store_rows(x, lane, lds + buf * (2 * kTileB), lds + buf * (2 * kTileB) + kTileB, s_scale[buf][0], s_scale[buf][1], 16 * wv, down);
+        if (lane == 0) s_top[buf][wv] = big;
+      }
     };
     for (bool careful = false;;) {
       bk.clear();
@@ -1042,7 +1037,7 @@ template <int MODE, int DT, int DP, bool PAD>
 __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
   constexpr bool kLow = BK::kLow;
-  using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 32>;
+  using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 32>;  // (16 bits: not used)
   constexpr int DB = BK::DB, kRowB = BK::kRowB, kTR = 32;
   constexpr int kSideB = 32 * kRowB;  // bytes of a wave's keys (or values); both: 32 rows of DP sums in fp32
   constexpr int kPieces = DP / 8;     // 16-byte pieces of a row
@@ -1079,10 +1074,12 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
     auto key_of = [&](int v) __attribute__((always_inline)) { return wk.tile(v >> 1) * kKeys + 32 * (v & 1); };
     RW x;
     auto load = [&](int v) __attribute__((always_inline)) {
-      const int k = key_of(v);
+      if constexpr (kLow) {
+        const int k = key_of(v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        load_rows(x, cc, lane, h, pages.of(v >> 1, 2 * (v & 1) + h), row_at(a, hk, k + 16 * h), rows_at(sg, k + 16 * h), rowb, sb, D);
+        for (int h = 0; h < 2; ++h)
+          load_rows(x, cc, lane, h, pages.of(v >> 1, 2 * (v & 1) + h), row_at(a, hk, k + 16 * h), rows_at(sg, k + 16 * h), rowb, sb, D);
+      }
     };
     // load i of a side fills the 16-byte places 64 i + lane; the first half of them is the first page's
     auto dma = [&](int v, int side) __attribute__((always_inline)) {
@@ -1147,11 +1144,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
           BK::drop_odd(vt, 32);
           lds_done();
         }
-        const bool sees = BK::sees(pl, a.sinks, k0, 32);
         if constexpr (kLow) {
-          if (sees) bk.template step<1, kRest<MODE, DT, 1>>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
+          if (BK::sees(pl, a.sinks, k0, 32)) bk.template step<1, kRest<MODE, DT, 1>>(pl, lane, a.sinks, k0, now, big, kt, vt, s_scale[wv][0], s_scale[wv][1], [] {});
           lds_done();  // (before the next rows take their places)
-        } else {
+        } else {  // (keys that no row sees, at most the rest of 64 of them, are masked like others)
           landed(true);  // (the keys)
           bk.template step<1, kRest<MODE, DT, 1>>(pl, lane, a.sinks, k0, now, big, kt, vt, nullptr, nullptr, [&] __attribute__((always_inline)) {
             lds_done();
