@@ -35,7 +35,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkArgs& a, int b) {
   Seq s{0, 0, 0, 0, 0, 0};
   if (b < a.B) {
     s.q0 = max(0, min(a.cu_q[b], a.Tq));
-    s.lq = max(0, min(a.cu_q[b + 1], a.Tq) - s.q0);
+    s.lq = max(0, max(0, min(a.cu_q[b + 1], a.Tq)) - s.q0);  // (a difference of numbers that are not negative)
     s.lk = max(0, min(a.lengths[b], a.reach));
     s.off = s.lk - s.lq;
     s.tiles = (s.lq + a.tokens - 1) / a.tokens;

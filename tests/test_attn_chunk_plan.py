@@ -1,5 +1,5 @@
 """The plan of attention of new tokens: the library's own code run on the CPU (chunk_plan_host.cpp), wave by wave.  Every key tile that a
-row tile sees is walked once, parts are where the join reads them, and sequences that lie over each other stay within memory."""
+row tile sees is walked once, parts are where the join reads them, and row numbers that do not ascend stay within memory."""
 import ctypes
 import os
 import random
@@ -135,6 +135,18 @@ def test_drawn(lib):
         sizes = [(g.choice([0, 1, 1, 2, 5, 40, 200]), g.randint(0, width * 16 + 20)) for _ in range(g.choice([1, 5, 70]))]
         if sum(r for r, _ in sizes):
             check(lib, sizes, Hq, H, D=g.choice([64, 256]), width=width, window=g.choice([0, 0, 1, 100, 2000]), sinks=g.choice([0, 4, 90]))
+
+
+@pytest.mark.parametrize("width,window", [(30, 0), (30, 9), (400, 0), (400, 1800), (4096, 0)])
+def test_row_numbers_that_do_not_ascend(lib, width, window):
+    """Whatever cu_q and lengths hold, the kernels index no row, key or part that is not there, and every walk ends."""
+    g = random.Random(8)
+    for i in range(8):
+        B, Tq = g.choice([1, 3, 70, 130]), g.choice([1, 40, 700])
+        wild = lambda most: g.choice([-2 ** 31, -1, 0, 1, most // 2, most, most + 1, 2 ** 31 - 1, g.randint(0, most)])  # noqa: E731
+        cu, lengths = [wild(Tq) for _ in range(B + 1)], [wild(16 * width) for _ in range(B)]
+        a, r = plan(lib, cu, lengths, Tq, 8, 2, width=width, window=window, sinks=g.choice([0, 5]), most=4000000)
+        in_memory(a, r, Tq, 16 * width)
 
 
 def test_sequences_that_all_have_every_row(lib):

@@ -204,3 +204,21 @@ def test_weights_of_few_rows_keep_their_bits(mode, dt, r):
     worst = ((got - out).abs() / tol).max().item()
     say(f"[gpu]   worst error {worst:.3f} of its bound")
     assert worst <= 1
+
+
+def test_row_numbers_far_below_zero():
+    """A cu_q that does not ascend, down to the smallest int32: a sequence has no rows then (a difference of these numbers passes 32 bits), and
+    those of the sequences beside it are right."""
+    g = torch.Generator().manual_seed(36)
+    r, n, D = 40, 300, 64
+    q, k, v = (torch.randn(m, h, D, generator=g).bfloat16() for m, h in ((r, 4), (n, 2), (n, 2)))
+    cache, table, kk, vv = _cache(k, v, "same", "bf16")
+    want, _, absv, top, vmax = attend(q.double(), kk, vv, seen_by(r, n, 0, 0), 1 / math.sqrt(D))
+    tol = bound(want, absv, top, vmax, n, D, "bf16", "bf16")
+    for low in (-1, -2 ** 31, -2 ** 31 + 39):
+        for cu in ((0, r, low, low), (r, low, r)):
+            say(f"[gpu] cu_q {cu}")
+            out = torch.full((r, 4, D), 7.0, dtype=torch.bfloat16, device=DEV)
+            B = len(cu) - 1
+            fq.attn_chunk(q.to(DEV), cache, table.expand(B, -1), _i32(*cu), _i32(*[n] * B), out=out)
+            assert ((out.cpu().double() - want).abs() <= tol).all()
