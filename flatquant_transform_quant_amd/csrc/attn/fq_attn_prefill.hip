@@ -93,9 +93,9 @@ __device__ __forceinline__ Place place_of(const PrefillArgs& a, int id, int part
     int s = 0, n = 0, ks = 0, kn = 0;
     if (b < a.B) {
       s = max(0, min(a.cu_q[b], a.Tq));
-      n = max(0, min(a.cu_q[b + 1], a.Tq) - s);
+      n = max(0, max(0, min(a.cu_q[b + 1], a.Tq)) - s);  // (a difference of numbers that are not negative)
       ks = max(0, min(a.cu_k[b], a.Tk));
-      kn = max(0, min(a.cu_k[b + 1], a.Tk) - ks);
+      kn = max(0, max(0, min(a.cu_k[b + 1], a.Tk)) - ks);
     }
     const int nt = (n + kRows - 1) / kRows;
     if (parts > 1) p.chunk = max(kMinChunk, (wave_top(nt > 0 ? key_tiles(a, kn - n, kn, n, nt - 1) : 0) + parts - 1) / parts);
