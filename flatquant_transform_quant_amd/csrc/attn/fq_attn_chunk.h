@@ -47,8 +47,6 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kAhead = 4;           // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
-// Scores up to this far from 0, in base-2 units, have their maximum taken off within the weights' exponent; its rounding is 2^-5 there.
-constexpr float kFar = 0x1p20f;
 
 template <int MODE>
 constexpr int kCodeBits = MODE == kKvInt8 || MODE == kKvE4M3 ? 8 : 4;

@@ -212,6 +212,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
 
   f32x16_t acc[DB];
   float m, l;
+  // The careful walk's maximum is a score, before c, until its end, and one beyond kFar (`far`: some row's of the wave), which as an fp32
+  // number in base 2 is off by units, is taken off as a score.
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
@@ -220,6 +222,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
       for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     m = -kInf;
     l = 0.0f;
+    bool far = false;
     if (CAREFUL && t_first < t_end) dma(t_first, t_first & 1);
     for (int t = t_first; t < t_end; ++t) {
       const int buf = t & 1;
@@ -284,17 +287,24 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
       float top = s[0][0];
 #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-      if (__any(top * c > m + kLazy)) {
-        const float mn = fmaxf(m, half_max(top) * c);
-        const float f = mn == -kInf ? 1.0f : CAREFUL ? rescale(m, mn) : __builtin_amdgcn_exp2f(m - mn);
+      if (far ? __any((top - m) * c > kLazy) : __any(top * c > (CAREFUL ? product(m, c) : m) + kLazy)) {
+        const float mn = fmaxf(m, CAREFUL ? half_max(top) : half_max(top) * c);
+        const float d = !CAREFUL ? m - mn : far ? (m - mn) * c : product(m, c) - product(mn, c);
+        const float f = mn == -kInf ? 1.0f : CAREFUL ? rescale(d, 0.0f) : __builtin_amdgcn_exp2f(d);
         m = mn;
+        if constexpr (CAREFUL) far = __any(m != -kInf && __builtin_fabsf(m) * c > kFar);
         l *= f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[d][i] *= f;
       }
-      const float ms = m == -kInf ? 0.0f : m - kUp<DT>;
+      float ms = m == -kInf ? 0.0f : (CAREFUL ? product(m, c) : m) - kUp<DT>;
+      if (CAREFUL && far) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i / 16][i % 16] -= m == -kInf ? 0.0f : m;
+        ms = -kUp<DT>;
+      }
       u32x4_t pf[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -338,6 +348,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
         }
       }
     }
+    if constexpr (CAREFUL) m *= c;
   };
   walk(std::false_type{});
   {
@@ -346,7 +357,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : DP == 64 ? 3 : 2) void pr
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) odd = __builtin_fmaf(acc[d][i], 0.0f, odd);
-    if (__syncthreads_or(odd != odd)) walk(std::true_type{});
+    if (__syncthreads_or(odd != odd || (m != -kInf && __builtin_fabsf(m) > kFar))) walk(std::true_type{});
   }
 
   l = half_sum(l);

@@ -12,6 +12,8 @@ namespace fq {
 // below one that stands out lost altogether (20000 of them 17.5 nats below: 5e-4 of the weights).
 template <int DT>
 constexpr float kUp = DT == kF16 ? 7.0f : 0.0f;
+// Scores up to this far from 0, in base-2 units, have their maximum taken off within the weights' exponent; its rounding is 2^-5 there.
+constexpr float kFar = 0x1p20f;
 constexpr float kInf = __builtin_inff();
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every resource
 
@@ -46,6 +48,12 @@ __device__ __forceinline__ void dma16(uint32_t lds, uint32_t voff, i32x4_t rs) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
 #pragma clang diagnostic pop
+
+// a b, rounded by itself (not within a fused sum)
+__device__ __forceinline__ float product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
 
 // This wave's loads landed and its LDS reads done, then the workgroup barrier.
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
