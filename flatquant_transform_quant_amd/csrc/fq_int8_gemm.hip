@@ -247,12 +247,16 @@ __global__ __launch_bounds__(64 * kRowWaves) void rows_kernel(Gemm g) {
 }
 
 // The smallest tile whose number the device still holds at once has the shortest walk (64 x 64: two a CU, the others one); more of
-// them than that read A and W too often.  us of 64 x 64, 128 x 128, 256 x 256, with eight waves:
+// them than that read A and W too often, where there is more than one band of rows.  us of 64 x 64, 128 x 128, 256 x 256, with eight waves:
 //   200 x 8192 x 8192   29.2  40.8  89.8      1024 x 8192 x 8192    119  72.7  96.2
 //   333 x 8200 x 4112   39.4  24.5  55.9      2048 x 4096 x 4096   60.7  39.3  53.3
 //   320 x 8192 x 4096   27.2  21.8            4096 x 4096 x 4096    122  88.3  62.6
 // and 128 x 256, where it fits: 1024 x 8192 x 8192 70.4, 2048 x 4096 x 4096 38.5.  Four waves a workgroup hide less of a stage's
 // waits: 100 x 1024 x 8192 19.3 (eight: 17.5), 128 x 4096 x 4096 11.6 (10.8), 512 x 8192 x 8192 53.6 (42.5).
+// One band of rows reads W once whatever its tiles are, and taller ones multiply zeros; us of 64 x 64, 128 x 128, 128 x 256, 256 x 256:
+//   48 x 131072 x 4096   107  126  126  137      100 x 131072 x 4096   152  137  135  145
+//   64 x 65536 x 8192    113  122  125  135      128 x 65536 x 8192    179  129  131  141
+//   64 x 32832 x 8192   71.4 91.2 68.9 90.8      65 x 65536 x 4096    76.6 69.5 67.8 70.8
 // Up to 32 rows without tiles: 20 x 8192 x 8192 20.2 us; 50 rows took 26.8 that way, in 64 x 64 tiles 18.6.
 template <int OUT>
 hipError_t go(const Gemm& g, hipStream_t s) {
@@ -265,11 +269,11 @@ hipError_t go(const Gemm& g, hipStream_t s) {
   if (g.T <= 32) {
     if (g.T <= 16) rows_kernel<1, 1, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 16)), 64 * kRowWaves, 0, s>>>(g);
     else rows_kernel<2, 2, OUT><<<static_cast<uint32_t>(ceil_div(g.O, 32)), 64 * kRowWaves, 0, s>>>(g);
-  } else if (tiles(64, 64) <= 512) {
+  } else if (g.T <= 64 || tiles(64, 64) <= 512) {
     run(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
   } else if (tiles(128, 128) <= 256) {
     run(std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 3>{});
-  } else if (tiles(128, 256) <= 256) {
+  } else if (g.T <= 128 || tiles(128, 256) <= 256) {
     run(std::integral_constant<int, 128>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
   } else {
     run(std::integral_constant<int, 256>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
