@@ -47,6 +47,10 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kAhead = 4;           // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
+// Workgroups a CU that there are registers for.  Heads of 64: 1024 single tokens of 8 heads on 2, int8, with a window of 1024, 154 us where there
+// are for two, 128 for three.
+template <int DP>
+constexpr int kGroups = DP == 256 ? 1 : DP == 64 ? 3 : 2;
 
 template <int MODE>
 constexpr int kCodeBits = MODE == kKvInt8 || MODE == kKvE4M3 ? 8 : 4;
@@ -368,6 +372,16 @@ __device__ __forceinline__ void pin_block(f32x16_t& a) {
   if constexpr (D == 7) asm("" : "={v[128:143]}"(a) : "0"(a));
 }
 
+// Means of two or more parts are joined by their weights' sums l, brought to one maximum: a part's share of them.  (A mean may hold the infinity of
+// an element that was seen: a share is never 0 but where nothing was.)
+__device__ __forceinline__ float part_weight(float l, float m, float to) { return m == -kInf ? 0.0f : l * rescale(m, to); }
+__device__ __forceinline__ float part_share(float w, float inv) {  // (inv: 1 over all; NaN stays)
+  const float s = w * inv;
+  return s < 0x1p-126f && w != 0.0f ? 0x1p-126f : s;
+}
+// (the part with the maximum has a weight of 1 at the least; all parts' are 0 where nothing was seen)
+__device__ __forceinline__ float over_all(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 // ---- the products of 32 keys with 32 query rows ------------------------------------------------------
 
 template <int MODE, int DT, int DP, bool PAD>
@@ -643,7 +657,7 @@ struct Block {
   // relative to m, without R, and m is in base-2 units.  Value scales were `down` of what they are.
   __device__ __forceinline__ void finish(float down) {
     l = half_sum(l);
-    float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float inv = over_all(l);
     constexpr bool kFirst = kUnitV<MODE> < 1.0f;  // (E2M1's sums are up to 2^13 above the values: that goes first)
     const float up = kLow ? kUnitV<MODE> / down : 1.0f;
     if (kFirst) inv *= up;
@@ -664,14 +678,6 @@ struct Block {
   }
 };
 
-// Means of two or more parts are joined by their weights' sums l, brought to one maximum: a part's share of them.  (A mean may hold the infinity of
-// an element that was seen: a share is never 0 but where nothing was.)
-__device__ __forceinline__ float part_weight(float l, float m, float to) { return m == -kInf ? 0.0f : l * rescale(m, to); }
-__device__ __forceinline__ float part_share(float w, float all) {
-  const float s = w == 0.0f ? 0.0f : w / all;  // (NaN stays)
-  return s < 0x1p-126f && w != 0.0f ? 0x1p-126f : s;
-}
-
 // A part for the join: its means [element][row] of TR rows, then m and l.
 template <int DP, int TR>
 constexpr int kPart = (DP + 2) * TR;
@@ -681,7 +687,7 @@ constexpr int kPart = (DP + 2) * TR;
 // RB blocks of 32 rows: 4, a wave each; or 2, where waves 2 and 3 have the same rows as 0 and 1 and the tile's other 32 keys, and
 // their sums are joined at the segment's end.
 template <int MODE, int DT, int DP, bool PAD, int RB>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel(ChunkArgs, float* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads, kGroups<DP>) void chunk_wide_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
   constexpr bool kLow = BK::kLow;
   using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 16>;  // (16 bits: not used)
@@ -833,7 +839,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
       const float w0 = part_weight(bk.l, bk.m, mn), w1 = part_weight(s_m[1][32 * wv + col], mo, mn);
       bk.m = mn;
       bk.l = w0 + w1;
-      const float f0 = part_share(w0, bk.l), f1 = part_share(w1, bk.l);
+      const float inv = over_all(bk.l), f0 = part_share(w0, inv), f1 = part_share(w1, inv);
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -872,7 +878,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_wide_kernel
 // waves' sums are joined.  Low-bit rows go through registers, the next 32 on their way during the products of these; 16-bit ones by
 // LDS-DMA, the next keys as soon as the scores are done with these, the next values behind the second products.
 template <int MODE, int DT, int DP, bool PAD>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kernel(ChunkArgs, float* __restrict__ ws) {
+__global__ __launch_bounds__(kThreads, kGroups<DP>) void chunk_narrow_kernel(ChunkArgs, float* __restrict__ ws) {
   using BK = Block<MODE, DT, DP, PAD>;
   constexpr bool kLow = BK::kLow;
   using RW = Rows<kLow ? MODE : kKvInt8, DP, PAD, 32>;  // (16 bits: not used)
@@ -1031,8 +1037,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
       f[w] = part_weight(s_l[w][col], s_m[w][col], m);
       l += f[w];
     }
+    const float inv = over_all(l);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) f[w] = part_share(f[w], l);
+    for (int w = 0; w < kWaves; ++w) f[w] = part_share(f[w], inv);
     // this lane's elements: DP / 8 from e0 on
     constexpr int NE = DP / 8;
     const int e0 = (2 * wv + hf) * NE;
@@ -1076,6 +1083,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void chunk_narrow_kern
 template <int MODE, int DT, int DP, int TR>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const float* __restrict__ ws) {
   constexpr int NE = TR / 8;
+  // parts whose loads are on their way together (tiles of 128 rows have 16 loads of a thread in each: document of 16384 rows with 1, 2 and 4
+  // parts 312.7, 314.3, 319.9 us, 5 chunks over int4 578, 581, 585; 16 x 3 drafts behind up to 8000 int8 tokens one after the other 51.2 us, by four 48.2)
+  constexpr int kAtOnce = TR == 128 ? 1 : 4;
   const int run = blockIdx.x;
   const Shared sh = shared_from(a, run);
   if (sh.parts == 0) return;
@@ -1088,10 +1098,10 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
   float m = -kInf, l = 0.0f, o[NE];
 #pragma unroll
   for (int j = 0; j < NE; ++j) o[j] = 0.0f;
-  for (int i = 0; i <= sh.parts; i += 4) {  // (four parts' loads at a time)
-    float mi[4], li[4], x[4][NE];
+  for (int i = 0; i <= sh.parts; i += kAtOnce) {
+    float mi[kAtOnce], li[kAtOnce], x[kAtOnce][NE];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kAtOnce; ++k) {
       const int part = min(i + k, sh.parts);
       const float* const p = ws + static_cast<int64_t>(part_at(run + part, part)) * kPart<DP, TR> + r;
       mi[k] = p[DP * TR];
@@ -1099,16 +1109,27 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const
 #pragma unroll
       for (int j = 0; j < NE; ++j) x[k][j] = p[(e + j) * TR];
     }
+    const int n = min(kAtOnce, sh.parts + 1 - i);
+    const float m0 = m, l0 = l;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (i + k > sh.parts) break;
-      const float mn = fmaxf(m, mi[k]);
-      const float w0 = part_weight(l, m, mn), w1 = part_weight(li[k], mi[k], mn);
-      m = mn;
-      l = w0 + w1;
-      const float f0 = part_share(w0, l), f1 = part_share(w1, l);
+    for (int k = 0; k < kAtOnce; ++k) m = fmaxf(m, mi[k]);
+    float w[kAtOnce];
+    l = part_weight(l0, m0, m);
+    const float before = l;
 #pragma unroll
-      for (int j = 0; j < NE; ++j) o[j] = __builtin_fmaf(o[j], f0, x[k][j] * f1);
+    for (int k = 0; k < kAtOnce; ++k) {
+      w[k] = k < n ? part_weight(li[k], mi[k], m) : 0.0f;
+      l += w[k];
+    }
+    const float inv = over_all(l), f0 = part_share(before, inv);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) o[j] *= f0;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (k >= n) break;
+      const float f = part_share(w[k], inv);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) o[j] = __builtin_fmaf(x[k][j], f, o[j]);
     }
   }
   const int64_t to = sg.s.q0 + token;
