@@ -807,7 +807,8 @@ def attn_chunk(q, cache: KVCache, block_table, cu_q, lengths, window: int = 0, s
     """Attention of new tokens over the cache, which holds their keys and values already: q [Tq, Hq, D], sequence b in rows
     cu_q[b] .. cu_q[b+1]-1 (int32 [B+1]), its last row at the last of its lengths[b] tokens (int32 [B]).  A row sees the keys up to its
     own position; with ``window`` only the last ``window`` of them and the first ``sinks`` tokens.  scale 0 means 1/sqrt(D).
-    ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least attn_chunk_workspace_size) may be passed to reuse one."""
+    ``lse``: float32 [Tq, Hq].  ``workspace`` (uint8, at least attn_chunk_workspace_size) may be passed to reuse one.  Long chunks and
+    single tokens can share a call, and take less time in calls of their own."""
     torch = _torch()
     window, sinks = _int32(window), _int32(sinks)
     _same_gpu(stream, cache.k, q, block_table, cu_q, lengths, out, lse, workspace)

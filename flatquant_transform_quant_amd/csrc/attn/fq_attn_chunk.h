@@ -4,13 +4,14 @@
 // among its lengths[b] tokens.  Row i sees the keys up to its own position, with a window only the last W of them and
 // the first S: o = sum_j p_j v_j, p = softmax over the visible keys of scale * <q, k_j>.
 //
-// A workgroup of four waves takes a row tile: the g query heads of one cache head for neighbouring tokens (a cached byte is
-// read once for all of them), 128, 64 or 32 rows, the smallest that the mean rows of a sequence and cache head fit.  With 128 a wave has
-// 32 rows; with 64 waves 2 and 3 have the rows of 0 and 1 and the other half of the keys; with 32 each wave has all rows and keys of its
-// own, in LDS of its own without barriers (24 sequences of 5 drafts, 40 rows, over int8, in tiles of 128 265 us, of 64 122; see kShort for
-// single tokens).  It walks the keys in tiles of 64 as the prompt kernel does: two LDS buffers, S^T = K Q^T and O^T = V^T P^T with
-// 32 x 32 x 16 products, a lane owning one row's statistics, the maximum moved only when a score passes m + 8 in base-2 units.  LDS
-// layouts as there.  A tile's keys lie in pages of 16 tokens at least: each wave brings the 16 rows that are one page's (16 bits by LDS-DMA).
+// A workgroup of four waves takes a row tile: the g query heads of one cache head for neighbouring tokens (a cached byte is read
+// once for all of them), 128, 64 or 32 rows, the smallest that the mean rows of a sequence and cache head fit.  With 128 a wave has
+// 32 rows; with 64 waves 2 and 3 have the rows of 0 and 1 and the other half of the keys; with 32 each wave has all rows and keys
+// of its own, in LDS of its own without barriers (24 sequences of 5 drafts, 40 rows, over int8, in tiles of 128 265 us, of 64 122;
+// see kShort for single tokens).  It walks the keys in tiles of 64 as the prompt kernel does: two LDS buffers, S^T = K Q^T and O^T
+// = V^T P^T with 32 x 32 x 16 products, a lane owning one row's statistics, the maximum moved only when a score passes m + 8 in
+// base-2 units.  LDS layouts as there.  A tile's keys lie in pages of 16 tokens at least: each wave brings the 16 rows that are one
+// page's (16 bits by LDS-DMA).
 //
 // Low-bit formats: the codes go through registers, are widened to f16 numbers there, exactly, and written to LDS;
 // a tile's bytes are widened once for all of its rows.  Widened: int8 and int4 the code times 2^-9, E4M3 the code, E2M1 the code
@@ -27,10 +28,10 @@
 // bisection.  A run that has a segment in part leaves its sums in the workspace, at most two such parts a run,
 // and a second launch joins them in order.  (Cuts moved to a segment's edge where that is near save few parts and cost as much: no gain.)
 //
-// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 309 us, 0.78 PFLOP/s, matrix cores 37% and
-// vector unit 42% busy, one after the other in a wave, two waves a SIMD; 5 chunks of 1024 over int4, 574 us, 0.63 PFLOP/s: widening and
-// softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 114 us, 2.9 TB/s: vector unit 43%, of which 24 of 64 rows are padding's;
-// 32 single tokens of 1028 keys in bf16, 35 us, 3.9 TB/s.
+// Bound, with 64 query heads on 8 or 32 on 8, D = 128: 16384 rows in f16 with a window of 4096, 305 to 324 us, up to 0.79 PFLOP/s,
+// matrix cores 37% and vector unit 42% busy, one after the other in a wave, two waves a SIMD; 5 chunks of 1024 over int4, 577 us,
+// 0.63 PFLOP/s: widening and softmax, vector unit 51%; 24 x 5 drafts over up to 16384 int8 tokens, 113 us, 2.9 TB/s: vector unit
+// 43%, of which 24 of 64 rows are padding's; 32 single tokens of 1028 keys in bf16, 36 us, 3.8 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -47,8 +48,8 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kAhead = 4;           // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
-// Workgroups a CU that there are registers for.  Heads of 64: 1024 single tokens of 8 heads on 2, int8, with a window of 1024, 154 us where there
-// are for two, 128 for three.
+// Workgroups a CU that there are registers for.  Heads of 64: 1024 single tokens of 8 heads on 2, int8, with a window of 1024, 154
+// us where there are for two, 128 for three.
 template <int DP>
 constexpr int kGroups = DP == 256 ? 1 : DP == 64 ? 3 : 2;
 
@@ -60,15 +61,15 @@ constexpr float kUnitK = MODE == kKvInt8 || MODE == kKvInt4 ? 512.0f : 1.0f;
 template <int MODE>
 constexpr float kUnitV = MODE == kKvFp4 ? 0x1p-13f : kUnitK<MODE>;
 // The reference R lies between these.  From kLeastRef on a walk's 2^31 weights sum below 2^127; up to kMostRef a weight of 1 is
-// well within fp32's normal numbers.  Above kFullRef those 2^-35 of the largest are not (exp2 gives 0 below 2^-126): the walk is done again with
-// value scales 2^-kDown of what they are, which are far below the largest where that is a subnormal number.
+// well within fp32's normal numbers.  Above kFullRef those 2^-35 of the largest are not (exp2 gives 0 below 2^-126): the walk is
+// done again with value scales 2^-kDown of what they are, which are far below the largest where that is a subnormal number.
 constexpr int kLeastRef = -82, kMostRef = 120, kFullRef = 96, kDown = 64;
-// Whether the weights of row tiles of 32 RB rows enter the second product in two parts, the rounded weight and what the rounding left, and
-// so with 16 bits (bf16) or 22.  Rounded once they add as much to an output's error as its own rounding where that has as many bits: 1.4 times the
-// error in all (single tokens over a bf16 cache 2.2e-3 of the output, so 1.6e-3).  us without and with: 32 single tokens of 1028 keys in
-// bf16 35.0, 35.8, like all tiles of 32, which wait for memory; 24 x 5 drafts over int8 in tiles of 64 113.8, 122.5, so not for
-// bf16 rows, whose output has 8 bits to these weights' 11; tiles of 128 keep one part, a document of 16384 rows in f16 314, 405, 5 chunks of
-// 1024 over int4 575, 656: matrix and vector unit are what bounds them.
+// Whether the weights of row tiles of 32 RB rows enter the second product in two parts, the rounded weight and what the rounding
+// left, and so with 16 bits (bf16) or 22.  Rounded once they add as much to an output's error as its own rounding where that has as
+// many bits: 1.4 times the error in all (single tokens over a bf16 cache 2.2e-3 of the output, so 1.6e-3).  us without and with: 32
+// single tokens of 1028 keys in bf16 35.0, 35.8, like all tiles of 32, which wait for memory; 24 x 5 drafts over int8 in tiles of
+// 64 113.8, 122.5, so not for bf16 rows, whose output has 8 bits to these weights' 11; tiles of 128 keep one part, a document of
+// 16384 rows in f16 314, 405, 5 chunks of 1024 over int4 575, 656: matrix and vector unit are what bounds them.
 template <int MODE, int DT, int RB>
 constexpr bool kRest = RB == 1 || (RB == 2 && (MODE == kKv16 || DT == kF16));
 // weights enter the second product 2^kUpW times above the row's reference
@@ -315,8 +316,8 @@ __device__ __forceinline__ int64_t row_at(const ChunkArgs& a, int hk, int k) {
 }
 
 // The same with the addresses of the 16 rows on both sides and their bytes, so that a tile's LDS-DMA needs no more than to pick a
-// lane's, and starts before the tile's products (formed a tile at a time from arguments read anew, under the first products: document of 16384
-// rows 317 us, so 309; the earlier start alone changes nothing).
+// lane's, and starts before the tile's products (formed a tile at a time from arguments read anew, under the first products:
+// document of 16384 rows 317 us, so 309; the earlier start alone changes nothing).
 struct PageRows : Pages {
   uint64_t at[2];
   int bytes;
@@ -336,17 +337,24 @@ struct PageRows : Pages {
   }
 };
 
-// a = acc[D] times f where `need` (the wave's) is not 0.  The compiler copies the 16-register blocks to other registers and back around such a
-// branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 315); so each block has a place
-// that the statements ask for, and the branch is inside: nothing is left to copy.  With it the wait states between the products that wrote the block and
-// this read (at most 18), and between this write and the products that read it.
+// a = acc[D] times f where `need` (the wave's) is not 0.  The compiler copies the 16-register blocks to other registers and back
+// around such a branch, for every tile, which waits for the products besides (document of 16384 rows 363 us, so 315); so each block
+// has a place that the statements ask for, and the branch is inside: nothing is left to copy.  With it the wait states between the
+// products that wrote the block and this read (at most 18), and between this write and the products that read it.
 template <int D>
 __device__ __forceinline__ void scale_block(f32x16_t& a, float f, int need) {
   need = __builtin_amdgcn_readfirstlane(need);
 #define FQ_SCALE(N, R0, R1, R2, R3, R4, R5, R6, R7, R8, R9, R10, R11, R12, R13, R14, R15) \
   if constexpr (D == N) \
     asm("s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 .Lfq_scaled%=\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\t" \
-        "v_mul_f32 v" #R0 ", %1, v" #R0 "\n\t" "v_mul_f32 v" #R1 ", %1, v" #R1 "\n\t" "v_mul_f32 v" #R2 ", %1, v" #R2 "\n\t" "v_mul_f32 v" #R3 ", %1, v" #R3 "\n\t" "v_mul_f32 v" #R4 ", %1, v" #R4 "\n\t" "v_mul_f32 v" #R5 ", %1, v" #R5 "\n\t" "v_mul_f32 v" #R6 ", %1, v" #R6 "\n\t" "v_mul_f32 v" #R7 ", %1, v" #R7 "\n\t" "v_mul_f32 v" #R8 ", %1, v" #R8 "\n\t" "v_mul_f32 v" #R9 ", %1, v" #R9 "\n\t" "v_mul_f32 v" #R10 ", %1, v" #R10 "\n\t" "v_mul_f32 v" #R11 ", %1, v" #R11 "\n\t" "v_mul_f32 v" #R12 ", %1, v" #R12 "\n\t" "v_mul_f32 v" #R13 ", %1, v" #R13 "\n\t" "v_mul_f32 v" #R14 ", %1, v" #R14 "\n\t" "v_mul_f32 v" #R15 ", %1, v" #R15 "\n\t" \
+        "v_mul_f32 v" #R0 ", %1, v" #R0 "\n\t" "v_mul_f32 v" #R1 ", %1, v" #R1 "\n\t" \
+        "v_mul_f32 v" #R2 ", %1, v" #R2 "\n\t" "v_mul_f32 v" #R3 ", %1, v" #R3 "\n\t" \
+        "v_mul_f32 v" #R4 ", %1, v" #R4 "\n\t" "v_mul_f32 v" #R5 ", %1, v" #R5 "\n\t" \
+        "v_mul_f32 v" #R6 ", %1, v" #R6 "\n\t" "v_mul_f32 v" #R7 ", %1, v" #R7 "\n\t" \
+        "v_mul_f32 v" #R8 ", %1, v" #R8 "\n\t" "v_mul_f32 v" #R9 ", %1, v" #R9 "\n\t" \
+        "v_mul_f32 v" #R10 ", %1, v" #R10 "\n\t" "v_mul_f32 v" #R11 ", %1, v" #R11 "\n\t" \
+        "v_mul_f32 v" #R12 ", %1, v" #R12 "\n\t" "v_mul_f32 v" #R13 ", %1, v" #R13 "\n\t" \
+        "v_mul_f32 v" #R14 ", %1, v" #R14 "\n\t" "v_mul_f32 v" #R15 ", %1, v" #R15 "\n\t" \
         "s_nop 3\n.Lfq_scaled%=:" : "={v[" #R0 ":" #R15 "]}"(a) : "v"(f), "s"(need), "0"(a) : "scc")
   FQ_SCALE(0, 16, 17, 18, 19, 20, 21, 22, 23, 24, 25, 26, 27, 28, 29, 30, 31);
   FQ_SCALE(1, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 42, 43, 44, 45, 46, 47);
@@ -372,8 +380,8 @@ __device__ __forceinline__ void pin_block(f32x16_t& a) {
   if constexpr (D == 7) asm("" : "={v[128:143]}"(a) : "0"(a));
 }
 
-// Means of two or more parts are joined by their weights' sums l, brought to one maximum: a part's share of them.  (A mean may hold the infinity of
-// an element that was seen: a share is never 0 but where nothing was.)
+// Means of two or more parts are joined by their weights' sums l, brought to one maximum: a part's share of them.  (A mean may hold
+// the infinity of an element that was seen: a share is never 0 but where nothing was.)
 __device__ __forceinline__ float part_weight(float l, float m, float to) { return m == -kInf ? 0.0f : l * rescale(m, to); }
 __device__ __forceinline__ float part_share(float w, float inv) {  // (inv: 1 over all; NaN stays)
   const float s = w * inv;
@@ -1083,8 +1091,9 @@ __global__ __launch_bounds__(kThreads, kGroups<DP>) void chunk_narrow_kernel(Chu
 template <int MODE, int DT, int DP, int TR>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a, const float* __restrict__ ws) {
   constexpr int NE = TR / 8;
-  // parts whose loads are on their way together (tiles of 128 rows have 16 loads of a thread in each: document of 16384 rows with 1, 2 and 4
-  // parts 312.7, 314.3, 319.9 us, 5 chunks over int4 578, 581, 585; 16 x 3 drafts behind up to 8000 int8 tokens one after the other 51.2 us, by four 48.2)
+  // parts whose loads are on their way together (tiles of 128 rows have 16 loads of a thread in each: document of 16384 rows with
+  // 1, 2 and 4 parts 312.7, 314.3, 319.9 us, 5 chunks over int4 578, 581, 585; 16 x 3 drafts behind up to 8000 int8 tokens one
+  // after the other 51.2 us, by four 48.2)
   constexpr int kAtOnce = TR == 128 ? 1 : 4;
   const int run = blockIdx.x;
   const Shared sh = shared_from(a, run);

@@ -8,11 +8,12 @@
 // fragments are read among the products of the one before (read in front of their own: 64 x 64 tiles 26 us where they then
 // took 19, 100 x 1024 x 8192).  Each XCD takes neighbouring tiles, in groups of four row bands.
 // Bound by the walk over the contraction while the device holds all tiles at once (100 x 1024 x 8192: 17.5 us, 270 ns a stage of barrier,
-// LDS reads and products); at 8192^3, 442 us (2.49 POP/s, half of the dense int8 peak, matrix cores 58% busy), by LDS: the reads and
+// LDS reads and products); at 8192^3, 443 us (2.48 POP/s, half of the dense int8 peak, matrix cores 58% busy), by LDS: the reads and
 // copies of a stage take as many cycles as its products.
-// Rows (up to 32, as in single steps): bound by reading W once, 4 x 10240 x 8192 (84 MB) 20.4 us, 4.1 TB/s.  A workgroup of eight waves has 16 or 32 channels; the waves
-// take 128 bytes of the contraction in turn, straight from memory into operand registers (both operands relabel the contraction the
-// same way: lane group kb has bytes 32 kb .. 32 kb + 31 of the 128), and their sums are added up in LDS.
+// Rows (up to 32, as in single steps): bound by reading W once, 4 x 10240 x 8192 (84 MB) 20.4 us, 4.1 TB/s.  A workgroup of eight
+// waves has 16 or 32 channels; the waves take 128 bytes of the contraction in turn, straight from memory into operand registers (both
+// operands relabel the contraction the same way: lane group kb has bytes 32 kb .. 32 kb + 31 of the 128), and their sums are added
+// up in LDS.
 #include <hip/hip_runtime.h>
 
 #include "attn/fq_attn_tile.h"

@@ -391,27 +391,30 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
                           const fq_tensor* lse, void* workspace, uint64_t workspaceSize, hipStream_t stream);
 
 /* ---- attention of new tokens over the cache ---------------------------------------------------
- * Sequences of a running batch with one or more new tokens each, whose keys and values the cache holds already: sequence b
- * has the query rows cu_q[b] .. cu_q[b+1]-1 of q, out [Tq, Hq, D] (INT32 [B+1], ascending from 0) and lengths[b] cached
- * tokens (INT32 [B], the new ones included; capped at the table's reach).  Its last query row stands at its last token, and
- * row i at position p = lengths[b] - (cu_q[b+1] - cu_q[b]) + i sees the keys j <= p; with window > 0 of those only j > p - window and
- * j < sinks (the first tokens, which stay visible).  window 0: all of them (sinks is not used then).  So chunks of prompts, drafted
- * tokens that are checked and single tokens share one call.
+ * Sequences of a running batch with one or more new tokens each, whose keys and values the cache holds already: sequence b has
+ * the query rows cu_q[b] .. cu_q[b+1]-1 of q, out [Tq, Hq, D] (INT32 [B+1], ascending from 0) and lengths[b] cached tokens
+ * (INT32 [B], the new ones included; capped at the table's reach).  Its last query row stands at its last token, and row i at
+ * position p = lengths[b] - (cu_q[b+1] - cu_q[b]) + i sees the keys j <= p; with window > 0 of those only the ones with
+ * j > p - window and the first ones, j < sinks, which stay visible.  window 0: all of them (sinks is not used then).  So chunks of prompts,
+ * drafted tokens that are checked and single tokens can share one call; the work is cut by the mean rows of a sequence, so
+ * that long chunks and single tokens take less time in calls of their own, and each workgroup looks at all B sequences: more
+ * than about 1000 are better dealt to several calls.
  * q, out, the cache, block_table, scale, lse FLOAT32 [Tq, Hq] and the workspace as for fq_attn_decode (of the size that
- * fq_attn_chunk_get_workspace_size gives for the same q, cache, table, cu_q, window and sinks; its contents need not be initialised; calls
- * that overlap in time must not share it); 1 <= B <= 65536, Hq <= 65536; reach and Tq below 2^31 - 65536, and
- * (floor(Tq / t) + min(B, Tq)) * Hkv * n * (ceilDiv(seen, 64) + 5) < 2^31, with row tiles of r rows (the first of 32, 64 and 128 that
- * ceilDiv(Tq, B) * g rows fit, else 128), n = ceilDiv(g, r) of them for a token's heads, t = floor(r / ceilDiv(g, n)) tokens of one, and
- * `seen` the keys that such a tile can see (reach + t, or window + t + 126 and the sinks).
- * A row that sees nothing (more rows than cached tokens, no page) gives zeros and lse = -infinity.  A token whose
- * table entry is outside the cache is left out.  What a row does not see never reaches it, infinities and NaN included; rows of out past
+ * fq_attn_chunk_get_workspace_size gives for the same q, cache, table, cu_q, window and sinks; its contents need not be
+ * initialised; calls that overlap in time must not share it); 1 <= B <= 65536, Hq <= 65536; reach and Tq below 2^31 - 65536,
+ * and (floor(Tq / t) + min(B, Tq)) * Hkv * n * (ceilDiv(seen, 64) + 5) < 2^31, with row tiles of r rows (the first of 32, 64
+ * and 128 that ceilDiv(Tq, B) * g rows fit, else 128), n = ceilDiv(g, r) of them for a token's heads, t = floor(r / ceilDiv(g,
+ * n)) tokens of one, and `seen` the keys that such a tile can see (reach + t, or window + t + 126 and the sinks).
+ * A row that sees nothing (more rows than cached tokens, no page) gives zeros and lse = -infinity.  A token whose table entry
+ * is outside the cache is left out.  What a row does not see never reaches it, infinities and NaN included; rows of out past
  * cu_q[B] are not written.  The same inputs give the same bits.
- * Scores, statistics and sums are fp32, codes enter the products exactly (E2M1 groups more than 2^26 below the largest of their
- * row lose bits, and a bf16 query's elements more than 2^28 below the largest of its row).  The weights are rounded for
- * the second product: to 11 bits and 2^-32 of the row's largest at the least over an f16 cache, 8 bits over a bf16 one; over the low-bit
- * formats a weight, off by up to 2^-17 of itself where value scales are far from 1, times its value's scale to 11 bits, and to 2^-30 of the largest of these.
- * Twice as many bits (as fq_attn_decode's) where r is 32, so for single tokens and few drafts, and, over 16-bit caches or with f16 rows, where r is 64.  Value scales below 2^-80 lose bits (E2M1:
- * values below 2^-80), and below 2^-16 where some of 128 neighbouring rows of a cache head see ones above 2^96. */
+ * Scores, statistics and sums are fp32, codes enter the products exactly (E2M1 groups more than 2^26 below the largest of
+ * their row lose bits, and a bf16 query's elements more than 2^28 below the largest of its row).  The weights are rounded for
+ * the second product: to 11 bits and 2^-32 of the row's largest at the least over an f16 cache, 8 bits over a bf16 one; over
+ * the low-bit formats a weight, off by up to 2^-17 of itself where value scales are far from 1, times its value's scale to 11
+ * bits, and to 2^-30 of the largest of these.  Twice as many bits (as fq_attn_decode's) where r is 32, so for single tokens and
+ * few drafts, and, over 16-bit caches or with f16 rows, where r is 64.  Value scales below 2^-80 lose bits (E2M1: values below
+ * 2^-80), and below 2^-16 where some of 128 neighbouring rows of a cache head see ones above 2^96. */
 fq_status fq_attn_chunk_get_workspace_size(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* block_table, const fq_tensor* cu_q,
                                            int32_t window, int32_t sinks, uint64_t* workspaceSize);
 fq_status fq_attn_chunk(const fq_tensor* q, const fq_tensor* k_cache, const fq_tensor* k_scale, const fq_tensor* v_cache,
