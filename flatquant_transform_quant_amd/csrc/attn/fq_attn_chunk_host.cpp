@@ -93,6 +93,8 @@ fq_status fq_attn_chunk(const fq_tensor* q, const fq_tensor* k_cache, const fq_t
       !out_rows_ok(*out, Tq, Hq, D, q->dtype, &a.out) || !lse_ok(lse, Tq, Hq) || (a.c.mode == kKv16 && a.c.dtype != row_dtype(q->dtype)))
     return FQ_ERR_PARAM_INVALID;
   a.c.dtype = row_dtype(q->dtype);
+  // (integer codes are operands of 2^-9 of theirs, and f16 rows go in as they are, so that the scores' factor is 2^9 times the scale)
+  if ((a.c.mode == kKvInt8 || a.c.mode == kKvInt4) && a.c.dtype == kF16 && std::fabs(a.scale) > 0x1p118f) return FQ_ERR_PARAM_INVALID;
   const uint64_t need = chunk_workspace(a, D);
   if (need > 0 && !workspace) return FQ_ERR_PARAM_NULLPTR;
   if (workspaceSize < need || (need > 0 && !aligned(workspace, 16))) return FQ_ERR_PARAM_INVALID;

@@ -399,7 +399,8 @@ fq_status fq_attn_prefill(const fq_tensor* q, const fq_tensor* k, const fq_tenso
  * drafted tokens that are checked and single tokens can share one call; the work is cut by the mean rows of a sequence, so
  * that long chunks and single tokens take less time in calls of their own, and each workgroup looks at all B sequences: more
  * than about 1000 are better dealt to several calls.
- * q, out, the cache, block_table, scale, lse FLOAT32 [Tq, Hq] and the workspace as for fq_attn_decode (of the size that
+ * q, out, the cache, block_table, scale (within 2^118 where f16 rows meet an int8 or int4 cache), lse FLOAT32 [Tq, Hq] and the
+ * workspace as for fq_attn_decode (of the size that
  * fq_attn_chunk_get_workspace_size gives for the same q, cache, table, cu_q, window and sinks; its contents need not be
  * initialised; calls that overlap in time must not share it); 1 <= B <= 65536, Hq <= 65536; reach and Tq below 2^31 - 65536,
  * and (floor(Tq / t) + min(B, Tq)) * Hkv * n * (ceilDiv(seen, 64) + 5) < 2^31, with row tiles of r rows (the first of 32, 64
